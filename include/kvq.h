@@ -315,6 +315,100 @@ kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const kvq_cache* 
                                         int32_t num_q_heads, float softmax_scale, int32_t max_seq_len,
                                         int32_t num_splits, void* out, kvq_dtype out_dtype, void* stream);
 
+/* ---- Drafted tokens, page mass and eviction.  The pages name speculative
+ * decoding and attention-guided page tiers without defining either; these
+ * three calls are this library's own: verify a tree of drafted tokens against
+ * the cache, accumulate where attention went, and drop the pages it left. */
+
+/* Most nodes of a tree (one bit each in a 64-bit ancestor word). */
+#define KVQ_TREE_MAX_NODES 64
+
+/* Workspace bytes kvq_tree_attention needs for (num_q_heads, num_nodes,
+ * max_seq_len, num_splits); num_splits = 0 asks for the library's choice. */
+kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t max_seq_len,
+                                    int32_t num_splits, size_t* bytes);
+
+/* Attention of up to num_nodes query tokens per sequence over the quantized
+ * cache and over each other: the verify step of speculative decoding with a
+ * tree (or a chain) of drafted tokens whose K and V are not in the cache yet.
+ * Query head h of node t of sequence b attends to the cached tokens
+ * j < seq_lens[b] and to the nodes j that t's ancestor word names:
+ *   a_j = softmax_scale * q . k_j,   out = sum_j e^a_j v_j / sum_j e^a_j.
+ *   q          device bf16 [num_seqs][num_nodes][num_q_heads][D], as for
+ *              kvq_decode_attention; num_nodes in 1..KVQ_TREE_MAX_NODES.
+ *   k_tree, v_tree  device bf16 [num_seqs][num_nodes][Hkv][D]: the drafted
+ *              tokens' K and V, or both NULL: the queries attend to the cache
+ *              alone (num_nodes = 1 is then kvq_decode_attention).
+ *   tree_mask  device uint64 [num_nodes] (mask_per_seq = 0: every sequence's
+ *              tree) or [num_seqs][num_nodes] (mask_per_seq = 1): bit j of word
+ *              t set where node t attends to node j (itself included, if it
+ *              shall).  Bits at and past the sequence's node count are ignored.
+ *              NULL: a chain, node t attends to nodes 0..t.
+ *   nodes_per_seq  device int32 [num_seqs] or NULL: sequence b has its first
+ *              nodes_per_seq[b] nodes (clamped to 0..num_nodes); the rows of
+ *              the others are written as empty rows.
+ *   out        device [num_seqs][num_nodes][num_q_heads][D] in out_dtype (bf16
+ *              or f32).  A row that attends to nothing is 0.
+ *   lse        NULL, or device fp32 [num_seqs][num_nodes][num_q_heads]:
+ *              ln sum_j e^a_j, -inf for an empty row.
+ *   page_lse   NULL, or device fp32 [num_seqs][num_nodes][num_q_heads][P],
+ *              P = ceil(min(max_seq_len, 16 pages_per_seq_max) / 16):
+ *              ln sum e^a_j over the tokens of logical page p, -inf for a page
+ *              (or a row) without tokens.  kvq_page_mass reads it.
+ *   max_seq_len, num_splits  as for kvq_decode_attention.
+ *   workspace  device, >= kvq_tree_workspace_bytes(), 16-byte aligned; needs no
+ *              initialisation.  Calls that may overlap on the GPU (two streams,
+ *              two graphs) need one each.
+ * q, k_tree and v_tree must be 16-byte aligned.  What a row does not attend to
+ * (masked nodes, nodes past the count, stale bytes of a page's unwritten
+ * tokens) never reaches it, whatever it holds; K and V that a row does attend
+ * to are taken as they are.  A bad page-table entry sets KVQ_STATUS_BAD_PAGE
+ * and its page (group, for KVQ_FMT_CB2_GROUP4) is left out.  Two launches. */
+kvq_status kvq_tree_attention(const kvq_config* cfg, const kvq_cache* cache, const void* q, int32_t num_q_heads,
+                              int32_t num_nodes, const void* k_tree, const void* v_tree, const uint64_t* tree_mask,
+                              int32_t mask_per_seq, const int32_t* nodes_per_seq, float softmax_scale,
+                              int32_t max_seq_len, int32_t num_splits, void* out, kvq_dtype out_dtype, float* lse,
+                              float* page_lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention mass of the logical pages, from what kvq_tree_attention wrote:
+ *   mass_out[b][p] = decay * mass_in[b][p]
+ *                    + sum over marked nodes t and heads h of
+ *                      e^(page_lse[b][t][h][p] - lse[b][t][h])
+ * so that each query head of a marked node adds up to 1 over the cache and its
+ * tree.  mass_in, mass_out: device fp32 [num_seqs][pages_per_seq_max] (may be
+ * the same array).
+ *   num_pages  the P of page_lse (0..pages_per_seq_max); pages past it only
+ *              decay.
+ *   node_mask  device uint64 [num_seqs] (bit t: node t counts; e.g. the nodes a
+ *              verify step accepted) or NULL: every node.
+ * Empty rows (lse = -inf) add nothing.  The sums run in a fixed order. */
+kvq_status kvq_page_mass(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t num_pages,
+                         const float* lse, const float* page_lse, const uint64_t* node_mask, float decay,
+                         const float* mass_in, float* mass_out, void* stream);
+
+/* Eviction of whole pages by their mass.  A sequence with more than keep_pages
+ * full pages keeps its first sink_pages and last recent_pages full pages and,
+ * of the others, those with the largest mass (ties to the lower page; NaN
+ * counts as the smallest) up to keep_pages in all; its partial last page always
+ * stays.  For KVQ_FMT_CB2_GROUP4 the unit is a group of 4 pages (their mass
+ * added up) and the three counts must be multiples of 4.
+ * Only the page table, lengths and masses change, no block is read or moved:
+ *   page_table_out[b] = kept pages in order, the partial page, the row's unused
+ *              entries, then the evicted pages in order -- a permutation of
+ *              page_table[b], so that later appends run into the evicted blocks
+ *              (or the caller takes the last evicted[b] entries back).
+ *   seq_lens_out[b] = seq_lens[b] - 16 * evicted[b].
+ *   mass_out[b] = the masses of the pages that stay, at their new places, then 0.
+ *   evicted    NULL, or device int32 [num_seqs]: pages evicted.
+ * cache->page_table, cache->seq_lens and mass are read; the outputs may be the
+ * same arrays (in place) or other ones, but may not overlap in part.  Keys were
+ * rotated (if at all) before they were cached, so kept tokens keep their
+ * positions.  Requires keep_pages >= sink_pages + recent_pages >= 0, and at
+ * most 28,672 pages per sequence (KVQ_ERR_UNSUPPORTED beyond). */
+kvq_status kvq_evict_pages(const kvq_config* cfg, const kvq_cache* cache, const float* mass, int32_t keep_pages,
+                           int32_t sink_pages, int32_t recent_pages, int32_t* page_table_out, int32_t* seq_lens_out,
+                           float* mass_out, int32_t* evicted, void* stream);
+
 /* The static channel mask of KVQ_FMT_CB2_STATIC ([P4] "Key Production
  * Engineering Takeaways" item 2: the top 1% channels by absolute magnitude stay
  * in FP16): for each (kv head, K|V), the cfg->static_channels channels with the

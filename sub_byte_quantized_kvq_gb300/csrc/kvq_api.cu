@@ -2,7 +2,9 @@
 // the split heuristic, and the debug dequantization kernel.
 #include <cmath>
 
+#include "kvq_block.cuh"
 #include "kvq_project.cuh"
+#include "kvq_tree.cuh"
 
 namespace kvq {
 // The CUDA runtime's error behind the last KVQ_ERR_CUDA this thread saw.
@@ -14,22 +16,8 @@ kvq_status cuda_status(cudaError_t e) {
 }
 
 // ----------------------------------------------------------------------------- debug dequantization
-// One thread per (token, channel) of the requested range; values are exactly
-// the ones the codes stand for (INT4: fmaf(q, S, m); E2M1: e2m1 * scale;
-// CB2: fp16 centroid or e4m3 outlier; FP8: e4m3 * scale in fp32; staging tail: as stored).
-__device__ __forceinline__ float dq_e4m3(uint32_t b) {
-  uint32_t d;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(d) : "r"(b & 0xFFu));
-  return __half2float(__ushort_as_half((unsigned short)(d & 0xFFFFu)));
-}
-__device__ __forceinline__ float dq_e2m1(uint32_t nib) {
-  const float mag[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
-  return (nib & 8u) ? -mag[nib & 7u] : mag[nib & 7u];
-}
-__device__ __forceinline__ float dq_f16(uint32_t bits) {
-  return __half2float(__ushort_as_half((unsigned short)(bits & 0xFFFFu)));
-}
-
+// One thread per (token, channel) of the requested range: block_value, or the
+// staged value as stored.
 struct DequantArgs {
   const uint8_t* pool;
   const uint8_t* tier_pool;
@@ -41,19 +29,8 @@ struct DequantArgs {
   int Hkv, D, ppsm, num_pages, num_tier_pages, fmt, seq, head, role, t0, t1;
 };
 
-// The value an outlier side-list (CB2, ASYM3) gives (t, c), else v.
-__device__ __forceinline__ float side_list_value(const uint8_t* hdr, int D, int t, int c, float v) {
-  const int n_ch = min((int)hdr[0], D);  // a corrupt side-list never reads past its block
-  for (int i = 0; i < n_ch; ++i) {
-    const uint8_t* rec = hdr + 4 + 20 * i;
-    const uint32_t tm = rec[2] | (rec[3] << 8);
-    if (rec[0] == c && (tm >> t & 1u)) v = dq_e4m3(rec[4 + t]);
-  }
-  return v;
-}
-
 __global__ void dequantize_kernel(const DequantArgs a) {
-  const int D = a.D, NS = D / 16;
+  const int D = a.D;
   const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (idx >= (long long)(a.t1 - a.t0) * D) return;
   const int pos = a.t0 + (int)(idx / D), c = (int)(idx % D);
@@ -81,12 +58,7 @@ __global__ void dequantize_kernel(const DequantArgs a) {
     const size_t stride = (size_t)block_stride(kBlkCb2g, D);
     const uint8_t* blk = a.pool + (((size_t)u * a.Hkv + a.head) * 2 + a.role) * stride;
     const uint8_t* cbk = a.pool + (((size_t)u0 * a.Hkv + a.head) * 2 + a.role) * stride;
-    const FragPos p = frag_pos(a.role, t, c);
-    const uint8_t* cw = blk + cb2g_code_off(D) + 2 * NS * p.lane + 2 * p.step;
-    const uint32_t q = ((cw[0] | (cw[1] << 8)) >> (4 * (p.slot & 3) + 2 * (p.slot >> 2))) & 3u;
-    const uint8_t* cb = cbk + 8 * cb2_slot(a.role, c);
-    v = dq_f16(cb[q] | (cb[4 + q] << 8));
-    v = side_list_value(blk + cb2_out_off(D), D, t, c, v);
+    v = block_value(kBlkCb2g, blk, cbk, a.role, D, t, c);
   } else {
     const uint32_t u = (uint32_t)a.page_table[(size_t)a.seq * a.ppsm + pg], phys = u & 0x7FFFFFFFu;
     const bool tier = (u >> 31) != 0;
@@ -99,55 +71,7 @@ __global__ void dequantize_kernel(const DequantArgs a) {
     const int bf = tier ? kBlkFp8 : (a.fmt == KVQ_FMT_TIERED ? kBlkCb2 : a.fmt);
     const size_t stride = (size_t)block_stride(bf, D);
     const uint8_t* blk = (tier ? a.tier_pool : a.pool) + (((size_t)phys * a.Hkv + a.head) * 2 + a.role) * stride;
-    const FragPos p = frag_pos(a.role, t, c);
-    if (bf == kBlkInt4) {
-      const uint32_t q = (blk[4 * NS * p.lane + 4 * p.step + p.slot / 2] >> (4 * (p.slot & 1))) & 0xFu;
-      const uint8_t* sz = blk + int4_sz_off(D) + 4 * (t * (D / 32) + c / 32);
-      v = fmaf((float)q, dq_f16(sz[0] | (sz[1] << 8)), dq_f16(sz[2] | (sz[3] << 8)));
-      const int cap = int4_cap(D), cnt = blk[int4_cnt_off(D) + t];
-      for (int i = 0; i < cnt && i < cap; ++i)
-        if (blk[int4_ch_off(D) + t * cap + i] == c) {
-          const uint8_t* vp = blk + int4_val_off(D) + 2 * (t * cap + i);
-          v = dq_f16(vp[0] | (vp[1] << 8));
-        }
-    } else if (bf == kBlkE2m1) {
-      const uint32_t q = (blk[4 * NS * p.lane + 4 * p.step + p.slot / 2] >> (4 * (p.slot & 1))) & 0xFu;
-      v = dq_e2m1(q) * dq_e4m3(blk[e2m1_sc_off(D) + 16 * (c / 16) + t]);
-    } else if (bf == kBlkCb2 || bf == kBlkCb2s) {
-      const uint32_t w = blk[2 * NS * p.lane + 2 * p.step] | (blk[2 * NS * p.lane + 2 * p.step + 1] << 8);
-      const uint32_t q = (w >> (4 * (p.slot & 3) + 2 * (p.slot >> 2))) & 3u;
-      const uint8_t* cb = blk + cb2_cb_off(D) + 8 * cb2_slot(a.role, c);
-      v = dq_f16(cb[q] | (cb[4 + q] << 8));
-      if (bf == kBlkCb2s) {   // static fp16 channels
-        const uint8_t* hdr = blk + cb2s_hdr_off(D);
-        const int n_s = min((int)hdr[0], kMaxStatic);
-        for (int i = 0; i < n_s; ++i)
-          if (hdr[1 + i] == c) {
-            const uint8_t* vp = blk + cb2s_val_off(D) + 32 * i + 2 * t;
-            v = dq_f16(vp[0] | (vp[1] << 8));
-          }
-      } else {
-        v = side_list_value(blk + cb2_out_off(D), D, t, c, v);
-      }
-    } else if (bf == kBlkA3) {
-      uint32_t vx, vy;
-      memcpy(&vx, blk + 4 * (p.lane * (NS / 2) + p.step / 2), 4);
-      memcpy(&vy, blk + a3_hi_off(D) + 4 * (p.lane * (NS / 4) + p.step / 4), 4);
-      const int bx = 8 * (p.step % 2) + 16 * (p.slot % 2) + 2 * (p.slot / 2);
-      const int by = 4 * (p.step % 4) + 16 * (p.slot % 2) + p.slot / 2;
-      const uint32_t q = ((vx >> bx) & 3u) | (((vy >> by) & 1u) << 2);
-      const int r = a3_rho(a.role, c);
-      const uint8_t* sp = blk + a3_s_off(D) + 2 * r;
-      const uint8_t* mp = blk + a3_m_off(D) + 2 * r;
-      // fp16(q * S + m): one rounding of the exact value (fp16 fused multiply-add)
-      v = __half2float(__hfma(__float2half_rn((float)q), __ushort_as_half((unsigned short)(sp[0] | (sp[1] << 8))),
-                              __ushort_as_half((unsigned short)(mp[0] | (mp[1] << 8)))));
-      v = side_list_value(blk + a3_out_off(D), D, t, c, v);
-    } else {
-      float s;
-      memcpy(&s, blk + fp8_sc_off(D), 4);
-      v = __fmul_rn(dq_e4m3(blk[8 * NS * p.lane + 8 * p.step + p.slot]), s);
-    }
+    v = block_value(bf, blk, blk, a.role, D, t, c);
   }
   a.out[idx] = v;
 }
@@ -508,6 +432,133 @@ kvq_status kvq_dequantize(const kvq_config* cfg, const kvq_cache* cache, int32_t
   if (!dim_supported(cfg)) return KVQ_ERR_UNSUPPORTED;
   return cuda_status(dequantize_launch(*cfg, *cache, seq, kv_head, which, tok_begin, tok_end, out,
                                        static_cast<cudaStream_t>(stream)));
+}
+
+// ----------------------------------------------------------------------------- drafted tokens, page mass, eviction
+static kvq_status tree_shape_ok(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t max_seq_len,
+                                int32_t num_splits) {
+  if (!cfg_ok(cfg) || num_q_heads <= 0 || num_q_heads % cfg->num_kv_heads || max_seq_len < 0 || num_splits < 0 ||
+      num_nodes < 1)
+    return KVQ_ERR_INVALID_ARG;
+  if (!dim_supported(cfg) || num_q_heads / cfg->num_kv_heads > 16 || num_nodes > KVQ_TREE_MAX_NODES)
+    return KVQ_ERR_UNSUPPORTED;
+  if (num_splits > kMaxSplits) return KVQ_ERR_CAPACITY;
+  return KVQ_OK;
+}
+static int visible_bound(const kvq_config* cfg, int32_t max_seq_len) {
+  const long long cap = (long long)cfg->pages_per_seq_max * kPage;
+  return max_seq_len < cap ? max_seq_len : (int)cap;
+}
+static int tree_splits(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t max_seq_len,
+                       int32_t num_splits) {
+  if (num_splits) return num_splits;
+  const int sms = num_sms();
+  return tree_auto_splits(cfg->format, cfg->head_dim, cfg->num_seqs, cfg->num_kv_heads,
+                          num_q_heads / cfg->num_kv_heads * num_nodes, visible_bound(cfg, max_seq_len), sms > 0 ? sms : 1);
+}
+static size_t tree_rows(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int S) {
+  return (size_t)cfg->num_seqs * num_q_heads * num_nodes * S;
+}
+
+kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t max_seq_len,
+                                    int32_t num_splits, size_t* bytes) {
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  const kvq_status st = tree_shape_ok(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
+  if (st != KVQ_OK) return st;
+  const int S = tree_splits(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
+  *bytes = tree_rows(cfg, num_q_heads, num_nodes, S) * (cfg->head_dim * sizeof(float) + sizeof(float2));
+  return KVQ_OK;
+}
+
+kvq_status kvq_tree_attention(const kvq_config* cfg, const kvq_cache* cache, const void* q, int32_t num_q_heads,
+                              int32_t num_nodes, const void* k_tree, const void* v_tree, const uint64_t* tree_mask,
+                              int32_t mask_per_seq, const int32_t* nodes_per_seq, float softmax_scale,
+                              int32_t max_seq_len, int32_t num_splits, void* out, kvq_dtype out_dtype, float* lse,
+                              float* page_lse, void* workspace, size_t workspace_bytes, void* stream) {
+  kvq_status st = tree_shape_ok(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
+  if (st != KVQ_OK) return st;
+  if (!cache_ok(cfg, cache) || !q || !out || !workspace || (out_dtype != KVQ_BF16 && out_dtype != KVQ_F32))
+    return KVQ_ERR_INVALID_ARG;
+  if (!k_tree != !v_tree || (!k_tree && tree_mask) || (mask_per_seq != 0 && mask_per_seq != 1)) return KVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  const int S = tree_splits(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
+  const size_t rows = tree_rows(cfg, num_q_heads, num_nodes, S);
+  if (workspace_bytes < rows * (cfg->head_dim * sizeof(float) + sizeof(float2))) return KVQ_ERR_WORKSPACE;
+  TreeArgs a;
+  a.pool = static_cast<const uint8_t*>(cache->pool);
+  a.tier_pool = static_cast<const uint8_t*>(cache->tier_pool);
+  a.page_table = cache->page_table;
+  a.seq_lens = cache->seq_lens;
+  a.staging = cache->staging;
+  a.status = cache->status;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv[0] = static_cast<const __nv_bfloat16*>(k_tree);
+  a.kv[1] = static_cast<const __nv_bfloat16*>(v_tree);
+  a.mask = tree_mask;
+  a.mask_stride = mask_per_seq ? num_nodes : 0;
+  a.nodes = nodes_per_seq;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * cfg->head_dim);
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.lse = lse;
+  a.page_lse = page_lse;
+  a.B = cfg->num_seqs;
+  a.Hkv = cfg->num_kv_heads;
+  a.Hq = num_q_heads;
+  a.G = num_q_heads / cfg->num_kv_heads;
+  a.T = num_nodes;
+  a.R = a.T * a.G;
+  a.max_seq_len = visible_bound(cfg, max_seq_len);
+  a.P = (a.max_seq_len + kPage - 1) / kPage;
+  a.fmt = cfg->format;
+  a.ppsm = cfg->pages_per_seq_max;
+  a.num_pages = cfg->num_pages;
+  a.num_tier_pages = cfg->num_tier_pages;
+  a.n_static = cfg->format == KVQ_FMT_CB2_STATIC ? cfg->static_channels : 0;
+  a.S = S;
+  a.pps = a.P > 0 ? (a.P + S - 1) / S : 1;
+  if (cfg->format == KVQ_FMT_CB2_GROUP4) a.pps = (a.pps + kGroupPages - 1) / kGroupPages * kGroupPages;   // whole groups
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  return cuda_status(tree_launch(a, cfg->head_dim, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_page_mass(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t num_pages,
+                         const float* lse, const float* page_lse, const uint64_t* node_mask, float decay,
+                         const float* mass_in, float* mass_out, void* stream) {
+  if (!cfg_ok(cfg) || num_q_heads <= 0 || num_q_heads % cfg->num_kv_heads || num_nodes < 1) return KVQ_ERR_INVALID_ARG;
+  if (num_nodes > KVQ_TREE_MAX_NODES) return KVQ_ERR_UNSUPPORTED;
+  if (!lse || (!page_lse && num_pages > 0) || !mass_in || !mass_out || !std::isfinite(decay) || num_pages < 0 ||
+      num_pages > cfg->pages_per_seq_max)
+    return KVQ_ERR_INVALID_ARG;
+  return cuda_status(page_mass_launch(lse, page_lse, node_mask, decay, mass_in, mass_out, cfg->num_seqs, num_nodes,
+                                      num_q_heads, num_pages, cfg->pages_per_seq_max, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_evict_pages(const kvq_config* cfg, const kvq_cache* cache, const float* mass, int32_t keep_pages,
+                           int32_t sink_pages, int32_t recent_pages, int32_t* page_table_out, int32_t* seq_lens_out,
+                           float* mass_out, int32_t* evicted, void* stream) {
+  if (!cfg_ok(cfg) || !cache_ok(cfg, cache) || !mass || !page_table_out || !seq_lens_out || !mass_out)
+    return KVQ_ERR_INVALID_ARG;
+  if (sink_pages < 0 || recent_pages < 0 || (long long)sink_pages + recent_pages > keep_pages) return KVQ_ERR_INVALID_ARG;
+  EvictArgs a;
+  a.unit = cfg->format == KVQ_FMT_CB2_GROUP4 ? kGroupPages : 1;
+  if (keep_pages % a.unit || sink_pages % a.unit || recent_pages % a.unit) return KVQ_ERR_INVALID_ARG;
+  if (cfg->pages_per_seq_max > kEvictMaxPages) return KVQ_ERR_UNSUPPORTED;
+  a.table_in = cache->page_table;
+  a.lens_in = cache->seq_lens;
+  a.mass_in = mass;
+  a.table_out = page_table_out;
+  a.lens_out = seq_lens_out;
+  a.mass_out = mass_out;
+  a.evicted = evicted;
+  a.B = cfg->num_seqs;
+  a.ppsm = cfg->pages_per_seq_max;
+  a.keep = keep_pages / a.unit;
+  a.sink = sink_pages / a.unit;
+  a.recent = recent_pages / a.unit;
+  return cuda_status(evict_launch(a, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t kvq_last_cuda_error(void) { return g_last_cuda_error; }

@@ -1,0 +1,59 @@
+// kvq_tree.cuh -- argument blocks and launches of tree attention, page mass and
+// page eviction (not part of the public ABI).
+#pragma once
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+// Rows of a (sequence, kv head): r = t * G + g, node t's query of the group's
+// head g; R = T * G of them.
+struct TreeArgs {
+  const uint8_t* pool;
+  const uint8_t* tier_pool;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const float* staging;
+  uint32_t* status;
+  const __nv_bfloat16* q;        // [B][T][Hq][D]
+  const __nv_bfloat16* kv[2];    // [B][T][Hkv][D], or null: no tree
+  const uint64_t* mask;          // [B or 1][T] ancestor words, or null: a chain
+  int mask_stride;               // T, or 0 when every sequence has the same tree
+  const int32_t* nodes;          // [B] live nodes, or null: T
+  float* part_o;                 // [B][Hkv][S][R][D]
+  float2* part_ml;               // [B][Hkv][S][R] (m in log2 units, l)
+  void* out;                     // [B][T][Hq][D] in out_dtype
+  int out_dtype;
+  float* lse;                    // [B][T][Hq], or null
+  float* page_lse;               // [B][T][Hq][P], or null
+  int B, Hkv, Hq, G, T, R, P;
+  int fmt, ppsm, num_pages, num_tier_pages, n_static;
+  int S, pps;                    // splits, pages per split (S * pps >= P)
+  int max_seq_len;
+  float scale_log2;              // softmax_scale * log2(e)
+};
+
+struct EvictArgs {
+  const int32_t* table_in;
+  const int32_t* lens_in;
+  const float* mass_in;
+  int32_t* table_out;
+  int32_t* lens_out;
+  float* mass_out;
+  int32_t* evicted;              // [B], or null
+  int B, ppsm;
+  int unit;                      // pages evicted together (4 for the group format)
+  int keep, sink, recent;        // units
+};
+
+cudaError_t tree_launch(const TreeArgs& a, int D, cudaStream_t st);
+// Splits tree_launch's first kernel is given when the caller leaves the choice.
+int tree_auto_splits(int fmt, int D, int B, int Hkv, int R, int max_seq_len, int sms);
+
+cudaError_t page_mass_launch(const float* lse, const float* page_lse, const uint64_t* nodes, float decay, const float* in,
+                             float* out, int B, int T, int Hq, int P, int ppsm, cudaStream_t st);
+
+// Longest page-table row evict_launch takes (it holds the row and its mass in shared memory).
+constexpr int kEvictMaxPages = 28672;
+cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st);
+
+}  // namespace kvq

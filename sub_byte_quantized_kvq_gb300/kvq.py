@@ -54,7 +54,8 @@ _lock = threading.Lock()
 EXPORTS = ("kvq_block_bytes", "kvq_cache_bytes", "kvq_quantize_append", "kvq_project_append",
            "kvq_decode_workspace_bytes",
            "kvq_decode_num_splits", "kvq_decode_split", "kvq_decode_combine", "kvq_decode_attention",
-           "kvq_decode_attention_noalloc", "kvq_select_static_channels", "kvq_dequantize", "kvq_status_string",
+           "kvq_decode_attention_noalloc", "kvq_tree_workspace_bytes", "kvq_tree_attention", "kvq_page_mass",
+           "kvq_evict_pages", "kvq_select_static_channels", "kvq_dequantize", "kvq_status_string",
            "kvq_last_cuda_error", "kvq_cuda_error_name", "kvq_version")
 
 
@@ -79,6 +80,11 @@ def lib() -> ctypes.CDLL:
                 "kvq_decode_combine": (I, [pcfg, I, I, I, P, S, P, I, P]),
                 "kvq_decode_attention": (I, [pcfg, pcache, P, I, ctypes.c_float, I, I, P, I, P, S, P]),
                 "kvq_decode_attention_noalloc": (I, [pcfg, pcache, P, I, ctypes.c_float, I, I, P, I, P]),
+                "kvq_tree_workspace_bytes": (I, [pcfg, I, I, I, I, ctypes.POINTER(S)]),
+                "kvq_tree_attention": (I, [pcfg, pcache, P, I, I, P, P, P, I, P, ctypes.c_float, I, I, P, I, P, P, P, S,
+                                           P]),
+                "kvq_page_mass": (I, [pcfg, I, I, I, P, P, P, ctypes.c_float, P, P, P]),
+                "kvq_evict_pages": (I, [pcfg, pcache, P, I, I, I, P, P, P, P, P]),
                 "kvq_select_static_channels": (I, [pcfg, P, P, I, I, P, P]),
                 "kvq_dequantize": (I, [pcfg, pcache, I, I, I, I, I, P, P]),
                 "kvq_status_string": (ctypes.c_char_p, [I]),
@@ -147,6 +153,38 @@ class QuantizedKVCache:
                            self.page_table.data_ptr(), self.seq_lens.data_ptr(),
                            self.staging.data_ptr() if self.staging is not None else None, self.status.data_ptr(),
                            self.static_mask.data_ptr() if self.static_mask is not None else None)
+
+    @classmethod
+    def from_buffers(cls, fmt: int, num_kv_heads: int, head_dim: int, pool: torch.Tensor, page_table: torch.Tensor,
+                     seq_lens: torch.Tensor, status: torch.Tensor, staging: torch.Tensor | None = None,
+                     tier_pool: torch.Tensor | None = None, static_mask: torch.Tensor | None = None,
+                     sigma: float = 3.0, lloyd_iters: int = 16, decode_math: int = KVQ_DECODE_AUTO) -> "QuantizedKVCache":
+        """A handle on device buffers the caller owns (page_table int32
+        [num_seqs, pages_per_seq_max], seq_lens int32 [num_seqs], status int32
+        [1], pool / tier_pool uint8 of whole blocks, staging fp32); nothing is
+        allocated or copied, and the pools' sizes give the page counts."""
+        num_seqs, ppsm = page_table.shape
+        buffers = [pool, page_table, seq_lens, status, staging, tier_pool, static_mask]
+        assert all(t is None or (t.is_contiguous() and t.device == pool.device) for t in buffers)
+        assert page_table.dtype == seq_lens.dtype == status.dtype == torch.int32 and seq_lens.numel() == num_seqs
+        self = cls.__new__(cls)
+        self.cfg = kvq_config(num_seqs, num_kv_heads, head_dim, ppsm, 1, 1 if tier_pool is not None else 0, fmt,
+                              lloyd_iters, sigma, static_mask.shape[-1] if static_mask is not None else 0, decode_math)
+        main = 2 * num_kv_heads * kvq_block_bytes(self.cfg, 0)
+        self.cfg.num_pages = pool.numel() * pool.element_size() // main
+        if tier_pool is not None:
+            self.cfg.num_tier_pages = (tier_pool.numel() * tier_pool.element_size() //
+                                       (2 * num_kv_heads * kvq_block_bytes(self.cfg, 1)))
+        pb, tb, sb = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib().kvq_cache_bytes(ctypes.byref(self.cfg), ctypes.byref(pb), ctypes.byref(tb), ctypes.byref(sb)),
+               "kvq_cache_bytes")
+        if sb.value:   # a page format
+            assert staging is not None and staging.dtype == torch.float32 and staging.numel() * 4 >= sb.value
+        self.device, self.pool, self.tier_pool, self.staging = pool.device, pool, tier_pool, staging
+        self.page_table, self.seq_lens, self.status, self.static_mask = page_table, seq_lens, status, static_mask
+        self.c = kvq_cache(*[None if t is None else t.data_ptr()
+                             for t in (pool, tier_pool, page_table, seq_lens, staging, status, static_mask)])
+        return self
 
     @property
     def head_dim(self) -> int:
@@ -285,6 +323,156 @@ def kvq_decode_attention_noalloc(cache: QuantizedKVCache, q: torch.Tensor, softm
                            f"{NOALLOC_SCRATCH_BYTES}-byte built-in scratch")
     _check(st, "kvq_decode_attention_noalloc")
     return out
+
+
+KVQ_TREE_MAX_NODES = 64
+
+
+def _check_on(device: torch.device, *tensors):
+    """Every tensor (None apart) lies on `device`, a CUDA device."""
+    for t in tensors:
+        if t is not None and (t.device != device or not t.is_cuda):
+            raise ValueError(f"a tensor on {t.device} beside a cache on {device}")
+
+
+def _call(device: torch.device, stream, f, *args) -> int:
+    """f(*args, stream) with `device` current; stream None is that device's current stream."""
+    if device.index == torch.cuda.current_device():
+        return f(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return f(*args, _stream(stream))
+
+
+def _scratch(t: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor allocated here for a call on `stream`: its memory is not handed on before that stream is done with it."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def kvq_tree_workspace_bytes(cache: QuantizedKVCache, num_q_heads: int, num_nodes: int, max_seq_len: int,
+                             num_splits: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().kvq_tree_workspace_bytes(ctypes.byref(cache.cfg), num_q_heads, num_nodes, max_seq_len, num_splits,
+                                          ctypes.byref(n)), "kvq_tree_workspace_bytes")
+    return n.value
+
+
+def alloc_tree_workspace(cache: QuantizedKVCache, num_q_heads: int, num_nodes: int, max_seq_len: int,
+                         num_splits: int = 0) -> torch.Tensor:
+    """A workspace for kvq_tree_attention calls of this shape (needs no initialisation)."""
+    nbytes = kvq_tree_workspace_bytes(cache, num_q_heads, num_nodes, max_seq_len, num_splits)
+    return torch.empty((nbytes + 15) // 16 * 4, dtype=torch.float32, device=cache.device)
+
+
+def tree_mask_from_parents(parents) -> torch.Tensor:
+    """Ancestor words (int64, CPU) of trees given by parent indices [.., T] (a
+    parent comes before its children, -1 for a root): each node attends to
+    itself and its ancestors."""
+    p = torch.as_tensor(parents).to("cpu", torch.int64)
+    T = p.shape[-1]
+    if T > KVQ_TREE_MAX_NODES or bool((p >= torch.arange(T)).any()) or bool((p < -1).any()):
+        raise ValueError("parents: at most 64 nodes, each parent before its children, -1 for a root")
+    words = torch.zeros_like(p)
+    for t in range(T):
+        up = words.gather(-1, p[..., t:t + 1].clamp_min(0)) * (p[..., t:t + 1] >= 0)
+        words[..., t:t + 1] = up | (-(1 << 63) if t == 63 else 1 << t)
+    return words
+
+
+def kvq_tree_attention(cache: QuantizedKVCache, q: torch.Tensor, softmax_scale: float, max_seq_len: int,
+                       k_tree: torch.Tensor | None = None, v_tree: torch.Tensor | None = None,
+                       tree_mask: torch.Tensor | None = None, nodes_per_seq: torch.Tensor | None = None,
+                       num_splits: int = 0, out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                       lse: torch.Tensor | None = None, page_lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q: [num_seqs, T, Hq, D] bf16 -> out [num_seqs, T, Hq, D] (bf16 or f32); T <= 64 drafted
+    tokens with k_tree, v_tree [num_seqs, T, Hkv, D] bf16 (None: the cache alone).
+    tree_mask: int64 ancestor words [T] or [num_seqs, T] (None: a chain).  lse fp32
+    [num_seqs, T, Hq] and page_lse fp32 [num_seqs, T, Hq, ceil(max_seq_len / 16)] are
+    filled when given."""
+    cfg = cache.cfg
+    assert q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 4
+    B, T, Hq, D = q.shape
+    assert B == cfg.num_seqs and D == cfg.head_dim
+    assert (k_tree is None) == (v_tree is None)
+    for t in (k_tree, v_tree):
+        assert t is None or (t.dtype == torch.bfloat16 and t.is_contiguous() and
+                             t.shape == (B, T, cfg.num_kv_heads, D))
+    if tree_mask is not None:
+        assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous()
+        assert tree_mask.shape in ((T,), (B, T))
+    if nodes_per_seq is not None:
+        assert nodes_per_seq.dtype == torch.int32 and nodes_per_seq.is_contiguous() and nodes_per_seq.shape == (B,)
+    if out is None:
+        out = _scratch(torch.empty(q.shape, dtype=out_dtype, device=q.device), stream)
+    assert out.shape == q.shape and out.is_contiguous() and out.dtype in (torch.bfloat16, torch.float32)
+    if lse is not None:
+        assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (B, T, Hq)
+    if page_lse is not None:
+        P = (min(max_seq_len, 16 * cfg.pages_per_seq_max) + 15) // 16
+        assert page_lse.dtype == torch.float32 and page_lse.is_contiguous() and page_lse.shape == (B, T, Hq, P)
+    if workspace is None:
+        workspace = _scratch(alloc_tree_workspace(cache, Hq, T, max_seq_len, num_splits), stream)
+    device = cache.pool.device
+    _check_on(device, q, k_tree, v_tree, tree_mask, nodes_per_seq, out, lse, page_lse, workspace)
+    _check(_call(device, stream, lib().kvq_tree_attention, ctypes.byref(cfg), ctypes.byref(cache.c), _ptr(q), Hq, T,
+                 _ptr(k_tree), _ptr(v_tree), _ptr(tree_mask), int(tree_mask is not None and tree_mask.dim() == 2),
+                 _ptr(nodes_per_seq), float(softmax_scale), max_seq_len, num_splits, _ptr(out), _DTYPE[out.dtype],
+                 _ptr(lse), _ptr(page_lse), _ptr(workspace), workspace.numel() * workspace.element_size()),
+           "kvq_tree_attention")
+    return out
+
+
+def kvq_page_mass(cache: QuantizedKVCache, lse: torch.Tensor, page_lse: torch.Tensor, mass: torch.Tensor,
+                  node_mask: torch.Tensor | None = None, decay: float = 1.0, mass_out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """mass_out = decay * mass + the page weights of the marked nodes (node_mask int64
+    [num_seqs], bit t = node t; None: all).  lse [num_seqs, T, Hq] and page_lse
+    [num_seqs, T, Hq, P] as kvq_tree_attention wrote them; mass fp32 [num_seqs,
+    pages_per_seq_max], updated in place unless mass_out is given."""
+    cfg = cache.cfg
+    B, T, Hq, P = page_lse.shape
+    if mass_out is None:
+        mass_out = mass
+    assert lse.shape == (B, T, Hq) and B == cfg.num_seqs
+    for t in (lse, page_lse, mass, mass_out):
+        assert t.dtype == torch.float32 and t.is_contiguous()
+    assert mass.shape == mass_out.shape == (B, cfg.pages_per_seq_max)
+    if node_mask is not None:
+        assert node_mask.dtype == torch.int64 and node_mask.is_contiguous() and node_mask.shape == (B,)
+    device = cache.pool.device
+    _check_on(device, lse, page_lse, mass, node_mask, mass_out)
+    _check(_call(device, stream, lib().kvq_page_mass, ctypes.byref(cfg), Hq, T, P, _ptr(lse), _ptr(page_lse),
+                 _ptr(node_mask), float(decay), _ptr(mass), _ptr(mass_out)), "kvq_page_mass")
+    return mass_out
+
+
+def kvq_evict_pages(cache: QuantizedKVCache, mass: torch.Tensor, keep_pages: int, sink_pages: int = 0,
+                    recent_pages: int = 0, page_table_out: torch.Tensor | None = None,
+                    seq_lens_out: torch.Tensor | None = None, mass_out: torch.Tensor | None = None,
+                    evicted: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Evict the lightest full pages of every sequence down to keep_pages; returns the int32
+    [num_seqs] counts.  Updates cache.page_table, cache.seq_lens and mass in place, each
+    unless its output tensor is given."""
+    cfg = cache.cfg
+    shape = (cfg.num_seqs, cfg.pages_per_seq_max)
+    page_table_out = cache.page_table if page_table_out is None else page_table_out
+    seq_lens_out = cache.seq_lens if seq_lens_out is None else seq_lens_out
+    mass_out = mass if mass_out is None else mass_out
+    if evicted is None:
+        evicted = _scratch(torch.empty(shape[0], dtype=torch.int32, device=cache.device), stream)
+    for t in (mass, mass_out):
+        assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == shape
+    assert page_table_out.dtype == torch.int32 and page_table_out.is_contiguous() and page_table_out.shape == shape
+    for t in (seq_lens_out, evicted):
+        assert t.dtype == torch.int32 and t.is_contiguous() and t.shape == shape[:1]
+    device = cache.pool.device
+    _check_on(device, mass, page_table_out, seq_lens_out, mass_out, evicted)
+    _check(_call(device, stream, lib().kvq_evict_pages, ctypes.byref(cfg), ctypes.byref(cache.c), _ptr(mass), keep_pages,
+                 sink_pages, recent_pages, _ptr(page_table_out), _ptr(seq_lens_out), _ptr(mass_out), _ptr(evicted)),
+           "kvq_evict_pages")
+    return evicted
 
 
 def kvq_dequantize(cache: QuantizedKVCache, seq: int, kv_head: int, which: int, tok_begin: int, tok_end: int,
