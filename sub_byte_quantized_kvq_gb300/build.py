@@ -24,7 +24,8 @@ PER_TU = {"kvq_quantize.cu": ["--fmad=false"]}
 TUS = ["kvq_api.cu", "kvq_quantize.cu", "kvq_decode.cu", "kvq_decode_int4.cu", "kvq_decode_e2m1.cu",
        "kvq_decode_cb2.cu", "kvq_decode_tiered.cu", "kvq_decode_cb2s.cu",
        "kvq_decode_a3.cu", "kvq_decode_cb2g.cu", "kvq_noalloc.cu",
-       "kvq_tree.cu", "kvq_evict.cu"]
+       "kvq_tree.cu", "kvq_tree_int4.cu", "kvq_tree_e2m1.cu", "kvq_tree_cb2.cu", "kvq_tree_tiered.cu",
+       "kvq_tree_cb2s.cu", "kvq_tree_a3.cu", "kvq_tree_cb2g.cu", "kvq_evict.cu"]
 
 
 def _nvcc() -> str:

@@ -1,5 +1,6 @@
 // kvq_api.cu -- the C ABI (include/kvq.h): argument validation, sizing queries,
 // the split heuristic, and the debug dequantization kernel.
+#include <algorithm>
 #include <cmath>
 
 #include "kvq_block.cuh"
@@ -453,7 +454,7 @@ static int tree_splits(const kvq_config* cfg, int32_t num_q_heads, int32_t num_n
                        int32_t num_splits) {
   if (num_splits) return num_splits;
   const int sms = num_sms();
-  return tree_auto_splits(cfg->format, cfg->head_dim, cfg->num_seqs, cfg->num_kv_heads,
+  return tree_auto_splits(cfg->num_seqs, cfg->num_kv_heads,
                           num_q_heads / cfg->num_kv_heads * num_nodes, visible_bound(cfg, max_seq_len), sms > 0 ? sms : 1);
 }
 static size_t tree_rows(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int S) {
@@ -518,8 +519,7 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const kvq_cache* cache, con
   a.num_tier_pages = cfg->num_tier_pages;
   a.n_static = cfg->format == KVQ_FMT_CB2_STATIC ? cfg->static_channels : 0;
   a.S = S;
-  a.pps = a.P > 0 ? (a.P + S - 1) / S : 1;
-  if (cfg->format == KVQ_FMT_CB2_GROUP4) a.pps = (a.pps + kGroupPages - 1) / kGroupPages * kGroupPages;   // whole groups
+  a.pps = (std::max((a.P + S - 1) / S, 1) + kTreeTilePages - 1) / kTreeTilePages * kTreeTilePages;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   return cuda_status(tree_launch(a, cfg->head_dim, static_cast<cudaStream_t>(stream)));
 }

@@ -1,5 +1,5 @@
 // kvq_block.cuh -- the value one element of a block stands for, read straight
-// from its bytes (the debug path, and the plain tree-attention kernel).
+// from its bytes (the debug path).
 #pragma once
 #include "kvq_common.cuh"
 

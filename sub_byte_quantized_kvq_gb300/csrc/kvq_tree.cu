@@ -10,8 +10,8 @@
 // fp32 staging tail and the drafted tokens' bf16 K and V), joins the splits and
 // writes the results.
 #include <algorithm>
+#include <mutex>
 
-#include "kvq_block.cuh"
 #include "kvq_tree.cuh"
 
 namespace kvq {
@@ -21,27 +21,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-constexpr float kLn2 = 0.69314718055994531f;
-
-__host__ __device__ constexpr bool page_format(int f) { return f >= KVQ_FMT_CB2_OUTLIER; }
-__host__ __device__ constexpr int unit_tokens(int f) { return f == KVQ_FMT_CB2_GROUP4 ? kPage * kGroupPages : kPage; }
-
-// What of a sequence is visible, and where it lies.
-struct SeqView {
-  int len;       // visible tokens
-  int blocks;    // pages of them that lie in blocks
-  int nodes;     // live tree nodes
-};
-__device__ __forceinline__ SeqView seq_view(const TreeArgs& a, int b) {
-  const int L = max(a.seq_lens[b], 0);
-  SeqView v;
-  v.len = min(L, a.max_seq_len);
-  const int pages = (v.len + kPage - 1) / kPage, u = unit_tokens(a.fmt);
-  v.blocks = page_format(a.fmt) ? min(pages, L / u * (u / kPage)) : pages;
-  v.nodes = a.nodes ? min(max(a.nodes[b], 0), a.T) : a.T;
-  return v;
-}
-
 // ----------------------------------------------------------------------------- rows on the CUDA cores
 // A warp's state for kWR rows: channel c = 32 i + lane of row w in o[w][i].
 constexpr int kWR = 4;
@@ -124,86 +103,6 @@ __device__ __forceinline__ void load_queries(const TreeArgs& a, int b, int h, in
     const int r = r0 + i / D, t = r / a.G, g = r % a.G;
     qs[i / D][i % D] =
         r < live ? __bfloat162float(a.q[(((size_t)b * a.T + t) * a.Hq + (size_t)h * a.G + g) * D + i % D]) : 0.f;
-  }
-}
-__device__ __forceinline__ float* page_lse_row(const TreeArgs& a, int b, int h, int r) {
-  return a.page_lse + (((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * a.P;
-}
-
-// ----------------------------------------------------------------------------- cached pages
-// Grid (S, Hkv * ceil(R / kRows), B): the pages of one split for kRows rows of
-// one kv head, page by page through shared memory in fp32.
-constexpr int kRows = 32;
-template <int D>
-__global__ void __launch_bounds__(256) tree_split_kernel(const TreeArgs a) {
-  __shared__ float qs[kRows][D];
-  __shared__ float kvs[2][kPage][D + 1];
-  const int nrt = (a.R + kRows - 1) / kRows;
-  const int split = blockIdx.x, h = blockIdx.y / nrt, r0 = (blockIdx.y % nrt) * kRows, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const SeqView v = seq_view(a, b);
-  const int live = v.nodes * a.G;
-  if (split == 0 && blockIdx.y == 0 && threadIdx.x == 0 && a.seq_lens[b] > a.max_seq_len)
-    atomicOr(a.status, KVQ_STATUS_SEQ_TOO_LONG);
-  load_queries<D>(a, b, h, r0, kRows, live, qs);
-  RowState<D> st;
-  row_state_init(st);
-  const int main_bf = a.fmt == KVQ_FMT_TIERED ? kBlkCb2 : a.fmt;
-  const int u = unit_tokens(a.fmt) / kPage;
-  const int32_t* pt = a.page_table + (size_t)b * a.ppsm;
-  for (int p = split * a.pps; p < min((split + 1) * a.pps, a.P); ++p) {
-    int ntok = p < v.blocks ? min(kPage, v.len - kPage * p) : 0;
-    bool tier = false;
-    const uint8_t *blk = nullptr, *cbk = nullptr;
-    size_t stride = 0;
-    if (ntok > 0) {
-      bool ok = true;
-      for (int j = p / u * u; j < p / u * u + u; ++j) {   // a group with a bad page is left out whole
-        const uint32_t e = (uint32_t)pt[j], phys = e & 0x7FFFFFFFu;
-        const bool te = (e >> 31) != 0;
-        ok = ok && (te ? (a.fmt == KVQ_FMT_TIERED && phys < (uint32_t)a.num_tier_pages) : phys < (uint32_t)a.num_pages);
-      }
-      if (ok) {
-        const uint32_t e = (uint32_t)pt[p], phys = e & 0x7FFFFFFFu;
-        tier = (e >> 31) != 0;
-        stride = block_stride(tier ? kBlkFp8 : main_bf, D);
-        blk = (tier ? a.tier_pool : a.pool) + ((size_t)phys * a.Hkv + h) * 2 * stride;
-        cbk = u > 1 ? a.pool + ((size_t)(uint32_t)pt[p / u * u] * a.Hkv + h) * 2 * stride : blk;
-      } else {
-        ntok = 0;
-        if (threadIdx.x == 0) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
-      }
-    }
-    __syncthreads();
-    if (ntok > 0)
-      for (int i = threadIdx.x; i < 2 * kPage * D; i += blockDim.x) {
-        const int role = i / (kPage * D), t = i / D % kPage, c = i % D;
-        kvs[role][t][c] = block_value(tier ? kBlkFp8 : main_bf, blk + role * stride, cbk + role * stride, role, D, t, c);
-      }
-    __syncthreads();
-    uint32_t seen[kWR];
-    float page[kWR];
-#pragma unroll
-    for (int w = 0; w < kWR; ++w) {
-      seen[w] = r0 + warp * kWR + w < live ? (1u << ntok) - 1u : 0u;
-      page[w] = -INFINITY;
-    }
-    if (ntok > 0) rows_chunk<D>(st, qs + warp * kWR, kvs[0], kvs[1], seen, a.scale_log2, page, lane);
-    if (a.page_lse && lane == 0)
-#pragma unroll
-      for (int w = 0; w < kWR; ++w) {
-        const int r = r0 + warp * kWR + w;
-        if (r < a.R) page_lse_row(a, b, h, r)[p] = page[w] * kLn2;
-      }
-  }
-#pragma unroll
-  for (int w = 0; w < kWR; ++w) {
-    const int r = r0 + warp * kWR + w;
-    if (r >= a.R) continue;
-    const size_t row = (((size_t)b * a.Hkv + h) * a.S + split) * a.R + r;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) a.part_o[row * D + 32 * i + lane] = st.o[w][i];
-    if (lane == 0) a.part_ml[row] = make_float2(st.m[w], st.l[w]);
   }
 }
 
@@ -289,17 +188,62 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
 }
 
 // ----------------------------------------------------------------------------- host side
-int tree_auto_splits(int, int, int B, int Hkv, int R, int max_seq_len, int sms) {
-  const long long pages = (max_seq_len + kPage - 1) / kPage;
-  const long long ctas = (long long)B * Hkv * ((R + kRows - 1) / kRows);
-  const long long want = (4ll * sms + ctas - 1) / ctas;
-  return (int)std::max(1ll, std::min({want, pages / 16, 64ll}));
+static TreeKernel tree_kernel(int fmt, int D) {
+  switch (fmt) {
+    case KVQ_FMT_INT4_G32: return tree_kernel_int4(D);
+    case KVQ_FMT_FP4_E2M1_S16: return tree_kernel_e2m1(D);
+    case KVQ_FMT_CB2_OUTLIER: return tree_kernel_cb2(D);
+    case KVQ_FMT_CB2_STATIC: return tree_kernel_cb2s(D);
+    case KVQ_FMT_ASYM3_OUTLIER: return tree_kernel_a3(D);
+    case KVQ_FMT_CB2_GROUP4: return tree_kernel_cb2g(D);
+    default: return tree_kernel_tiered(D);
+  }
+}
+
+// One CTA runs per SM, so the cached pages of the call take
+// waves(S) x (tiles of a split + what a CTA costs besides, about three tiles:
+// barriers, tensor memory, the query, the pipeline's fill and drain, the
+// partial state) -- the smallest product, and among equals the fewest splits.
+int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms) {
+  const long long tiles = (max_seq_len + kPage * kTreeTilePages - 1) / (kPage * kTreeTilePages);
+  const long long units = (long long)B * Hkv * ((R + kTreeRows - 1) / kTreeRows);
+  long long best = 1, cost = -1;
+  for (long long s = 1; s <= std::min<long long>(std::max<long long>(tiles, 1), 256); ++s) {
+    const long long c = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
+    if (cost < 0 || c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return (int)best;
+}
+
+// The split kernels' dynamic shared memory, allowed once per kernel and device.
+static cudaError_t allow_smem(const TreeKernel& k) {
+  static std::mutex mutex;
+  static struct { void* fn; int dev; } done[256];
+  static int n = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  for (int i = 0; i < n; ++i)
+    if (done[i].fn == k.fn && done[i].dev == dev) return cudaSuccess;
+  e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+  if (e == cudaSuccess && n < 256) {
+    done[n].fn = k.fn;
+    done[n++].dev = dev;
+  }
+  return e;
 }
 
 template <int D>
 static cudaError_t tree_launch_d(const TreeArgs& a, cudaStream_t st) {
-  tree_split_kernel<D><<<dim3(a.S, a.Hkv * ((a.R + kRows - 1) / kRows), a.B), 256, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const TreeKernel k = tree_kernel(a.fmt, D);
+  cudaError_t e = allow_smem(k);
+  if (e != cudaSuccess) return e;
+  void* args[] = {const_cast<TreeArgs*>(&a)};
+  e = cudaLaunchKernel(k.fn, dim3(a.S, a.Hkv * ((a.R + kTreeRows - 1) / kTreeRows), a.B), dim3(k.threads), args, k.smem, st);
   if (e != cudaSuccess) return e;
   tree_merge_kernel<D><<<dim3((a.R + kMRows - 1) / kMRows, a.Hkv, a.B), 128, 0, st>>>(a);
   return cudaGetLastError();

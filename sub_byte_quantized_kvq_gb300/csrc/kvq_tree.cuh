@@ -45,9 +45,49 @@ struct EvictArgs {
   int keep, sink, recent;        // units
 };
 
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kTreeRows = 128;      // rows of a CTA
+constexpr int kTreeTilePages = 8;   // a split is whole tiles of this many pages
+
+__host__ __device__ constexpr bool page_format(int f) { return f >= KVQ_FMT_CB2_OUTLIER; }
+__host__ __device__ constexpr int unit_tokens(int f) { return f == KVQ_FMT_CB2_GROUP4 ? kPage * kGroupPages : kPage; }
+
+// What of a sequence is visible, and where it lies.
+struct SeqView {
+  int len;       // visible tokens
+  int blocks;    // pages of them that lie in blocks
+  int nodes;     // live tree nodes
+};
+__device__ __forceinline__ SeqView seq_view(const TreeArgs& a, int b) {
+  const int L = max(a.seq_lens[b], 0);
+  SeqView v;
+  v.len = min(L, a.max_seq_len);
+  const int pages = (v.len + kPage - 1) / kPage, u = unit_tokens(a.fmt);
+  v.blocks = page_format(a.fmt) ? min(pages, L / u * (u / kPage)) : pages;
+  v.nodes = a.nodes ? min(max(a.nodes[b], 0), a.T) : a.T;
+  return v;
+}
+__device__ __forceinline__ float* page_lse_row(const TreeArgs& a, int b, int h, int r) {
+  return a.page_lse + (((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * a.P;
+}
+
+// One translation unit per format instantiates its kernels.
+struct TreeKernel {
+  void* fn;
+  size_t smem;
+  int threads;
+};
+TreeKernel tree_kernel_int4(int D);
+TreeKernel tree_kernel_e2m1(int D);
+TreeKernel tree_kernel_cb2(int D);
+TreeKernel tree_kernel_tiered(int D);
+TreeKernel tree_kernel_cb2s(int D);
+TreeKernel tree_kernel_a3(int D);
+TreeKernel tree_kernel_cb2g(int D);
+
 cudaError_t tree_launch(const TreeArgs& a, int D, cudaStream_t st);
 // Splits tree_launch's first kernel is given when the caller leaves the choice.
-int tree_auto_splits(int fmt, int D, int B, int Hkv, int R, int max_seq_len, int sms);
+int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms);
 
 cudaError_t page_mass_launch(const float* lse, const float* page_lse, const uint64_t* nodes, float decay, const float* in,
                              float* out, int B, int T, int Hq, int P, int ppsm, cudaStream_t st);

@@ -1,0 +1,8 @@
+// kvq_tree_cb2s.cu -- instantiates the tree attention kernels of one cache format.
+#include "kvq_tree_split.cuh"
+
+namespace kvq {
+TreeKernel tree_kernel_cb2s(int D) {
+  return D == 64 ? tree::tree_kernel_info<KVQ_FMT_CB2_STATIC, 64>() : tree::tree_kernel_info<KVQ_FMT_CB2_STATIC, 128>();
+}
+}  // namespace kvq

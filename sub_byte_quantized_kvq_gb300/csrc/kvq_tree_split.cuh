@@ -1,0 +1,636 @@
+// kvq_tree_split.cuh -- tree attention over the cached pages on the tensor cores.
+//
+// One CTA per (split, kv head x tile of 128 rows, sequence).  A tile of 128
+// rows (node, head of the group) x kTok tokens costs two MMAs, S = Q K^T and
+// O += P V, and each page's codes are expanded once for all of the rows:
+//
+//   producer warp   one bulk asynchronous copy per block into a ring of stages
+//                   (a stage: the K or the V blocks of one tile's pages)
+//   8 dequant warps codes -> fp16 tiles in shared memory, K as [token][channel],
+//                   V transposed as [channel][token], both K-major with 128-byte
+//                   swizzle; the block layout holds mma fragments, which
+//                   stmatrix turns into rows; outliers are stored over their slots
+//   MMA warp        tcgen05.mma with Q and P from tensor memory, the tiles from
+//                   shared memory; S(i + 1) is issued before PV(i), so the tensor
+//                   cores work while the softmax warps do
+//   4 softmax warps one row a thread (tensor-memory lane): running maximum with
+//                   lazy rescale, p = 2^(s - m), page sums for page_lse; P goes
+//                   over S's own columns
+//
+// Precision: Q is scaled by a power of two into fp16 range and exact; K is
+// exact in fp16 (INT4: an fp16 pair, two MMAs); S, m, l and O are fp32.  P is
+// rounded to fp16 (2^-12 relative on average; biased by 2^kPBias so that small
+// p keep their bits), V to fp16 where the format's value has more (INT4, FP8
+// tier): for a bf16 result both are below its own rounding.
+//
+// What bounds it: at 128 rows a tile of 128 tokens takes about 1024 cycles of
+// MMA, 1024 of exponentials (16 a cycle and SM) and 800-1200 of this SM's share
+// of the measured HBM rate, next to 64 KB of shared-memory tile writes and
+// reads; fewer rows leave the exponentials out, not the rest.
+#pragma once
+#include "kvq_decode.cuh"
+#include "kvq_tc.cuh"
+#include "kvq_tree.cuh"
+
+namespace kvq {
+namespace tree {
+
+constexpr int kM = kTreeRows;
+constexpr int kDequantWarps = 8;
+constexpr int kThreads = 32 * (4 + kDequantWarps + 2);
+constexpr int kMeta = 8;                // tiles whose page records are kept (producer to softmax: at most 7 apart)
+constexpr float kPBias = 6.f;           // p <= 2^(kRescaleTh + kPBias) stays in fp16 range
+
+template <int FMT, int D>
+struct Plan {
+  using F = Fmt<FMT>;
+  static constexpr bool kPair = F::kMain == kBlkInt4;        // K as an fp16 pair
+  static constexpr int kTok = kPair ? 64 : 128;              // (two K tiles of 128 tokens would not fit)
+  static constexpr int kPages = kTok / kPage;
+  static constexpr int kTile = kTok * D * 2;                 // bytes of an fp16 tile
+  static constexpr int kBuf = (kPair ? 3 : 2) * kTile;       // one buffer: K [, K low], V
+  // a page's slot: its (virtual) block from offset 0; the group format keeps the codebook in the first page's
+  static constexpr int kSlot = F::kGroup ? 12 * D + kOutPrefetch : half_slot_bytes<FMT, D>();
+  static constexpr int kStage = kPages * kSlot;
+  static constexpr int kMisc = 1024;                         // barriers and page records
+  static constexpr int kFit = (227 * 1024 - 1024 - 2 * kBuf - kMisc) / kStage;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kSmem = 1024 + 2 * kBuf + kStages * kStage + kMisc;   // 1024: alignment slack
+  static_assert(kStages >= 2 && kStage % 16 == 0 && kTile % 1024 == 0, "tree attention plan");
+};
+
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((unsigned short)v) : "memory");
+}
+
+// Where a page's values go in a swizzled tile.  A row is 64 fp16 (128 bytes);
+// 16-byte chunk k of row r lies at chunk k ^ (r % 8).
+template <int D, int TOK>
+struct KTile {   // rows = tokens, D / 64 row groups
+  uint32_t tile;
+  int page;
+  __device__ __forceinline__ uint32_t at(int t, int c) const {
+    const int row = kPage * page + t;
+    return tile + (c >> 6) * (TOK * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2;
+  }
+  // lane's row address of step 0, and of step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15)
+  __device__ __forceinline__ uint32_t lane_row(int lane) const { return tile + (kPage * page + (lane & 15)) * 128; }
+  __device__ __forceinline__ uint32_t step(uint32_t row, int lane, int s) const {
+    return row + (s >> 2) * (TOK * 128) + (((((s & 3) * 2) ^ (lane & 7)) ^ (lane >> 4)) << 4);
+  }
+};
+template <int D, int TOK>
+struct VTile {   // rows = channels, TOK / 64 row groups
+  uint32_t tile;
+  int page;
+  __device__ __forceinline__ uint32_t at(int t, int c) const {
+    return tile + (page >> 2) * (D * 128) + c * 128 + ((((page & 3) * 2 + (t >> 3)) ^ (c & 7)) << 4) + (t & 7) * 2;
+  }
+  // (matrices: channels 0-7 / 8-15 x tokens 0-7 / 8-15)
+  __device__ __forceinline__ uint32_t lane_row(int lane) const {
+    return tile + (page >> 2) * (D * 128) + (lane & 15) * 128 + ((((page & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+  }
+  __device__ __forceinline__ uint32_t step(uint32_t row, int, int s) const { return row + s * 2048; }
+};
+
+// The outliers of a side-list over their slots' values: two records at a time,
+// a token a lane.  Records past the prefetched ones come from global memory.
+template <int D, int BLK, class Tile>
+__device__ __forceinline__ void patch_side_list(uint32_t side_s, const uint8_t* side_g, const Tile& tile, int lane) {
+  const int n = min((int)lds8(side_s), D), t = lane & 15;
+  for (int i = lane >> 4; i < n; i += 2) {
+    uint32_t head, value;
+    if (i < kChunk) {
+      head = lds32(side_s + 4 + 20 * i);
+      value = lds8(side_s + 8 + 20 * i + t);
+    } else {
+      head = *reinterpret_cast<const uint32_t*>(side_g + 4 + 20 * i);
+      value = side_g[8 + 20 * i + t];
+    }
+    if ((head >> (16 + t)) & 1u) sts16(tile.at(t, head & (D - 1)), e4m3x2_to_f16x2(value));
+  }
+}
+
+// Tokens from `ntok` on as zeros in a V tile (their probability is 0, and stale bytes may stand for anything).
+template <int D, class Tile>
+__device__ __forceinline__ void zero_tokens(const Tile& tile, int ntok, int lane) {
+  for (int c = lane; c < D; c += 32)
+#pragma unroll
+    for (int t = 0; t < kPage; ++t)
+      if (t >= ntok) sts16(tile.at(t, c), 0u);
+}
+
+// One K block (role 0) or V block (role 1) -> its place in the fp16 tile.
+//   blk    shared address of the page's slot, cb of the slot that holds its codebook
+//   gblk   the block in global memory (side-list records past the prefetch)
+//   tier   the block is an FP8 block
+// K of an FP8 block is left unscaled (its page's scale is applied to the scores).
+template <int FMT, int D, int ROLE, class Tile>
+__device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const uint8_t* gblk, bool tier, const Tile& tile,
+                                              const Tile& low, int lane) {
+  using F = Fmt<FMT>;
+  constexpr int NS = D / 16, BLK = F::kMain;
+  const int g = lane >> 2, q4 = lane & 3;
+  const uint32_t row = tile.lane_row(lane);
+  if (FMT == KVQ_FMT_TIERED && tier) {
+    const float sc = ROLE == 1 ? ldsf(blk + fp8_sc_off(D)) : 1.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint32_t x[4];
+      fp8_frag(lds64(blk + 8 * NS * lane + 8 * s), x);
+      if (ROLE == 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(u32_as_h2(x[k]));
+          x[k] = h2_as_u32(__floats2half2_rn(f.x * sc, f.y * sc));
+        }
+      stmatrix4(tile.step(row, lane, s), x);
+    }
+    return;
+  }
+  if constexpr (BLK == kBlkInt4) {
+    constexpr int NG = D / 32, CAP = int4_cap(D);
+    const uint32_t lrow = low.lane_row(lane);
+    uint32_t w[NS];
+    load_e2m1_words<D>(blk, lane, w);   // one u32 of nibbles per step, as E2M1
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint32_t hi[4], lo[4];
+      if (ROLE == 0) {
+        const uint32_t z0 = lds32(blk + int4_sz_off(D) + 4 * (g * NG + (s >> 1)));
+        const uint32_t z1 = lds32(blk + int4_sz_off(D) + 4 * ((g + 8) * NG + (s >> 1)));
+        int4_k_frag(w[s], fp16_bits_to_float(z0), fp16_bits_to_float(z0 >> 16), fp16_bits_to_float(z1),
+                    fp16_bits_to_float(z1 >> 16), hi, lo);
+        stmatrix4(low.step(lrow, lane, s), lo);
+      } else {
+        float S[4], M[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t z = lds32(blk + int4_sz_off(D) + 4 * ((2 * q4 + (i & 1) + 8 * (i >> 1)) * NG + (s >> 1)));
+          S[i] = fp16_bits_to_float(z);
+          M[i] = fp16_bits_to_float(z >> 16);
+        }
+        int4_v_frag(w[s], S, M, hi, lo);
+      }
+      stmatrix4(tile.step(row, lane, s), hi);
+    }
+    __syncwarp();
+    for (int e = lane; e < kPage * CAP; e += 32) {
+      const int t = e / CAP;
+      if (e - t * CAP < (int)lds8(blk + int4_cnt_off(D) + t)) {
+        const int c = lds8(blk + int4_ch_off(D) + e) & (D - 1);
+        sts16(tile.at(t, c), lds16(blk + int4_val_off(D) + 2 * e));
+        if (ROLE == 0) sts16(low.at(t, c), 0u);
+      }
+    }
+  } else if constexpr (BLK == kBlkE2m1) {
+    uint32_t w[NS];
+    load_e2m1_words<D>(blk, lane, w);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint32_t x[4];
+      e2m1_frag(w[s], x);
+      const uint32_t sc = blk + e2m1_sc_off(D) + 16 * s;
+      if (ROLE == 0) {   // tokens g (registers 0, 2) and g + 8
+        const __half2 sh = u32_as_h2(e4m3x2_to_f16x2(lds8(sc + g) | (lds8(sc + g + 8) << 8)));
+        const __half2 s0 = __low2half2(sh), s1 = __high2half2(sh);
+        x[0] = h2_as_u32(__hmul2(u32_as_h2(x[0]), s0));
+        x[1] = h2_as_u32(__hmul2(u32_as_h2(x[1]), s1));
+        x[2] = h2_as_u32(__hmul2(u32_as_h2(x[2]), s0));
+        x[3] = h2_as_u32(__hmul2(u32_as_h2(x[3]), s1));
+      } else {           // tokens 2q, 2q + 1 (registers 0, 1) and + 8
+        const uint32_t s01 = e4m3x2_to_f16x2(lds16(sc + 2 * q4)), s23 = e4m3x2_to_f16x2(lds16(sc + 2 * q4 + 8));
+        x[0] = hmul2u(x[0], s01);
+        x[1] = hmul2u(x[1], s01);
+        x[2] = hmul2u(x[2], s23);
+        x[3] = hmul2u(x[3], s23);
+      }
+      stmatrix4(tile.step(row, lane, s), x);
+    }
+  } else if constexpr (BLK == kBlkA3) {
+    uint32_t xw[D / 32], yw[D / 64];
+    load_a3_words<D>(blk, lane, xw, yw);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint32_t x[4];
+      if (ROLE == 0) a3_k_frag<D>(blk, xw, yw, s, q4, x);
+      else a3_v_frag<D>(blk, xw, yw, s, g, x);
+      stmatrix4(tile.step(row, lane, s), x);
+    }
+    __syncwarp();
+    patch_side_list<D, BLK>(blk + a3_out_off(D), gblk + a3_out_off(D), tile, lane);
+  } else {   // 2-bit codebooks
+    const uint32_t book = cb + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
+    uint32_t w[D / 32];
+    load_codes<D>(blk + (F::kGroup ? cb2g_code_off(D) : 0), lane, w);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      uint32_t x[4];
+      const uint32_t w16 = (s & 1) ? w[s >> 1] >> 16 : w[s >> 1];
+      if (ROLE == 0) cb2_k_frag(book, w16, s, x);
+      else cb2_v_frag(book, w16, s, x);
+      stmatrix4(tile.step(row, lane, s), x);
+    }
+    __syncwarp();
+    if constexpr (BLK == kBlkCb2s) {   // the static channels' fp16 values
+      const int n = min((int)lds8(blk + cb2s_hdr_off(D)), kMaxStatic), t = lane & 15;
+      for (int i = lane >> 4; i < n; i += 2)
+        sts16(tile.at(t, lds8(blk + cb2s_hdr_off(D) + 1 + i) & (D - 1)), lds16(blk + cb2s_val_off(D) + 32 * i + 2 * t));
+    } else {
+      patch_side_list<D, BLK>(blk + cb2_out_off(D), gblk + cb2_out_off(D), tile, lane);
+    }
+  }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ const uint8_t* tree_block(const TreeArgs& a, int h, int32_t e, int role) {
+  const size_t phys = (uint32_t)e & 0x7FFFFFFFu;
+  if (FMT == KVQ_FMT_TIERED && e < 0) return a.tier_pool + ((phys * a.Hkv + h) * 2 + role) * block_stride(kBlkFp8, D);
+  return a.pool + ((phys * a.Hkv + h) * 2 + role) * block_stride(Fmt<FMT>::kMain, D);
+}
+
+// -inf in page_lse for pages [p_lo, p_hi) of the CTA's rows [r_lo, r_hi).
+__device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, int r_lo, int r_hi, int p_lo, int p_hi) {
+  const int n = p_hi - p_lo;
+  if (n <= 0) return;
+  for (int r = r_lo + (int)(threadIdx.x >> 5); r < r_hi; r += kThreads / 32) {
+    float* row = page_lse_row(a, b, h, r);
+    for (int p = p_lo + (int)(threadIdx.x & 31); p < p_hi; p += 32) row[p] = -INFINITY;
+  }
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs a) {
+  using F = Fmt<FMT>;
+  using P = Plan<FMT, D>;
+  constexpr int TOK = P::kTok, PAGES = P::kPages, RS = P::kStages, SLOT = P::kSlot;
+  extern __shared__ uint8_t raw_smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nmt = (a.R + kM - 1) / kM;
+  const int split = blockIdx.x, h = blockIdx.y / nmt, r0 = (blockIdx.y % nmt) * kM, b = blockIdx.z;
+  const SeqView v = seq_view(a, b);
+  const int live = min(v.nodes * a.G, a.R), rows = min(kM, live - r0), r_end = min(r0 + kM, a.R);
+  if (split == 0 && blockIdx.y == 0 && tid == 0 && a.seq_lens[b] > a.max_seq_len) atomicOr(a.status, KVQ_STATUS_SEQ_TOO_LONG);
+  const int p0 = split * a.pps, p1 = min(p0 + a.pps, v.blocks), pn = min(p0 + a.pps, a.P);
+  const int n_tiles = rows > 0 && p1 > p0 ? (p1 - p0 + PAGES - 1) / PAGES : 0;
+  if (a.page_lse) {
+    fill_page_lse(a, b, h, max(r0, live), r_end, p0, pn);
+    if (rows > 0) fill_page_lse(a, b, h, r0, r0 + rows, max(p0, p1), pn);
+  }
+  const size_t part0 = (((size_t)b * a.Hkv + h) * a.S + split) * a.R + r0;
+  if (n_tiles == 0) {
+    for (int r = tid; r < rows; r += kThreads) a.part_ml[part0 + r] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+
+  uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
+  uint8_t* stages = smem + 2 * P::kBuf;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stages + RS * P::kStage);
+  uint64_t *raw_full = bars, *raw_empty = raw_full + RS, *k_full = raw_empty + RS, *k_empty = k_full + 2, *v_full = k_empty + 2,
+           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 1;
+  int32_t* meta = reinterpret_cast<int32_t*>(drain + 1);                  // [kMeta][PAGES] page-table entry or kNoPage
+  float* kscale = reinterpret_cast<float*>(meta + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(kscale + kMeta * PAGES);
+  static_assert((2 * RS + 14) * 8 + 2 * kMeta * PAGES * 4 + 4 <= P::kMisc, "barriers and page records");
+  const int n_sm = (rows + 31) / 32;   // softmax warps with rows
+  if (tid == 0) {
+    for (int i = 0; i < RS; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], PAGES);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], PAGES);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], PAGES);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], n_sm);
+    }
+    mbar_init(o_done, 1);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  // tensor memory: S tiles (P over them) at columns 0 and 128, O at 256, Q at 384
+  const uint32_t tmem = *tslot, t_o = tmem + 256, t_q = tmem + 384;
+  bool ok = true;
+
+  // ---- each softmax thread's query row into tensor memory
+  float f = 0.f;
+  if (warp < n_sm) {
+    const int r = r0 + tid;
+    const bool on = tid < rows;
+    const __nv_bfloat16* qr = a.q + (((size_t)b * a.T + (on ? r / a.G : 0)) * a.Hq + (size_t)h * a.G + (on ? r % a.G : 0)) * D;
+    float mx = 0.f;
+    for (int i = 0; i < D / 8; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(qr)[i];
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+    }
+    int e = 0;
+    frexpf(mx, &e);
+    const int k = mx > 0.f && mx < INFINITY ? min(max(e - 15, -100), 100) : 0;
+    // the scale's sign goes with the query, so that the score factor f is positive
+    const float qs = on ? copysignf(ldexpf(1.f, -k), a.scale_log2) : 0.f;
+    f = fmaxf(ldexpf(fabsf(a.scale_log2), k), 1e-36f);
+    for (int c = 0; c < D / 64; ++c) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(qr)[8 * c + i];
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[4 * i + j] = on ? h2_as_u32(__floats2half2_rn(__uint_as_float(u[j] << 16) * qs,
+                                                          __uint_as_float(u[j] & 0xFFFF0000u) * qs))
+                            : 0u;
+      }
+      tc::st32(t_q + ((uint32_t)(32 * warp) << 16) + 32 * c, w);
+    }
+    tc::wait_st();
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+
+  if (warp < n_sm) {
+    // ------------------------------------------------------------------ softmax
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    const bool on = tid < rows;
+    float* lse_row = a.page_lse && on ? page_lse_row(a, b, h, r0 + tid) : nullptr;
+    const bool vec = a.page_lse && (a.P & 3) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 15) == 0;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n_tiles; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, kWaitLimitNs));
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t ts = tmem + lanes + (i & 1) * 128;
+      const int32_t* ent = meta + (i & (kMeta - 1)) * PAGES;
+      const float* ks = kscale + (i & (kMeta - 1)) * PAGES;
+      const int pt = p0 + i * PAGES;
+      auto ntok_of = [&](int j) { return ent[j] == kNoPage ? 0 : min(kPage, v.len - kPage * (pt + j)); };
+      float pm[PAGES], mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < TOK / 32; ++c) {
+        float s[32];
+        tc::ld32(ts + 32 * c, s);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int j = 2 * c + hh, n = ntok_of(j);
+          float x = -INFINITY;
+          if (n == kPage) {
+#pragma unroll
+            for (int k = 0; k < kPage; ++k) x = fmaxf(x, s[kPage * hh + k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < kPage; ++k) x = k < n ? fmaxf(x, s[kPage * hh + k]) : x;
+          }
+          pm[j] = x * (FMT == KVQ_FMT_TIERED ? f * ks[j] : f);
+          mx = fmaxf(mx, pm[j]);
+        }
+      }
+      const bool need = mx > m + kRescaleTh;
+      if (__any_sync(0xffffffffu, need)) {
+        const float alpha = need ? ex2(m - mx) : 1.f;
+        l *= alpha;
+        m = need ? mx : m;
+        if (i > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done, (i - 1) & 1, kWaitLimitNs));
+          if (!ok) break;
+          tc::fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            uint32_t u[32];
+            tc::ld32(t_o + lanes + 32 * c, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * alpha);
+            tc::st32(t_o + lanes + 32 * c, u);
+          }
+          tc::wait_st();
+        }
+      }
+      const float mb = (m == -INFINITY ? 0.f : m) - kPBias;
+      float pg[PAGES];
+#pragma unroll
+      for (int c = 0; c < TOK / 32; ++c) {
+        float s[32];
+        uint32_t u[16];
+        tc::ld32(ts + 32 * c, s);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int j = 2 * c + hh, n = ntok_of(j);
+          const float fk = FMT == KVQ_FMT_TIERED ? f * ks[j] : f;
+          if (n != kPage)
+#pragma unroll
+            for (int k = 0; k < kPage; ++k) s[kPage * hh + k] = k < n ? s[kPage * hh + k] : -INFINITY;
+          float sum = 0.f, shift = mb;
+          float p[kPage];
+#pragma unroll
+          for (int k = 0; k < kPage; ++k) {
+            p[k] = ex2(fmaf(s[kPage * hh + k], fk, -mb));
+            sum += p[k];
+          }
+          l += sum;
+#pragma unroll
+          for (int k = 0; k < kPage; k += 2) u[(kPage * hh + k) / 2] = h2_as_u32(__floats2half2_rn(p[k], p[k + 1]));
+          if (a.page_lse) {
+            if (pm[j] - mb < -100.f && n > 0) {   // far below the row's maximum: the sum relative to the page's own
+              sum = 0.f;
+              shift = pm[j];
+#pragma unroll
+              for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(s[kPage * hh + k], fk, -shift));
+            }
+            pg[j] = n > 0 ? (__log2f(sum) + shift) * kLn2 : -INFINITY;
+          }
+        }
+        tc::st16(ts + 16 * c, u);
+      }
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[i & 1]);
+      if (lse_row) {
+        if (vec && pt + PAGES <= p1) {
+#pragma unroll
+          for (int j = 0; j < PAGES; j += 4)
+            *reinterpret_cast<float4*>(lse_row + pt + j) = make_float4(pg[j], pg[j + 1], pg[j + 2], pg[j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < PAGES; ++j)
+            if (pt + j < p1) lse_row[pt + j] = pg[j];
+        }
+      }
+    }
+    // the last two phases in turn: S of the last tile only says that the PV two tiles before it is done, and a
+    // parity wait may be at most one phase ahead
+    for (int i = max(n_tiles - 2, 0); i < n_tiles && ok; ++i)
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done, i & 1, kWaitLimitNs));
+    if (ok) {
+      tc::fence_after();
+      if (on) a.part_ml[part0 + tid] = make_float2(m == -INFINITY ? m : m - kPBias, l);
+      float* po = a.part_o + (part0 + tid) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        tc::ld32(t_o + lanes + 32 * c, o);
+        if (on)
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(po + 32 * c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+      }
+      tc::fence_before();
+    }
+  } else if (warp >= 4 && warp < 4 + kDequantWarps) {
+    // ------------------------------------------------------------------ dequantization
+    // 8 pages a tile: a warp takes one page, K then V; 4 pages (INT4): one page's K or V
+    const int wi = warp - 4, j = wi % PAGES;
+    const int role_lo = PAGES == kDequantWarps ? 0 : wi / PAGES, role_hi = PAGES == kDequantWarps ? 2 : role_lo + 1;
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      for (int role = role_lo; role < role_hi; ++role) {
+        const int seq = 2 * i + role, st = seq % RS;
+        ok = mbar_wait_bounded(&raw_full[st], (seq / RS) & 1, kWaitLimitNs);
+        uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
+        if (ok && i >= 2) ok = mbar_wait_bounded(empty, ((i >> 1) - 1) & 1, kWaitLimitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int32_t e = meta[(i & (kMeta - 1)) * PAGES + j];
+        const int ntok = e == kNoPage ? 0 : min(kPage, v.len - kPage * (p0 + i * PAGES + j));
+        const bool tier = FMT == KVQ_FMT_TIERED && e < 0;
+        const uint32_t stage = smem_u32(stages + st * P::kStage), blk = stage + j * SLOT;
+        const uint32_t cb = F::kGroup ? stage + (j / kGroupPages * kGroupPages) * SLOT : blk;
+        const uint32_t buf = smem_u32(smem) + (i & 1) * P::kBuf;
+        if (role == 0) {
+          const KTile<D, TOK> kt{buf, j}, lo{buf + (P::kPair ? 2 * P::kTile : 0), j};
+          if (FMT == KVQ_FMT_TIERED && lane == 0)
+            kscale[(i & (kMeta - 1)) * PAGES + j] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
+          if (ntok > 0) dequant_block<FMT, D, 0>(blk, cb, tree_block<FMT, D>(a, h, e, 0), tier, kt, lo, lane);
+        } else {
+          const VTile<D, TOK> vt{buf + P::kTile, j};
+          if (ntok > 0) dequant_block<FMT, D, 1>(blk, cb, tree_block<FMT, D>(a, h, e, 1), tier, vt, vt, lane);
+          if (ntok < kPage) {
+            __syncwarp();
+            zero_tokens<D>(vt, ntok, lane);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
+          mbar_arrive(&raw_empty[st]);
+        }
+      }
+    }
+  } else if (warp == 4 + kDequantWarps) {
+    // ------------------------------------------------------------------ producer
+    const int32_t* pt = a.page_table + (size_t)b * a.ppsm;
+    // the group format looks at the whole of a group that the bound on the length cuts
+    const int p_end = F::kGroup ? min((p1 + kGroupPages - 1) / kGroupPages * kGroupPages, a.ppsm) : p1;
+    auto entry = [&](int i) { return lane < PAGES && p0 + i * PAGES + lane < p_end ? pt[p0 + i * PAGES + lane] : 0; };
+    int32_t next = entry(0);
+    int issued = 0;
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      const int page = p0 + i * PAGES + lane;
+      const int32_t e = next;
+      next = entry(i + 1);
+      const uint32_t phys = (uint32_t)e & 0x7FFFFFFFu;
+      const bool tier = e < 0, mine = lane < PAGES && page < p_end;
+      bool good = mine && (tier ? (FMT == KVQ_FMT_TIERED && phys < (uint32_t)a.num_tier_pages) : phys < (uint32_t)a.num_pages);
+      if (mine && !good) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+      if (F::kGroup) {   // a group with a bad page is left out whole
+        const uint32_t all = __ballot_sync(0xffffffffu, good);
+        good = ((all >> (lane & ~3)) & 0xFu) == 0xFu;
+      }
+      uint32_t bytes = 0;
+      if (good)
+        bytes = tier                      ? (uint32_t)fetch_bytes<D>(kBlkFp8)
+                : F::kMain == kBlkCb2s    ? (uint32_t)(12 * D + 16 + 32 * a.n_static)
+                : F::kGroup               ? (uint32_t)((lane % kGroupPages ? 4 * D : 12 * D) + kOutPrefetch)
+                                          : (uint32_t)fetch_bytes<D>(F::kMain);
+      const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+      for (int role = 0; role < 2; ++role) {
+        const int seq = 2 * i + role, st = seq % RS;
+        if (seq >= RS && !__all_sync(0xffffffffu, mbar_wait_bounded(&raw_empty[st], (seq / RS - 1) & 1, kWaitLimitNs))) {
+          ok = false;
+          break;
+        }
+        if (role == 0 && lane < PAGES) meta[(i & (kMeta - 1)) * PAGES + lane] = good ? (tier ? e : (int32_t)phys) : kNoPage;
+        __syncwarp();
+        if (lane == 0) {
+          if (total) mbar_arrive_expect_tx(&raw_full[st], total);
+          else mbar_arrive(&raw_full[st]);
+        }
+        __syncwarp();
+        if (bytes) {
+          fence_proxy_async();
+          const int skip = F::kGroup && lane % kGroupPages ? 8 * D : 0;
+          bulk_g2s(stages + st * P::kStage + lane * SLOT + skip, tree_block<FMT, D>(a, h, e, role) + skip, bytes, &raw_full[st]);
+        }
+        ++issued;
+      }
+    }
+    if (!ok)   // let copies in flight land before the CTA can exit
+      for (int seq = max(issued - RS, 0); seq < issued; ++seq) mbar_wait_bounded(&raw_full[seq % RS], (seq / RS) & 1, kWaitLimitNs);
+  } else if (warp == 5 + kDequantWarps && lane == 0) {
+    // ------------------------------------------------------------------ MMA
+    constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);
+    const uint32_t base = smem_u32(smem);
+    auto scores = [&](int i) {
+      if (!mbar_wait_bounded(&k_full[i & 1], (i >> 1) & 1, kWaitLimitNs)) return false;
+      tc::fence_after();
+      const uint32_t kt = base + (i & 1) * P::kBuf;
+#pragma unroll
+      for (int half = 0; half < (P::kPair ? 2 : 1); ++half)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_ta(tmem + (i & 1) * 128, t_q + 8 * k,
+                     tc::desc_sw128(kt + half * 2 * P::kTile + (k >> 2) * (TOK * 128) + (k & 3) * 32), id_s, (half | k) != 0);
+      tc::commit(&s_full[i & 1]);
+      tc::commit(&k_empty[i & 1]);
+      return true;
+    };
+    ok = scores(0);
+    for (int i = 0; i < n_tiles && ok; ++i) {
+      if (i + 1 < n_tiles) ok = scores(i + 1);
+      ok = ok && mbar_wait_bounded(&p_full[i & 1], (i >> 1) & 1, kWaitLimitNs) &&
+           mbar_wait_bounded(&v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      if (!ok) break;
+      tc::fence_after();
+      const uint32_t vt = base + (i & 1) * P::kBuf + P::kTile;
+#pragma unroll
+      for (int k = 0; k < TOK / 16; ++k)
+        tc::mma_ta(t_o, tmem + (i & 1) * 128 + 8 * k, tc::desc_sw128(vt + (k >> 2) * (D * 128) + (k & 3) * 32), id_o, (i | k) != 0);
+      tc::commit(&v_empty[i & 1]);
+      tc::commit(o_done);
+    }
+    if (!ok) {   // tensor memory may be freed once what was issued is done
+      tc::commit(drain);
+      mbar_wait_bounded(drain, 0, kWaitLimitNs);
+    }
+  }
+  if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
+  __syncthreads();
+  if (warp == 4) {
+    tc::fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <int FMT, int D>
+static TreeKernel tree_kernel_info() {
+  return {reinterpret_cast<void*>(tree_cache_kernel<FMT, D>), (size_t)Plan<FMT, D>::kSmem, kThreads};
+}
+
+}  // namespace tree
+}  // namespace kvq

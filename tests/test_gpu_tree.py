@@ -285,3 +285,16 @@ def test_from_buffers_reads_the_same_cache():
         assert (same.cfg.num_pages, same.cfg.num_tier_pages) == (c.cfg.num_pages, c.cfg.num_tier_pages)
         q, k, v, _ = [x.cuda() if isinstance(x, torch.Tensor) else x for x in draft(1, 2, 4, 2, 8, 128)]
         assert torch.equal(*[kvq.kvq_tree_attention(x, q, 128 ** -0.5, 209, k, v) for x in (c, same)])
+
+
+def test_first_call_after_another_format():
+    """What an earlier kernel left in shared or tensor memory never shows: each format's
+    first call after another's gives the bits of its later ones."""
+    q, k, v, _ = [x.cuda() if isinstance(x, torch.Tensor) else x for x in draft(1, 2, 4, 2, 8, 128)]
+    pairs = [build(fmt, 128, [209, 77]) for fmt in ALL]
+    big = build(E2M1, 128, [250, 250], dist=("student_t4", 0, 1.0))
+    for pair in pairs:
+        for splits in (0, 1):
+            kvq.kvq_tree_attention(big.gpu, q * 3, 0.3, 250, v, k, num_splits=1)
+            outs = [kvq.kvq_tree_attention(pair.gpu, q, 128 ** -0.5, 209, k, v, num_splits=splits) for _ in range(3)]
+            assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
