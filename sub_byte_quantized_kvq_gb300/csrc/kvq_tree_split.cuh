@@ -292,11 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   uint8_t* stages = smem + 2 * P::kBuf;
   uint64_t* bars = reinterpret_cast<uint64_t*>(stages + RS * P::kStage);
   uint64_t *raw_full = bars, *raw_empty = raw_full + RS, *k_full = raw_empty + RS, *k_empty = k_full + 2, *v_full = k_empty + 2,
-           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 1;
-  int32_t* meta = reinterpret_cast<int32_t*>(drain + 1);                  // [kMeta][PAGES] page-table entry or kNoPage
+           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
+  int32_t* meta = reinterpret_cast<int32_t*>(done + 1);                  // [kMeta][PAGES] page-table entry or kNoPage
   float* kscale = reinterpret_cast<float*>(meta + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
   uint32_t* tslot = reinterpret_cast<uint32_t*>(kscale + kMeta * PAGES);
-  static_assert((2 * RS + 14) * 8 + 2 * kMeta * PAGES * 4 + 4 <= P::kMisc, "barriers and page records");
+  static_assert((2 * RS + 13) * 8 + 2 * kMeta * PAGES * 4 + 4 <= P::kMisc, "barriers and page records");
   const int n_sm = (rows + 31) / 32;   // softmax warps with rows
   if (tid == 0) {
     for (int i = 0; i < RS; ++i) {
@@ -311,8 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], n_sm);
     }
-    mbar_init(o_done, 1);
-    mbar_init(drain, 1);
+    mbar_init(done, 1);
     fence_mbar_init();
   }
   if (warp == 4) {
@@ -407,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         l *= alpha;
         m = need ? mx : m;
         if (i > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done, (i - 1) & 1, kWaitLimitNs));
+          // PV(i - 1) has to be done; PV(i - 3), this barrier's phase before, is (S(i - 1) was committed after it)
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, kWaitLimitNs));
           if (!ok) break;
           tc::fence_after();
 #pragma unroll
@@ -474,10 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         }
       }
     }
-    // the last two phases in turn: S of the last tile only says that the PV two tiles before it is done, and a
-    // parity wait may be at most one phase ahead
-    for (int i = max(n_tiles - 2, 0); i < n_tiles && ok; ++i)
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(o_done, i & 1, kWaitLimitNs));
+    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, kWaitLimitNs));
     if (ok) {
       tc::fence_after();
       if (on) a.part_ml[part0 + tid] = make_float2(m == -INFINITY ? m : m - kPBias, l);
@@ -612,12 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       for (int k = 0; k < TOK / 16; ++k)
         tc::mma_ta(t_o, tmem + (i & 1) * 128 + 8 * k, tc::desc_sw128(vt + (k >> 2) * (D * 128) + (k & 3) * 32), id_o, (i | k) != 0);
       tc::commit(&v_empty[i & 1]);
-      tc::commit(o_done);
     }
-    if (!ok) {   // tensor memory may be freed once what was issued is done
-      tc::commit(drain);
-      mbar_wait_bounded(drain, 0, kWaitLimitNs);
-    }
+    tc::commit(done);
+    if (!ok) mbar_wait_bounded(done, 0, kWaitLimitNs);   // tensor memory may be freed once what was issued is done
   }
   if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
   __syncthreads();

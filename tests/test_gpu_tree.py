@@ -298,3 +298,31 @@ def test_first_call_after_another_format():
             kvq.kvq_tree_attention(big.gpu, q * 3, 0.3, 250, v, k, num_splits=1)
             outs = [kvq.kvq_tree_attention(pair.gpu, q, 128 ** -0.5, 209, k, v, num_splits=splits) for _ in range(3)]
             assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("fmt", ALL, ids=NAMES)
+def test_no_wait_gives_up_over_many_tiles(fmt):
+    """Long splits of every format, few and many rows, repeated: no wait times out and
+    every call gives the same bits."""
+    D, Hkv, L = 128, 2, 6000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    P = L // 16 + 1
+    pt = torch.arange(2 * P).view(2, P)
+    tiers = torch.zeros((2, P), dtype=torch.bool)
+    if fmt == TIERED:
+        tiers[:, ::7] = True
+        pt = torch.where(tiers, (tiers.view(-1).cumsum(0) - 1).view(2, P) - (1 << 31), pt)
+    cache = kvq.QuantizedKVCache(fmt, 2, Hkv, D, P, 2 * P, int(tiers.sum()), page_table=pt, static_channels=2 if fmt == CB2S else 0)
+    k, v = [torch.randn((2, L, Hkv, D), generator=g, device="cuda") for _ in range(2)]
+    if fmt == CB2S:
+        kvq.kvq_select_static_channels(cache, k[0, :64].contiguous(), v[0, :64].contiguous())
+    kvq.kvq_quantize_append(cache, k, v)
+    for T, Hq in ((1, 2), (3, 16), (16, 16), (40, 16)):
+        q = torch.randn((2, T, Hq, D), generator=g, device="cuda").to(torch.bfloat16)
+        ws = kvq.alloc_tree_workspace(cache, Hq, T, L, 3)
+        first = kvq.kvq_tree_attention(cache, q, D ** -0.5, L, num_splits=1, workspace=ws)
+        for splits in (1, 1, 1, 2, 3):
+            out = kvq.kvq_tree_attention(cache, q, D ** -0.5, L, num_splits=splits, workspace=ws)
+            if splits == 1:
+                assert torch.equal(out, first)
+    assert cache.status_word() == 0
