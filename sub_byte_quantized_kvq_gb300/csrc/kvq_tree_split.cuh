@@ -36,8 +36,12 @@ namespace kvq {
 namespace tree {
 
 constexpr int kM = kTreeRows;
-constexpr int kDequantWarps = 8;
-constexpr int kThreads = 32 * (4 + kDequantWarps + 2);
+constexpr int kDequantWarps = 16;
+constexpr int kThreads = 32 * (4 + kDequantWarps + 4);
+// Registers a thread: the launch has 80 each; the softmax warps take what the others give up.
+constexpr int kRegsLaunch = 80, kRegsSoftmax = 144, kRegsDequant = 72, kRegsRest = 48;
+static_assert(4 * kRegsSoftmax + kDequantWarps * kRegsDequant + 4 * kRegsRest <= (kThreads / 32) * kRegsLaunch,
+              "setmaxnreg shares exceed what the launch has");
 constexpr int kMeta = 8;                // tiles whose page records are kept (producer to softmax: at most 7 apart)
 constexpr float kPBias = 6.f;           // p <= 2^(kRescaleTh + kPBias) stays in fp16 range
 
@@ -52,7 +56,7 @@ struct Plan {
   // a page's slot: its (virtual) block from offset 0; the group format keeps the codebook in the first page's
   static constexpr int kSlot = F::kGroup ? 12 * D + kOutPrefetch : half_slot_bytes<FMT, D>();
   static constexpr int kStage = kPages * kSlot;
-  static constexpr int kMisc = 1024;                         // barriers and page records
+  static constexpr int kMisc = 1152;                         // barriers and page records
   static constexpr int kFit = (227 * 1024 - 1024 - 2 * kBuf - kMisc) / kStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kSmem = 1024 + 2 * kBuf + kStages * kStage + kMisc;   // 1024: alignment slack
@@ -139,10 +143,13 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const u
   const uint32_t row = tile.lane_row(lane);
   if (FMT == KVQ_FMT_TIERED && tier) {
     const float sc = ROLE == 1 ? ldsf(blk + fp8_sc_off(D)) : 1.f;
+    uint2 w[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) w[s] = lds64(blk + 8 * NS * lane + 8 * s);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       uint32_t x[4];
-      fp8_frag(lds64(blk + 8 * NS * lane + 8 * s), x);
+      fp8_frag(w[s], x);
       if (ROLE == 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -158,23 +165,28 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const u
     const uint32_t lrow = low.lane_row(lane);
     uint32_t w[NS];
     load_e2m1_words<D>(blk, lane, w);   // one u32 of nibbles per step, as E2M1
+    constexpr int NZ = ROLE == 0 ? 2 : 4;   // tokens whose scale and minimum the lane needs
+    uint32_t z[NG][NZ];
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+      for (int i = 0; i < NZ; ++i) {
+        const int t = ROLE == 0 ? g + 8 * i : 2 * q4 + (i & 1) + 8 * (i >> 1);
+        z[gr][i] = lds32(blk + int4_sz_off(D) + 4 * (t * NG + gr));
+      }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       uint32_t hi[4], lo[4];
-      if (ROLE == 0) {
-        const uint32_t z0 = lds32(blk + int4_sz_off(D) + 4 * (g * NG + (s >> 1)));
-        const uint32_t z1 = lds32(blk + int4_sz_off(D) + 4 * ((g + 8) * NG + (s >> 1)));
-        int4_k_frag(w[s], fp16_bits_to_float(z0), fp16_bits_to_float(z0 >> 16), fp16_bits_to_float(z1),
-                    fp16_bits_to_float(z1 >> 16), hi, lo);
+      float S[NZ], M[NZ];
+#pragma unroll
+      for (int i = 0; i < NZ; ++i) {
+        S[i] = fp16_bits_to_float(z[s >> 1][i]);
+        M[i] = fp16_bits_to_float(z[s >> 1][i] >> 16);
+      }
+      if constexpr (ROLE == 0) {
+        int4_k_frag(w[s], S[0], M[0], S[1], M[1], hi, lo);
         stmatrix4(low.step(lrow, lane, s), lo);
       } else {
-        float S[4], M[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t z = lds32(blk + int4_sz_off(D) + 4 * ((2 * q4 + (i & 1) + 8 * (i >> 1)) * NG + (s >> 1)));
-          S[i] = fp16_bits_to_float(z);
-          M[i] = fp16_bits_to_float(z >> 16);
-        }
         int4_v_frag(w[s], S, M, hi, lo);
       }
       stmatrix4(tile.step(row, lane, s), hi);
@@ -189,22 +201,31 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const u
       }
     }
   } else if constexpr (BLK == kBlkE2m1) {
-    uint32_t w[NS];
+    uint32_t w[NS], sc[NS][ROLE == 0 ? 1 : 2];
     load_e2m1_words<D>(blk, lane, w);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const uint32_t at = blk + e2m1_sc_off(D) + 16 * s;
+      if constexpr (ROLE == 0) {   // tokens g (registers 0, 2) and g + 8
+        sc[s][0] = lds8(at + g) | (lds8(at + g + 8) << 8);
+      } else {                     // tokens 2q, 2q + 1 (registers 0, 1) and + 8
+        sc[s][0] = lds16(at + 2 * q4);
+        sc[s][1] = lds16(at + 2 * q4 + 8);
+      }
+    }
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       uint32_t x[4];
       e2m1_frag(w[s], x);
-      const uint32_t sc = blk + e2m1_sc_off(D) + 16 * s;
-      if (ROLE == 0) {   // tokens g (registers 0, 2) and g + 8
-        const __half2 sh = u32_as_h2(e4m3x2_to_f16x2(lds8(sc + g) | (lds8(sc + g + 8) << 8)));
+      if constexpr (ROLE == 0) {
+        const __half2 sh = u32_as_h2(e4m3x2_to_f16x2(sc[s][0]));
         const __half2 s0 = __low2half2(sh), s1 = __high2half2(sh);
         x[0] = h2_as_u32(__hmul2(u32_as_h2(x[0]), s0));
         x[1] = h2_as_u32(__hmul2(u32_as_h2(x[1]), s1));
         x[2] = h2_as_u32(__hmul2(u32_as_h2(x[2]), s0));
         x[3] = h2_as_u32(__hmul2(u32_as_h2(x[3]), s1));
-      } else {           // tokens 2q, 2q + 1 (registers 0, 1) and + 8
-        const uint32_t s01 = e4m3x2_to_f16x2(lds16(sc + 2 * q4)), s23 = e4m3x2_to_f16x2(lds16(sc + 2 * q4 + 8));
+      } else {
+        const uint32_t s01 = e4m3x2_to_f16x2(sc[s][0]), s23 = e4m3x2_to_f16x2(sc[s][1]);
         x[0] = hmul2u(x[0], s01);
         x[1] = hmul2u(x[1], s01);
         x[2] = hmul2u(x[2], s23);
@@ -228,13 +249,24 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const u
     const uint32_t book = cb + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
     uint32_t w[D / 32];
     load_codes<D>(blk + (F::kGroup ? cb2g_code_off(D) : 0), lane, w);
+    // four steps' codebook columns at a time, so that their loads overlap
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      uint32_t x[4];
-      const uint32_t w16 = (s & 1) ? w[s >> 1] >> 16 : w[s >> 1];
-      if (ROLE == 0) cb2_k_frag(book, w16, s, x);
-      else cb2_v_frag(book, w16, s, x);
-      stmatrix4(tile.step(row, lane, s), x);
+    for (int s0 = 0; s0 < NS; s0 += 4) {
+      KCols kc[ROLE == 0 ? 4 : 1];
+      uint4 vc[ROLE == 0 ? 1 : 4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if constexpr (ROLE == 0) kc[k] = cb2_k_cols(book, s0 + k);
+        else vc[k] = cb2_v_cols(book, s0 + k);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int s = s0 + k;
+        uint32_t x[4];
+        const uint32_t w16 = (s & 1) ? w[s >> 1] >> 16 : w[s >> 1];
+        if constexpr (ROLE == 0) cb2_k_expand(kc[k], w16, x);
+        else cb2_v_expand(vc[k], w16, x);
+        stmatrix4(tile.step(row, lane, s), x);
+      }
     }
     __syncwarp();
     if constexpr (BLK == kBlkCb2s) {   // the static channels' fp16 values
@@ -263,6 +295,129 @@ __device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, i
     for (int p = p_lo + (int)(threadIdx.x & 31); p < p_hi; p += 32) row[p] = -INFINITY;
   }
 }
+
+// A softmax thread's row: m in log2 units, p = 2^(s f - m + kPBias), l the fp32 sum of p.
+template <int FMT, int D>
+struct SoftmaxRow {
+  float m = -INFINITY, l = 0.f, f;
+  float* lse_row;
+  bool vec;
+
+  // NC chunks of 32 columns (two pages) of S at ts, from chunk c0 on, in one
+  // pass: the chunk's maximum, p, P over S's columns.  A chunk that raises m
+  // by more than kRescaleTh (rare after the first) scales what is there: O
+  // (once o_free says that the MMAs are done with it) and the tile's earlier P.
+  template <int NC, class OFree>
+  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c0, const int32_t* ntok, const float* ks, int pt, int p1,
+                                       bool has_o, OFree&& o_free) {
+    uint32_t s[NC > 1 ? 2 : 1][32];
+    float pg[2 * NC];
+    tc::ld32_issue(ts + 32 * c0, s[0]);
+#pragma unroll
+    for (int cc = 0; cc < NC; ++cc) {
+      uint32_t(&x)[32] = s[cc & 1];
+      const int c = c0 + cc, n0 = ntok[2 * c], n1 = ntok[2 * c + 1];
+      tc::wait_ld(x);
+      if (cc + 1 < NC) tc::ld32_issue(ts + 32 * (c + 1), s[(cc + 1) & 1]);
+      if (n0 != kPage || n1 != kPage) {   // absent tokens
+#pragma unroll
+        for (int k = 0; k < kPage; ++k) {
+          x[k] = k < n0 ? x[k] : 0xFF800000u;
+          x[kPage + k] = k < n1 ? x[kPage + k] : 0xFF800000u;
+        }
+      }
+      const float f0 = FMT == KVQ_FMT_TIERED ? f * ks[2 * c] : f, f1 = FMT == KVQ_FMT_TIERED ? f * ks[2 * c + 1] : f;
+      float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[kPage]);
+#pragma unroll
+      for (int k = 1; k < kPage; ++k) {
+        mx0 = fmaxf(mx0, __uint_as_float(x[k]));
+        mx1 = fmaxf(mx1, __uint_as_float(x[kPage + k]));
+      }
+      const float pm0 = mx0 * f0, pm1 = mx1 * f1, mx = fmaxf(pm0, pm1);
+      const bool need = mx > m + kRescaleTh;
+      if (__any_sync(0xffffffffu, need)) {
+        const float alpha = need ? ex2(m - mx) : 1.f;
+        l *= alpha;
+        m = need ? mx : m;
+        if (has_o) {
+          if (!o_free()) return false;
+          tc::fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) scale_columns(to + 32 * k, alpha);
+        }
+#pragma unroll 1
+        for (int k = 0; k < cc; ++k) scale_p(ts + 16 * (c0 + k), alpha);
+        tc::wait_st();
+      }
+      const float mb = (m == -INFINITY ? 0.f : m) - kPBias;
+      uint32_t u[16];
+      float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < kPage; k += 2) {
+        const float p0 = ex2(fmaf(__uint_as_float(x[k]), f0, -mb)), q0 = ex2(fmaf(__uint_as_float(x[k + 1]), f0, -mb));
+        const float p1_ = ex2(fmaf(__uint_as_float(x[kPage + k]), f1, -mb)),
+                    q1 = ex2(fmaf(__uint_as_float(x[kPage + k + 1]), f1, -mb));
+        u[k / 2] = h2_as_u32(__floats2half2_rn(p0, q0));
+        u[8 + k / 2] = h2_as_u32(__floats2half2_rn(p1_, q1));
+        a0 += p0;
+        b0 += q0;
+        a1 += p1_;
+        b1 += q1;
+      }
+      a0 += b0;
+      a1 += b1;
+      l += a0 + a1;
+      tc::st16(ts + 16 * c, u);
+      if (lse_row) {
+        pg[2 * cc] = page_sum(x, 0, n0, f0, pm0, mb, a0);
+        pg[2 * cc + 1] = page_sum(x, kPage, n1, f1, pm1, mb, a1);
+      }
+    }
+    if (lse_row) {
+      float* o = lse_row + pt + 2 * c0;
+      if (vec && NC > 1 && pt + 2 * (c0 + NC) <= p1) {
+#pragma unroll
+        for (int j = 0; j < 2 * NC; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(pg[j], pg[j + 1], pg[j + 2], pg[j + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2 * NC; ++j)
+          if (pt + 2 * c0 + j < p1) o[j] = pg[j];
+      }
+    }
+    return true;
+  }
+
+  // ln of a page's sum, given sum = sum 2^(s f - mb); where the page lies so far
+  // below the row's maximum that its terms vanish, the sum relative to its own.
+  __device__ __forceinline__ float page_sum(const uint32_t (&x)[32], int at, int n, float fk, float pm, float mb, float sum) const {
+    float shift = mb;
+    if (pm - mb < -100.f && n > 0) {
+      sum = 0.f;
+      shift = pm;
+#pragma unroll
+      for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(__uint_as_float(x[at + k]), fk, -pm));
+    }
+    return n > 0 ? (__log2f(sum) + shift) * kLn2 : -INFINITY;
+  }
+  static __device__ __forceinline__ void scale_columns(uint32_t t, float alpha) {
+    uint32_t o[32];
+    tc::ld32_issue(t, o);
+    tc::wait_ld(o);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+    tc::st32(t, o);
+  }
+  static __device__ __forceinline__ void scale_p(uint32_t t, float alpha) {   // 16 columns of fp16 pairs
+    uint32_t r[16];
+    tc::ld16(t, r);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 v = __half22float2(u32_as_h2(r[k]));
+      r[k] = h2_as_u32(__floats2half2_rn(v.x * alpha, v.y * alpha));
+    }
+    tc::st16(t, r);
+  }
+};
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs a) {
@@ -294,10 +449,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   uint64_t *raw_full = bars, *raw_empty = raw_full + RS, *k_full = raw_empty + RS, *k_empty = k_full + 2, *v_full = k_empty + 2,
            *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
   int32_t* meta = reinterpret_cast<int32_t*>(done + 1);                  // [kMeta][PAGES] page-table entry or kNoPage
-  float* kscale = reinterpret_cast<float*>(meta + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
+  int32_t* ntok = meta + kMeta * PAGES;                                   // [kMeta][PAGES] its tokens
+  float* kscale = reinterpret_cast<float*>(ntok + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
   uint32_t* tslot = reinterpret_cast<uint32_t*>(kscale + kMeta * PAGES);
-  static_assert((2 * RS + 13) * 8 + 2 * kMeta * PAGES * 4 + 4 <= P::kMisc, "barriers and page records");
-  const int n_sm = (rows + 31) / 32;   // softmax warps with rows
+  static_assert((2 * RS + 13) * 8 + 3 * kMeta * PAGES * 4 + 4 <= P::kMisc, "barriers and page records");
+  // Few rows: the 128 tensor-memory lanes hold `rep` copies of them, and each copy's warps take their share of a
+  // tile's columns (P = 0 in the others), so that the softmax of a tile takes a rep-th of the time.
+  const int rep = rows <= 32 && TOK == 128 ? 4 : rows <= 64 ? 2 : 1, row = tid % (kM / rep);
+  const int n_sm = rep > 1 ? 4 : (rows + 31) / 32;   // softmax warps with rows
   if (tid == 0) {
     for (int i = 0; i < RS; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -328,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   // ---- each softmax thread's query row into tensor memory
   float f = 0.f;
   if (warp < n_sm) {
-    const int r = r0 + tid;
-    const bool on = tid < rows;
+    const int r = r0 + row;
+    const bool on = row < rows;
     const __nv_bfloat16* qr = a.q + (((size_t)b * a.T + (on ? r / a.G : 0)) * a.Hq + (size_t)h * a.G + (on ? r % a.G : 0)) * D;
     float mx = 0.f;
     for (int i = 0; i < D / 8; ++i) {
@@ -364,138 +523,93 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   __syncthreads();
   tc::fence_after();
 
-  if (warp < n_sm) {
+  if (warp < 4) {
     // ------------------------------------------------------------------ softmax
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const bool on = tid < rows;
-    float* lse_row = a.page_lse && on ? page_lse_row(a, b, h, r0 + tid) : nullptr;
-    const bool vec = a.page_lse && (a.P & 3) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 15) == 0;
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < n_tiles; ++i) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, kWaitLimitNs));
-      if (!ok) break;
-      tc::fence_after();
-      const uint32_t ts = tmem + lanes + (i & 1) * 128;
-      const int32_t* ent = meta + (i & (kMeta - 1)) * PAGES;
-      const float* ks = kscale + (i & (kMeta - 1)) * PAGES;
-      const int pt = p0 + i * PAGES;
-      auto ntok_of = [&](int j) { return ent[j] == kNoPage ? 0 : min(kPage, v.len - kPage * (pt + j)); };
-      float pm[PAGES], mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < TOK / 32; ++c) {
-        float s[32];
-        tc::ld32(ts + 32 * c, s);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int j = 2 * c + hh, n = ntok_of(j);
-          float x = -INFINITY;
-          if (n == kPage) {
-#pragma unroll
-            for (int k = 0; k < kPage; ++k) x = fmaxf(x, s[kPage * hh + k]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < kPage; ++k) x = k < n ? fmaxf(x, s[kPage * hh + k]) : x;
-          }
-          pm[j] = x * (FMT == KVQ_FMT_TIERED ? f * ks[j] : f);
-          mx = fmaxf(mx, pm[j]);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    if (warp < n_sm) {
+      const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+      SoftmaxRow<FMT, D> sr;
+      sr.f = f;
+      sr.lse_row = a.page_lse && row < rows ? page_lse_row(a, b, h, r0 + row) : nullptr;
+      sr.vec = a.page_lse && (a.P & 3) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 15) == 0;
+      const int chunks = TOK / 32 / rep, c0 = warp / (4 / rep) * chunks;   // this warp's 32-column chunks
+      for (int i = 0; i < n_tiles; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, kWaitLimitNs));
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t ts = tmem + lanes + (i & 1) * 128;
+        const int slot = (i & (kMeta - 1)) * PAGES, pt = p0 + i * PAGES;
+        // PV(i - 1) has to be done before O changes; PV(i - 3), that barrier's phase before, is (S(i - 1) was committed after it)
+        auto o_free = [&]() {
+          return i == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, kWaitLimitNs));
+        };
+        if (TOK == 128 && rep == 1) ok = sr.template tile<4>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        else if (TOK / 32 / rep == 2) ok = sr.template tile<2>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        else ok = sr.template tile<1>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        if (!ok) break;
+        if (rep > 1) {   // the columns of the row's other copies: P = 0
+          const uint32_t z[16] = {};
+          for (int c = 0; c < TOK / 32; ++c)
+            if (c < c0 || c >= c0 + chunks) tc::st16(ts + 16 * c, z);
         }
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i & 1]);
       }
-      const bool need = mx > m + kRescaleTh;
-      if (__any_sync(0xffffffffu, need)) {
-        const float alpha = need ? ex2(m - mx) : 1.f;
-        l *= alpha;
-        m = need ? mx : m;
-        if (i > 0) {
-          // PV(i - 1) has to be done; PV(i - 3), this barrier's phase before, is (S(i - 1) was committed after it)
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, kWaitLimitNs));
-          if (!ok) break;
-          tc::fence_after();
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, kWaitLimitNs));
+      // ---- the partial state, through shared memory (the tiles are done): copies of a row are joined, rows stored whole
+      constexpr int XS = D + 4;
+      float* xo = reinterpret_cast<float*>(smem);                       // [128][XS], thread's row of O
+      float2* xml = reinterpret_cast<float2*>(smem + kM * XS * 4);      // [128]
+      static_assert(kM * XS * 4 + kM * 8 <= 2 * P::kBuf, "partial state fits over the tiles");
+      const int n_thr = 32 * n_sm;
+      if (ok) {
+        tc::fence_after();
+        xml[tid] = make_float2(sr.m == -INFINITY ? -INFINITY : sr.m - kPBias, sr.l);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            uint32_t u[32];
-            tc::ld32(t_o + lanes + 32 * c, o);
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tc::ld32(t_o + lanes + 32 * c, o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * alpha);
-            tc::st32(t_o + lanes + 32 * c, u);
-          }
-          tc::wait_st();
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(xo + tid * XS + 32 * c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
+        tc::fence_before();
       }
-      const float mb = (m == -INFINITY ? 0.f : m) - kPBias;
-      float pg[PAGES];
-#pragma unroll
-      for (int c = 0; c < TOK / 32; ++c) {
-        float s[32];
-        uint32_t u[16];
-        tc::ld32(ts + 32 * c, s);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int j = 2 * c + hh, n = ntok_of(j);
-          const float fk = FMT == KVQ_FMT_TIERED ? f * ks[j] : f;
-          if (n != kPage)
-#pragma unroll
-            for (int k = 0; k < kPage; ++k) s[kPage * hh + k] = k < n ? s[kPage * hh + k] : -INFINITY;
-          float sum = 0.f, shift = mb;
-          float p[kPage];
-#pragma unroll
-          for (int k = 0; k < kPage; ++k) {
-            p[k] = ex2(fmaf(s[kPage * hh + k], fk, -mb));
-            sum += p[k];
-          }
-          l += sum;
-#pragma unroll
-          for (int k = 0; k < kPage; k += 2) u[(kPage * hh + k) / 2] = h2_as_u32(__floats2half2_rn(p[k], p[k + 1]));
-          if (a.page_lse) {
-            if (pm[j] - mb < -100.f && n > 0) {   // far below the row's maximum: the sum relative to the page's own
-              sum = 0.f;
-              shift = pm[j];
-#pragma unroll
-              for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(s[kPage * hh + k], fk, -shift));
+      asm volatile("bar.sync 1, %0;" ::"r"(n_thr) : "memory");
+      if (ok) {
+        const int per = kM / rep;   // threads of one copy
+        for (int r = warp; r < rows; r += n_sm) {
+          float M = -INFINITY, L = 0.f;
+          for (int c = 0; c < rep; ++c) M = fmaxf(M, xml[c * per + r].x);
+          float4 o;
+          const bool mine = 4 * lane < D;
+          o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = 0; c < rep; ++c) {
+            const float2 ml = xml[c * per + r];
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            L = fmaf(w, ml.y, L);
+            if (mine && ml.x != -INFINITY) {
+              const float4 x = *reinterpret_cast<const float4*>(xo + (c * per + r) * XS + 4 * lane);
+              o.x = fmaf(w, x.x, o.x);
+              o.y = fmaf(w, x.y, o.y);
+              o.z = fmaf(w, x.z, o.z);
+              o.w = fmaf(w, x.w, o.w);
             }
-            pg[j] = n > 0 ? (__log2f(sum) + shift) * kLn2 : -INFINITY;
           }
-        }
-        tc::st16(ts + 16 * c, u);
-      }
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i & 1]);
-      if (lse_row) {
-        if (vec && pt + PAGES <= p1) {
-#pragma unroll
-          for (int j = 0; j < PAGES; j += 4)
-            *reinterpret_cast<float4*>(lse_row + pt + j) = make_float4(pg[j], pg[j + 1], pg[j + 2], pg[j + 3]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < PAGES; ++j)
-            if (pt + j < p1) lse_row[pt + j] = pg[j];
+          if (mine) *reinterpret_cast<float4*>(a.part_o + (part0 + r) * D + 4 * lane) = o;
+          if (lane == 0) a.part_ml[part0 + r] = make_float2(M, L);
         }
       }
-    }
-    ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, kWaitLimitNs));
-    if (ok) {
-      tc::fence_after();
-      if (on) a.part_ml[part0 + tid] = make_float2(m == -INFINITY ? m : m - kPBias, l);
-      float* po = a.part_o + (part0 + tid) * D;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        tc::ld32(t_o + lanes + 32 * c, o);
-        if (on)
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) *reinterpret_cast<float4*>(po + 32 * c + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-      }
-      tc::fence_before();
     }
   } else if (warp >= 4 && warp < 4 + kDequantWarps) {
     // ------------------------------------------------------------------ dequantization
-    // 8 pages a tile: a warp takes one page, K then V; 4 pages (INT4): one page's K or V
-    const int wi = warp - 4, j = wi % PAGES;
-    const int role_lo = PAGES == kDequantWarps ? 0 : wi / PAGES, role_hi = PAGES == kDequantWarps ? 2 : role_lo + 1;
-    for (int i = 0; i < n_tiles && ok; ++i) {
-      for (int role = role_lo; role < role_hi; ++role) {
+    // a warp takes one page's K or V; with 4 pages a tile (INT4) of every other tile
+    constexpr int kTasks = 2 * PAGES, kTurns = kDequantWarps / kTasks;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
+    const int wi = warp - 4, j = wi % PAGES, role = wi / PAGES % 2;
+    for (int i = wi / kTasks; i < n_tiles && ok; i += kTurns) {
         const int seq = 2 * i + role, st = seq % RS;
         ok = mbar_wait_bounded(&raw_full[st], (seq / RS) & 1, kWaitLimitNs);
         uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
@@ -503,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const int32_t e = meta[(i & (kMeta - 1)) * PAGES + j];
-        const int ntok = e == kNoPage ? 0 : min(kPage, v.len - kPage * (p0 + i * PAGES + j));
+        const int n = ntok[(i & (kMeta - 1)) * PAGES + j];
         const bool tier = FMT == KVQ_FMT_TIERED && e < 0;
         const uint32_t stage = smem_u32(stages + st * P::kStage), blk = stage + j * SLOT;
         const uint32_t cb = F::kGroup ? stage + (j / kGroupPages * kGroupPages) * SLOT : blk;
@@ -512,13 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           const KTile<D, TOK> kt{buf, j}, lo{buf + (P::kPair ? 2 * P::kTile : 0), j};
           if (FMT == KVQ_FMT_TIERED && lane == 0)
             kscale[(i & (kMeta - 1)) * PAGES + j] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
-          if (ntok > 0) dequant_block<FMT, D, 0>(blk, cb, tree_block<FMT, D>(a, h, e, 0), tier, kt, lo, lane);
+          if (n > 0) dequant_block<FMT, D, 0>(blk, cb, tree_block<FMT, D>(a, h, e, 0), tier, kt, lo, lane);
         } else {
           const VTile<D, TOK> vt{buf + P::kTile, j};
-          if (ntok > 0) dequant_block<FMT, D, 1>(blk, cb, tree_block<FMT, D>(a, h, e, 1), tier, vt, vt, lane);
-          if (ntok < kPage) {
+          if (n > 0) dequant_block<FMT, D, 1>(blk, cb, tree_block<FMT, D>(a, h, e, 1), tier, vt, vt, lane);
+          if (n < kPage) {
             __syncwarp();
-            zero_tokens<D>(vt, ntok, lane);
+            zero_tokens<D>(vt, n, lane);
           }
         }
         fence_proxy_async();
@@ -527,9 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
           mbar_arrive(&raw_empty[st]);
         }
-      }
     }
-  } else if (warp == 4 + kDequantWarps) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 4 + kDequantWarps) {
     // ------------------------------------------------------------------ producer
     const int32_t* pt = a.page_table + (size_t)b * a.ppsm;
     // the group format looks at the whole of a group that the bound on the length cuts
@@ -562,7 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           ok = false;
           break;
         }
-        if (role == 0 && lane < PAGES) meta[(i & (kMeta - 1)) * PAGES + lane] = good ? (tier ? e : (int32_t)phys) : kNoPage;
+        if (role == 0 && lane < PAGES) {
+          meta[(i & (kMeta - 1)) * PAGES + lane] = good ? (tier ? e : (int32_t)phys) : kNoPage;
+          ntok[(i & (kMeta - 1)) * PAGES + lane] = good ? max(min(kPage, v.len - kPage * page), 0) : 0;
+        }
         __syncwarp();
         if (lane == 0) {
           if (total) mbar_arrive_expect_tx(&raw_full[st], total);
@@ -579,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     }
     if (!ok)   // let copies in flight land before the CTA can exit
       for (int seq = max(issued - RS, 0); seq < issued; ++seq) mbar_wait_bounded(&raw_full[seq % RS], (seq / RS) & 1, kWaitLimitNs);
-  } else if (warp == 5 + kDequantWarps && lane == 0) {
+    } else if (warp == 5 + kDequantWarps && lane == 0) {
     // ------------------------------------------------------------------ MMA
     constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);
     const uint32_t base = smem_u32(smem);
@@ -612,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     }
     tc::commit(done);
     if (!ok) mbar_wait_bounded(done, 0, kWaitLimitNs);   // tensor memory may be freed once what was issued is done
+    }
   }
   if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
   __syncthreads();
