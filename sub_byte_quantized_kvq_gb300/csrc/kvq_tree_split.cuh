@@ -4,9 +4,11 @@
 // rows (node, head of the group) x kTok tokens costs two MMAs, S = Q K^T and
 // O += P V, and each page's codes are expanded once for all of the rows:
 //
-//   producer warp   one bulk asynchronous copy per block into a ring of stages
-//                   (a stage: the K or the V blocks of one tile's pages)
-//   8 dequant warps codes -> fp16 tiles in shared memory, K as [token][channel],
+//   16 dequant warps  each takes one page's K or V of every tile: its own ring of
+//                   bulk asynchronous copies (a single warp issues one copy
+//                   every 90 ns whatever its size, measured, so one producer
+//                   for all would cap the SM at 10-20 bytes a cycle), then
+//                   codes -> fp16 tiles in shared memory, K as [token][channel],
 //                   V transposed as [channel][token], both K-major with 128-byte
 //                   swizzle; the block layout holds mma fragments, which
 //                   stmatrix turns into rows; outliers are stored over their slots
@@ -42,7 +44,8 @@ constexpr int kThreads = 32 * (4 + kDequantWarps + 4);
 constexpr int kRegsLaunch = 80, kRegsSoftmax = 144, kRegsDequant = 72, kRegsRest = 48;
 static_assert(4 * kRegsSoftmax + kDequantWarps * kRegsDequant + 4 * kRegsRest <= (kThreads / 32) * kRegsLaunch,
               "setmaxnreg shares exceed what the launch has");
-constexpr int kMeta = 8;                // tiles whose page records are kept (producer to softmax: at most 7 apart)
+constexpr int kMeta = 4;                // tiles whose page records are kept: K(i) is written once S(i - 2) is done, whose
+                                        // MMAs were issued after the softmax of tile i - 4
 constexpr float kPBias = 6.f;           // p <= 2^(kRescaleTh + kPBias) stays in fp16 range
 
 template <int FMT, int D>
@@ -53,14 +56,20 @@ struct Plan {
   static constexpr int kPages = kTok / kPage;
   static constexpr int kTile = kTok * D * 2;                 // bytes of an fp16 tile
   static constexpr int kBuf = (kPair ? 3 : 2) * kTile;       // one buffer: K [, K low], V
-  // a page's slot: its (virtual) block from offset 0; the group format keeps the codebook in the first page's
+  // a page's slot: its (virtual) block from offset 0 (the group format copies the group's codebook into each)
   static constexpr int kSlot = F::kGroup ? 12 * D + kOutPrefetch : half_slot_bytes<FMT, D>();
-  static constexpr int kStage = kPages * kSlot;
-  static constexpr int kMisc = 1152;                         // barriers and page records
-  static constexpr int kFit = (227 * 1024 - 1024 - 2 * kBuf - kMisc) / kStage;
-  static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr int kSmem = 1024 + 2 * kBuf + kStages * kStage + kMisc;   // 1024: alignment slack
-  static_assert(kStages >= 2 && kStage % 16 == 0 && kTile % 1024 == 0, "tree attention plan");
+  static constexpr int misc(int depth) { return 8 * (kDequantWarps * depth + 13) + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8; }
+  static constexpr int smem(int depth) {   // 1024: alignment slack
+    return 1024 + 2 * kBuf + kDequantWarps * depth * kSlot + misc(depth);
+  }
+  static constexpr int fit() {
+    int d = 6;
+    while (d > 1 && smem(d) > 227 * 1024) --d;
+    return d;
+  }
+  static constexpr int kDepth = fit();                       // slots of a warp's copy ring
+  static constexpr int kSmem = smem(kDepth);
+  static_assert(kDepth >= 2 && kSlot % 16 == 0 && kTile % 1024 == 0, "tree attention plan");
 };
 
 __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
@@ -130,12 +139,12 @@ __device__ __forceinline__ void zero_tokens(const Tile& tile, int ntok, int lane
 }
 
 // One K block (role 0) or V block (role 1) -> its place in the fp16 tile.
-//   blk    shared address of the page's slot, cb of the slot that holds its codebook
+//   blk    shared address of the page's slot
 //   gblk   the block in global memory (side-list records past the prefetch)
 //   tier   the block is an FP8 block
 // K of an FP8 block is left unscaled (its page's scale is applied to the scores).
 template <int FMT, int D, int ROLE, class Tile>
-__device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const uint8_t* gblk, bool tier, const Tile& tile,
+__device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk, bool tier, const Tile& tile,
                                               const Tile& low, int lane) {
   using F = Fmt<FMT>;
   constexpr int NS = D / 16, BLK = F::kMain;
@@ -246,7 +255,7 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, uint32_t cb, const u
     __syncwarp();
     patch_side_list<D, BLK>(blk + a3_out_off(D), gblk + a3_out_off(D), tile, lane);
   } else {   // 2-bit codebooks
-    const uint32_t book = cb + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
+    const uint32_t book = blk + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
     uint32_t w[D / 32];
     load_codes<D>(blk + (F::kGroup ? cb2g_code_off(D) : 0), lane, w);
     // four steps' codebook columns at a time, so that their loads overlap
@@ -423,7 +432,7 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs a) {
   using F = Fmt<FMT>;
   using P = Plan<FMT, D>;
-  constexpr int TOK = P::kTok, PAGES = P::kPages, RS = P::kStages, SLOT = P::kSlot;
+  constexpr int TOK = P::kTok, PAGES = P::kPages, DEPTH = P::kDepth, SLOT = P::kSlot;
   extern __shared__ uint8_t raw_smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nmt = (a.R + kM - 1) / kM;
@@ -444,24 +453,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   }
 
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
-  uint8_t* stages = smem + 2 * P::kBuf;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stages + RS * P::kStage);
-  uint64_t *raw_full = bars, *raw_empty = raw_full + RS, *k_full = raw_empty + RS, *k_empty = k_full + 2, *v_full = k_empty + 2,
-           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
-  int32_t* meta = reinterpret_cast<int32_t*>(done + 1);                  // [kMeta][PAGES] page-table entry or kNoPage
-  int32_t* ntok = meta + kMeta * PAGES;                                   // [kMeta][PAGES] its tokens
+  uint8_t* slots = smem + 2 * P::kBuf;                                    // [kDequantWarps][DEPTH]
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(slots + kDequantWarps * DEPTH * SLOT);   // [kDequantWarps][DEPTH]
+  uint64_t *k_full = raw_full + kDequantWarps * DEPTH, *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2,
+           *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
+  int32_t* ntok = reinterpret_cast<int32_t*>(done + 1);                   // [kMeta][PAGES] tokens of a tile's pages
   float* kscale = reinterpret_cast<float*>(ntok + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(kscale + kMeta * PAGES);
-  static_assert((2 * RS + 13) * 8 + 3 * kMeta * PAGES * 4 + 4 <= P::kMisc, "barriers and page records");
+  int32_t* entries = reinterpret_cast<int32_t*>(kscale + kMeta * PAGES);  // [kDequantWarps][DEPTH] page-table entries of the slots
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(entries + kDequantWarps * DEPTH);
   // Few rows: the 128 tensor-memory lanes hold `rep` copies of them, and each copy's warps take their share of a
   // tile's columns (P = 0 in the others), so that the softmax of a tile takes a rep-th of the time.
   const int rep = rows <= 32 && TOK == 128 ? 4 : rows <= 64 ? 2 : 1, row = tid % (kM / rep);
   const int n_sm = rep > 1 ? 4 : (rows + 31) / 32;   // softmax warps with rows
   if (tid == 0) {
-    for (int i = 0; i < RS; ++i) {
-      mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], PAGES);
-    }
+    for (int i = 0; i < kDequantWarps * DEPTH; ++i) mbar_init(&raw_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], PAGES);
       mbar_init(&k_empty[i], 1);
@@ -608,96 +613,102 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     // a warp takes one page's K or V; with 4 pages a tile (INT4) of every other tile
     constexpr int kTasks = 2 * PAGES, kTurns = kDequantWarps / kTasks;
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
-    const int wi = warp - 4, j = wi % PAGES, role = wi / PAGES % 2;
-    for (int i = wi / kTasks; i < n_tiles && ok; i += kTurns) {
-        const int seq = 2 * i + role, st = seq % RS;
-        ok = mbar_wait_bounded(&raw_full[st], (seq / RS) & 1, kWaitLimitNs);
-        uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
-        if (ok && i >= 2) ok = mbar_wait_bounded(empty, ((i >> 1) - 1) & 1, kWaitLimitNs);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const int32_t e = meta[(i & (kMeta - 1)) * PAGES + j];
-        const int n = ntok[(i & (kMeta - 1)) * PAGES + j];
-        const bool tier = FMT == KVQ_FMT_TIERED && e < 0;
-        const uint32_t stage = smem_u32(stages + st * P::kStage), blk = stage + j * SLOT;
-        const uint32_t cb = F::kGroup ? stage + (j / kGroupPages * kGroupPages) * SLOT : blk;
-        const uint32_t buf = smem_u32(smem) + (i & 1) * P::kBuf;
-        if (role == 0) {
-          const KTile<D, TOK> kt{buf, j}, lo{buf + (P::kPair ? 2 * P::kTile : 0), j};
-          if (FMT == KVQ_FMT_TIERED && lane == 0)
-            kscale[(i & (kMeta - 1)) * PAGES + j] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
-          if (n > 0) dequant_block<FMT, D, 0>(blk, cb, tree_block<FMT, D>(a, h, e, 0), tier, kt, lo, lane);
-        } else {
-          const VTile<D, TOK> vt{buf + P::kTile, j};
-          if (n > 0) dequant_block<FMT, D, 1>(blk, cb, tree_block<FMT, D>(a, h, e, 1), tier, vt, vt, lane);
-          if (n < kPage) {
-            __syncwarp();
-            zero_tokens<D>(vt, n, lane);
-          }
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
-          mbar_arrive(&raw_empty[st]);
-        }
-    }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 4 + kDequantWarps) {
-    // ------------------------------------------------------------------ producer
+    const int wi = warp - 4, j = wi % PAGES, role = wi / PAGES % 2, i0 = wi / kTasks;
+    const int n_mine = i0 < n_tiles ? (n_tiles - i0 + kTurns - 1) / kTurns : 0;   // this warp's tiles i0, i0 + kTurns, ...
+    uint64_t* full = raw_full + wi * DEPTH;
+    uint8_t* ring = slots + wi * DEPTH * SLOT;
     const int32_t* pt = a.page_table + (size_t)b * a.ppsm;
-    // the group format looks at the whole of a group that the bound on the length cuts
-    const int p_end = F::kGroup ? min((p1 + kGroupPages - 1) / kGroupPages * kGroupPages, a.ppsm) : p1;
-    auto entry = [&](int i) { return lane < PAGES && p0 + i * PAGES + lane < p_end ? pt[p0 + i * PAGES + lane] : 0; };
-    int32_t next = entry(0);
-    int issued = 0;
-    for (int i = 0; i < n_tiles && ok; ++i) {
-      const int page = p0 + i * PAGES + lane;
-      const int32_t e = next;
-      next = entry(i + 1);
-      const uint32_t phys = (uint32_t)e & 0x7FFFFFFFu;
-      const bool tier = e < 0, mine = lane < PAGES && page < p_end;
-      bool good = mine && (tier ? (FMT == KVQ_FMT_TIERED && phys < (uint32_t)a.num_tier_pages) : phys < (uint32_t)a.num_pages);
-      if (mine && !good) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
-      if (F::kGroup) {   // a group with a bad page is left out whole
-        const uint32_t all = __ballot_sync(0xffffffffu, good);
-        good = ((all >> (lane & ~3)) & 0xFu) == 0xFu;
+    // The page's entry in this warp's k-th tile: a window of 32 in the lanes.  kNoPage: absent, or bad.
+    // The group format looks at the whole of the page's group, which the bound on the length may cut.
+    int32_t* ent = entries + wi * DEPTH;
+    int win_base = 0, win = kNoPage;
+    auto load_window = [&](int base) {
+      win_base = base;
+      win = kNoPage;
+      const int p = p0 + (i0 + (base + lane) * kTurns) * PAGES + j;
+      if (base + lane >= n_mine || p >= p1) return;
+      bool good = true;
+      int32_t e = 0;
+      const int lo = F::kGroup ? p / kGroupPages * kGroupPages : p, hi = F::kGroup ? min(lo + kGroupPages, a.ppsm) : p + 1;
+      for (int x = lo; x < hi; ++x) {
+        const int32_t ex = pt[x];
+        const uint32_t phys = (uint32_t)ex & 0x7FFFFFFFu;
+        good = good && (ex < 0 ? (FMT == KVQ_FMT_TIERED && phys < (uint32_t)a.num_tier_pages) : phys < (uint32_t)a.num_pages);
+        e = x == p ? ex : e;
       }
-      uint32_t bytes = 0;
-      if (good)
-        bytes = tier                      ? (uint32_t)fetch_bytes<D>(kBlkFp8)
-                : F::kMain == kBlkCb2s    ? (uint32_t)(12 * D + 16 + 32 * a.n_static)
-                : F::kGroup               ? (uint32_t)((lane % kGroupPages ? 4 * D : 12 * D) + kOutPrefetch)
-                                          : (uint32_t)fetch_bytes<D>(F::kMain);
-      const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
-      for (int role = 0; role < 2; ++role) {
-        const int seq = 2 * i + role, st = seq % RS;
-        if (seq >= RS && !__all_sync(0xffffffffu, mbar_wait_bounded(&raw_empty[st], (seq / RS - 1) & 1, kWaitLimitNs))) {
-          ok = false;
-          break;
-        }
-        if (role == 0 && lane < PAGES) {
-          meta[(i & (kMeta - 1)) * PAGES + lane] = good ? (tier ? e : (int32_t)phys) : kNoPage;
-          ntok[(i & (kMeta - 1)) * PAGES + lane] = good ? max(min(kPage, v.len - kPage * page), 0) : 0;
-        }
-        __syncwarp();
+      if (good) win = e;
+      else if (role == 0) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
+    };
+    auto issue = [&](int k) {   // the copy of the warp's k-th block
+      if (k >= n_mine) return;
+      if (k - win_base >= 32) load_window(k);
+      const int32_t e = __shfl_sync(0xffffffffu, win, k - win_base);
+      if (lane != 0) return;
+      ent[k % DEPTH] = e;
+      uint64_t* bar = full + k % DEPTH;
+      uint8_t* dst = ring + (k % DEPTH) * SLOT;
+      if (e == kNoPage) {
+        mbar_arrive(bar);
+        return;
+      }
+      const uint8_t* src = tree_block<FMT, D>(a, h, e, role);
+      if constexpr (F::kGroup) {
+        const int page = p0 + (i0 + k * kTurns) * PAGES + j, first = page / kGroupPages * kGroupPages;
+        mbar_arrive_expect_tx(bar, 12 * D + kOutPrefetch);
+        bulk_g2s(dst, tree_block<FMT, D>(a, h, pt[first], role), 8 * D, bar);
+        bulk_g2s(dst + 8 * D, src + 8 * D, 4 * D + kOutPrefetch, bar);
+      } else {
+        const uint32_t bytes = FMT == KVQ_FMT_TIERED && e < 0 ? fetch_bytes<D>(kBlkFp8)
+                               : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
+                                                             : fetch_bytes<D>(F::kMain);
+        mbar_arrive_expect_tx(bar, bytes);
+        bulk_g2s(dst, src, bytes, bar);
+      }
+    };
+    load_window(0);
+    for (int k = 0; k < DEPTH; ++k) issue(k);
+    __syncwarp();
+    int issued = min(DEPTH, n_mine), waited = 0;
+    for (int k = 0; k < n_mine; ++k) {
+      const int i = i0 + k * kTurns;
+      ok = mbar_wait_bounded(full + k % DEPTH, (k / DEPTH) & 1, kWaitLimitNs);
+      waited += ok;
+      uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
+      if (ok && i >= 2) ok = mbar_wait_bounded(empty, ((i >> 1) - 1) & 1, kWaitLimitNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int32_t e = ent[k % DEPTH];
+      const int n = e == kNoPage ? 0 : min(kPage, v.len - kPage * (p0 + i * PAGES + j));
+      const bool tier = FMT == KVQ_FMT_TIERED && e < 0;
+      const uint32_t blk = smem_u32(ring + (k % DEPTH) * SLOT);
+      const uint32_t buf = smem_u32(smem) + (i & 1) * P::kBuf;
+      if (role == 0) {
+        const KTile<D, TOK> kt{buf, j}, low{buf + (P::kPair ? 2 * P::kTile : 0), j};
         if (lane == 0) {
-          if (total) mbar_arrive_expect_tx(&raw_full[st], total);
-          else mbar_arrive(&raw_full[st]);
+          ntok[(i & (kMeta - 1)) * PAGES + j] = n;
+          if (FMT == KVQ_FMT_TIERED) kscale[(i & (kMeta - 1)) * PAGES + j] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
         }
-        __syncwarp();
-        if (bytes) {
-          fence_proxy_async();
-          const int skip = F::kGroup && lane % kGroupPages ? 8 * D : 0;
-          bulk_g2s(stages + st * P::kStage + lane * SLOT + skip, tree_block<FMT, D>(a, h, e, role) + skip, bytes, &raw_full[st]);
+        if (n > 0) dequant_block<FMT, D, 0>(blk, tree_block<FMT, D>(a, h, e, 0), tier, kt, low, lane);
+      } else {
+        const VTile<D, TOK> vt{buf + P::kTile, j};
+        if (n > 0) dequant_block<FMT, D, 1>(blk, tree_block<FMT, D>(a, h, e, 1), tier, vt, vt, lane);
+        if (n < kPage) {
+          __syncwarp();
+          zero_tokens<D>(vt, n, lane);
         }
-        ++issued;
       }
+      fence_proxy_async();   // the tile for the MMAs, and the slot's reads before its next copy
+      __syncwarp();
+      if (lane == 0) mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
+      issue(k + DEPTH);
+      __syncwarp();
+      issued += k + DEPTH < n_mine;
     }
     if (!ok)   // let copies in flight land before the CTA can exit
-      for (int seq = max(issued - RS, 0); seq < issued; ++seq) mbar_wait_bounded(&raw_full[seq % RS], (seq / RS) & 1, kWaitLimitNs);
-    } else if (warp == 5 + kDequantWarps && lane == 0) {
+      for (int k = waited; k < issued; ++k) mbar_wait_bounded(full + k % DEPTH, (k / DEPTH) & 1, kWaitLimitNs);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 4 + kDequantWarps && lane == 0) {
     // ------------------------------------------------------------------ MMA
     constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);
     const uint32_t base = smem_u32(smem);
