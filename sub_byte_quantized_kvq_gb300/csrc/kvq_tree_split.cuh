@@ -72,6 +72,17 @@ struct Plan {
   static_assert(kDepth >= 2 && kSlot % 16 == 0 && kTile % 1024 == 0, "tree attention plan");
 };
 
+// A bounded mbarrier wait on the SM's own clock (reading the global timer costs
+// a waiting warp about a microsecond): gives up after 2^28 cycles, 130 ms at
+// the highest clock.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u))
+    if (clock64() - t0 > (1ll << 28)) return false;
+  return true;
+}
+
 __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3])
@@ -539,14 +550,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       sr.vec = a.page_lse && (a.P & 3) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 15) == 0;
       const int chunks = TOK / 32 / rep, c0 = warp / (4 / rep) * chunks;   // this warp's 32-column chunks
       for (int i = 0; i < n_tiles; ++i) {
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i & 1], (i >> 1) & 1, kWaitLimitNs));
+        ok = __all_sync(0xffffffffu, wait_bar(&s_full[i & 1], (i >> 1) & 1));
         if (!ok) break;
         tc::fence_after();
         const uint32_t ts = tmem + lanes + (i & 1) * 128;
         const int slot = (i & (kMeta - 1)) * PAGES, pt = p0 + i * PAGES;
         // PV(i - 1) has to be done before O changes; PV(i - 3), that barrier's phase before, is (S(i - 1) was committed after it)
         auto o_free = [&]() {
-          return i == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1, kWaitLimitNs));
+          return i == 0 || __all_sync(0xffffffffu, wait_bar(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
         };
         if (TOK == 128 && rep == 1) ok = sr.template tile<4>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
         else if (TOK / 32 / rep == 2) ok = sr.template tile<2>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
@@ -562,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[i & 1]);
       }
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, kWaitLimitNs));
+      ok = ok && __all_sync(0xffffffffu, wait_bar(done, 0));
       // ---- the partial state, through shared memory (the tiles are done): copies of a row are joined, rows stored whole
       constexpr int XS = D + 4;
       float* xo = reinterpret_cast<float*>(smem);                       // [128][XS], thread's row of O
@@ -671,10 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     int issued = min(DEPTH, n_mine), waited = 0;
     for (int k = 0; k < n_mine; ++k) {
       const int i = i0 + k * kTurns;
-      ok = mbar_wait_bounded(full + k % DEPTH, (k / DEPTH) & 1, kWaitLimitNs);
+      ok = wait_bar(full + k % DEPTH, (k / DEPTH) & 1);
       waited += ok;
       uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
-      if (ok && i >= 2) ok = mbar_wait_bounded(empty, ((i >> 1) - 1) & 1, kWaitLimitNs);
+      if (ok && i >= 2) ok = wait_bar(empty, ((i >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int32_t e = ent[k % DEPTH];
@@ -705,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       issued += k + DEPTH < n_mine;
     }
     if (!ok)   // let copies in flight land before the CTA can exit
-      for (int k = waited; k < issued; ++k) mbar_wait_bounded(full + k % DEPTH, (k / DEPTH) & 1, kWaitLimitNs);
+      for (int k = waited; k < issued; ++k) wait_bar(full + k % DEPTH, (k / DEPTH) & 1);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 4 + kDequantWarps && lane == 0) {
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);
     const uint32_t base = smem_u32(smem);
     auto scores = [&](int i) {
-      if (!mbar_wait_bounded(&k_full[i & 1], (i >> 1) & 1, kWaitLimitNs)) return false;
+      if (!wait_bar(&k_full[i & 1], (i >> 1) & 1)) return false;
       tc::fence_after();
       const uint32_t kt = base + (i & 1) * P::kBuf;
 #pragma unroll
@@ -729,8 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     ok = scores(0);
     for (int i = 0; i < n_tiles && ok; ++i) {
       if (i + 1 < n_tiles) ok = scores(i + 1);
-      ok = ok && mbar_wait_bounded(&p_full[i & 1], (i >> 1) & 1, kWaitLimitNs) &&
-           mbar_wait_bounded(&v_full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+      ok = ok && wait_bar(&p_full[i & 1], (i >> 1) & 1) &&
+           wait_bar(&v_full[i & 1], (i >> 1) & 1);
       if (!ok) break;
       tc::fence_after();
       const uint32_t vt = base + (i & 1) * P::kBuf + P::kTile;
@@ -740,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       tc::commit(&v_empty[i & 1]);
     }
     tc::commit(done);
-    if (!ok) mbar_wait_bounded(done, 0, kWaitLimitNs);   // tensor memory may be freed once what was issued is done
+    if (!ok) wait_bar(done, 0);   // tensor memory may be freed once what was issued is done
     }
   }
   if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
