@@ -96,20 +96,22 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
 // 16-byte chunk k of row r lies at chunk k ^ (r % 8).
 template <int D, int TOK>
 struct KTile {   // rows = tokens, D / 64 row groups
+  static constexpr int kStep4 = TOK * 128;   // four steps: the next row group
   uint32_t tile;
   int page;
   __device__ __forceinline__ uint32_t at(int t, int c) const {
     const int row = kPage * page + t;
     return tile + (c >> 6) * (TOK * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2;
   }
-  // lane's row address of step 0, and of step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15)
+  // lane's row address of a group of four steps, and of its step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15)
   __device__ __forceinline__ uint32_t lane_row(int lane) const { return tile + (kPage * page + (lane & 15)) * 128; }
   __device__ __forceinline__ uint32_t step(uint32_t row, int lane, int s) const {
-    return row + (s >> 2) * (TOK * 128) + (((((s & 3) * 2) ^ (lane & 7)) ^ (lane >> 4)) << 4);
+    return row + ((((s * 2) ^ (lane & 7)) ^ (lane >> 4)) << 4);
   }
 };
 template <int D, int TOK>
 struct VTile {   // rows = channels, TOK / 64 row groups
+  static constexpr int kStep4 = 4 * 2048;
   uint32_t tile;
   int page;
   __device__ __forceinline__ uint32_t at(int t, int c) const {
@@ -149,67 +151,74 @@ __device__ __forceinline__ void zero_tokens(const Tile& tile, int ntok, int lane
       if (t >= ntok) sts16(tile.at(t, c), 0u);
 }
 
-// One K block (role 0) or V block (role 1) -> its place in the fp16 tile.
+// One K block (role 0) or V block (role 1) -> its place in the fp16 tile, four
+// steps (64 channels) at a time: their loads overlap, and the loop is kept
+// rolled -- the warps of a scheduler run three different loops (softmax, K, V),
+// and unrolled ones spent half the time waiting for instructions.
 //   blk    shared address of the page's slot
 //   gblk   the block in global memory (side-list records past the prefetch)
 //   tier   the block is an FP8 block
 // K of an FP8 block is left unscaled (its page's scale is applied to the scores).
 template <int FMT, int D, int ROLE, class Tile>
-__device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk, bool tier, const Tile& tile,
-                                              const Tile& low, int lane) {
+__device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk, bool tier, const Tile& tile, const Tile& low,
+                                              int lane) {
   using F = Fmt<FMT>;
   constexpr int NS = D / 16, BLK = F::kMain;
   const int g = lane >> 2, q4 = lane & 3;
-  const uint32_t row = tile.lane_row(lane);
+  uint32_t row = tile.lane_row(lane);
   if (FMT == KVQ_FMT_TIERED && tier) {
     const float sc = ROLE == 1 ? ldsf(blk + fp8_sc_off(D)) : 1.f;
-    uint2 w[NS];
+#pragma unroll 1
+    for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4) {
+      const uint4 w0 = lds128(blk + 8 * NS * lane + 8 * s0), w1 = lds128(blk + 8 * NS * lane + 8 * s0 + 16);
+      const uint2 w[4] = {{w0.x, w0.y}, {w0.z, w0.w}, {w1.x, w1.y}, {w1.z, w1.w}};
 #pragma unroll
-    for (int s = 0; s < NS; ++s) w[s] = lds64(blk + 8 * NS * lane + 8 * s);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t x[4];
+        fp8_frag(w[k], x);
+        if (ROLE == 1)
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      uint32_t x[4];
-      fp8_frag(w[s], x);
-      if (ROLE == 1)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(u32_as_h2(x[k]));
-          x[k] = h2_as_u32(__floats2half2_rn(f.x * sc, f.y * sc));
-        }
-      stmatrix4(tile.step(row, lane, s), x);
+          for (int r = 0; r < 4; ++r) {
+            const float2 f = __half22float2(u32_as_h2(x[r]));
+            x[r] = h2_as_u32(__floats2half2_rn(f.x * sc, f.y * sc));
+          }
+        stmatrix4(tile.step(row, lane, k), x);
+      }
     }
     return;
   }
   if constexpr (BLK == kBlkInt4) {
-    constexpr int NG = D / 32, CAP = int4_cap(D);
-    const uint32_t lrow = low.lane_row(lane);
-    uint32_t w[NS];
-    load_e2m1_words<D>(blk, lane, w);   // one u32 of nibbles per step, as E2M1
-    constexpr int NZ = ROLE == 0 ? 2 : 4;   // tokens whose scale and minimum the lane needs
-    uint32_t z[NG][NZ];
-#pragma unroll
-    for (int gr = 0; gr < NG; ++gr)
+    constexpr int NG = D / 32, CAP = int4_cap(D), NZ = ROLE == 0 ? 2 : 4;   // NZ: tokens whose scale and minimum the lane needs
+    uint32_t lrow = low.lane_row(lane);
+#pragma unroll 1
+    for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4, lrow += Tile::kStep4) {
+      const uint4 w4 = lds128(blk + 4 * NS * lane + 4 * s0);   // one u32 of nibbles per step
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      uint32_t z[2][NZ];
 #pragma unroll
       for (int i = 0; i < NZ; ++i) {
         const int t = ROLE == 0 ? g + 8 * i : 2 * q4 + (i & 1) + 8 * (i >> 1);
-        z[gr][i] = lds32(blk + int4_sz_off(D) + 4 * (t * NG + gr));
+        const uint2 zz = lds64(blk + int4_sz_off(D) + 4 * (t * NG + (s0 >> 1)));
+        z[0][i] = zz.x;
+        z[1][i] = zz.y;
       }
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      uint32_t hi[4], lo[4];
-      float S[NZ], M[NZ];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t hi[4], lo[4];
+        float S[NZ], M[NZ];
 #pragma unroll
-      for (int i = 0; i < NZ; ++i) {
-        S[i] = fp16_bits_to_float(z[s >> 1][i]);
-        M[i] = fp16_bits_to_float(z[s >> 1][i] >> 16);
+        for (int i = 0; i < NZ; ++i) {
+          S[i] = fp16_bits_to_float(z[k >> 1][i]);
+          M[i] = fp16_bits_to_float(z[k >> 1][i] >> 16);
+        }
+        if constexpr (ROLE == 0) {
+          int4_k_frag(w[k], S[0], M[0], S[1], M[1], hi, lo);
+          stmatrix4(low.step(lrow, lane, k), lo);
+        } else {
+          int4_v_frag(w[k], S, M, hi, lo);
+        }
+        stmatrix4(tile.step(row, lane, k), hi);
       }
-      if constexpr (ROLE == 0) {
-        int4_k_frag(w[s], S[0], M[0], S[1], M[1], hi, lo);
-        stmatrix4(low.step(lrow, lane, s), lo);
-      } else {
-        int4_v_frag(w[s], S, M, hi, lo);
-      }
-      stmatrix4(tile.step(row, lane, s), hi);
     }
     __syncwarp();
     for (int e = lane; e < kPage * CAP; e += 32) {
@@ -221,71 +230,93 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk,
       }
     }
   } else if constexpr (BLK == kBlkE2m1) {
-    uint32_t w[NS], sc[NS][ROLE == 0 ? 1 : 2];
-    load_e2m1_words<D>(blk, lane, w);
+#pragma unroll 1
+    for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4) {
+      const uint4 w4 = lds128(blk + 4 * NS * lane + 4 * s0);
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      uint32_t sc[4][ROLE == 0 ? 1 : 2];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const uint32_t at = blk + e2m1_sc_off(D) + 16 * s;
-      if constexpr (ROLE == 0) {   // tokens g (registers 0, 2) and g + 8
-        sc[s][0] = lds8(at + g) | (lds8(at + g + 8) << 8);
-      } else {                     // tokens 2q, 2q + 1 (registers 0, 1) and + 8
-        sc[s][0] = lds16(at + 2 * q4);
-        sc[s][1] = lds16(at + 2 * q4 + 8);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t at = blk + e2m1_sc_off(D) + 16 * (s0 + k);
+        if constexpr (ROLE == 0) {   // tokens g (registers 0, 2) and g + 8
+          sc[k][0] = lds8(at + g) | (lds8(at + g + 8) << 8);
+        } else {                     // tokens 2q, 2q + 1 (registers 0, 1) and + 8
+          sc[k][0] = lds16(at + 2 * q4);
+          sc[k][1] = lds16(at + 2 * q4 + 8);
+        }
       }
-    }
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      uint32_t x[4];
-      e2m1_frag(w[s], x);
-      if constexpr (ROLE == 0) {
-        const __half2 sh = u32_as_h2(e4m3x2_to_f16x2(sc[s][0]));
-        const __half2 s0 = __low2half2(sh), s1 = __high2half2(sh);
-        x[0] = h2_as_u32(__hmul2(u32_as_h2(x[0]), s0));
-        x[1] = h2_as_u32(__hmul2(u32_as_h2(x[1]), s1));
-        x[2] = h2_as_u32(__hmul2(u32_as_h2(x[2]), s0));
-        x[3] = h2_as_u32(__hmul2(u32_as_h2(x[3]), s1));
-      } else {
-        const uint32_t s01 = e4m3x2_to_f16x2(sc[s][0]), s23 = e4m3x2_to_f16x2(sc[s][1]);
-        x[0] = hmul2u(x[0], s01);
-        x[1] = hmul2u(x[1], s01);
-        x[2] = hmul2u(x[2], s23);
-        x[3] = hmul2u(x[3], s23);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t x[4];
+        e2m1_frag(w[k], x);
+        if constexpr (ROLE == 0) {
+          const __half2 sh = u32_as_h2(e4m3x2_to_f16x2(sc[k][0]));
+          const __half2 h0 = __low2half2(sh), h1 = __high2half2(sh);
+          x[0] = h2_as_u32(__hmul2(u32_as_h2(x[0]), h0));
+          x[1] = h2_as_u32(__hmul2(u32_as_h2(x[1]), h1));
+          x[2] = h2_as_u32(__hmul2(u32_as_h2(x[2]), h0));
+          x[3] = h2_as_u32(__hmul2(u32_as_h2(x[3]), h1));
+        } else {
+          const uint32_t s01 = e4m3x2_to_f16x2(sc[k][0]), s23 = e4m3x2_to_f16x2(sc[k][1]);
+          x[0] = hmul2u(x[0], s01);
+          x[1] = hmul2u(x[1], s01);
+          x[2] = hmul2u(x[2], s23);
+          x[3] = hmul2u(x[3], s23);
+        }
+        stmatrix4(tile.step(row, lane, k), x);
       }
-      stmatrix4(tile.step(row, lane, s), x);
     }
   } else if constexpr (BLK == kBlkA3) {
-    uint32_t xw[D / 32], yw[D / 64];
-    load_a3_words<D>(blk, lane, xw, yw);
+#pragma unroll 1
+    for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4) {
+      const uint2 xw = lds64(blk + 2 * NS * lane + 2 * s0);                       // low code bits, two steps a word
+      const uint32_t yw = lds32(blk + a3_hi_off(D) + NS * lane + s0);             // high code bit, four steps
+      uint2 sc[4], zp[4];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      uint32_t x[4];
-      if (ROLE == 0) a3_k_frag<D>(blk, xw, yw, s, q4, x);
-      else a3_v_frag<D>(blk, xw, yw, s, g, x);
-      stmatrix4(tile.step(row, lane, s), x);
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (ROLE == 0) {   // 4 adjacent S and m: channels x, x + 1 (registers 0, 1), x + 8, x + 9
+          const int at = 2 * (16 * (s0 + k) + 4 * q4);
+          sc[k] = lds64(blk + a3_s_off(D) + at);
+          zp[k] = lds64(blk + a3_m_off(D) + at);
+        } else {                     // channels c (registers 0, 2) and c + 8, each for both tokens of a register
+          const int at = 2 * (16 * (s0 + k) + 2 * g);
+          const uint32_t s2 = lds32(blk + a3_s_off(D) + at), m2 = lds32(blk + a3_m_off(D) + at);
+          sc[k] = {prmt(s2, s2, 0x1010u), prmt(s2, s2, 0x3232u)};
+          zp[k] = {prmt(m2, m2, 0x1010u), prmt(m2, m2, 0x3232u)};
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t w = k < 2 ? xw.x : xw.y;
+        uint32_t x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool second = ROLE == 0 ? r >= 2 : (r & 1) != 0;
+          x[r] = a3_value(w, yw, k, r, second ? sc[k].y : sc[k].x, second ? zp[k].y : zp[k].x);
+        }
+        stmatrix4(tile.step(row, lane, k), x);
+      }
     }
     __syncwarp();
     patch_side_list<D, BLK>(blk + a3_out_off(D), gblk + a3_out_off(D), tile, lane);
   } else {   // 2-bit codebooks
-    const uint32_t book = blk + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
-    uint32_t w[D / 32];
-    load_codes<D>(blk + (F::kGroup ? cb2g_code_off(D) : 0), lane, w);
-    // four steps' codebook columns at a time, so that their loads overlap
-#pragma unroll
-    for (int s0 = 0; s0 < NS; s0 += 4) {
+    uint32_t book = blk + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
+#pragma unroll 1
+    for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4, book += 512) {
+      const uint2 w2 = lds64(blk + (F::kGroup ? cb2g_code_off(D) : 0) + 2 * NS * lane + 2 * s0);
       KCols kc[ROLE == 0 ? 4 : 1];
       uint4 vc[ROLE == 0 ? 1 : 4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if constexpr (ROLE == 0) kc[k] = cb2_k_cols(book, s0 + k);
-        else vc[k] = cb2_v_cols(book, s0 + k);
+        if constexpr (ROLE == 0) kc[k] = cb2_k_cols(book, k);
+        else vc[k] = cb2_v_cols(book, k);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int s = s0 + k;
+        const uint32_t w = k < 2 ? w2.x : w2.y, w16 = (k & 1) ? w >> 16 : w;
         uint32_t x[4];
-        const uint32_t w16 = (s & 1) ? w[s >> 1] >> 16 : w[s >> 1];
         if constexpr (ROLE == 0) cb2_k_expand(kc[k], w16, x);
         else cb2_v_expand(vc[k], w16, x);
-        stmatrix4(tile.step(row, lane, s), x);
+        stmatrix4(tile.step(row, lane, k), x);
       }
     }
     __syncwarp();
@@ -316,94 +347,121 @@ __device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, i
   }
 }
 
+// Pairs of fp32 in a 64-bit register.
+__device__ __forceinline__ uint64_t pack2u(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) { return pack2u(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  uint32_t x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // A softmax thread's row: m in log2 units, p = 2^(s f - m + kPBias), l the fp32 sum of p.
 template <int FMT, int D>
 struct SoftmaxRow {
   float m = -INFINITY, l = 0.f, f;
   float* lse_row;
-  bool vec;
+  bool vec;                // lse_row may be written two pages at a time
+  bool o_ready = false;    // this tile has already waited for O
 
-  // NC chunks of 32 columns (two pages) of S at ts, from chunk c0 on, in one
+  // `nc` chunks of 32 columns (two pages) of S at ts, from chunk c0 on, in one
   // pass: the chunk's maximum, p, P over S's columns.  A chunk that raises m
   // by more than kRescaleTh (rare after the first) scales what is there: O
   // (once o_free says that the MMAs are done with it) and the tile's earlier P.
-  template <int NC, class OFree>
-  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c0, const int32_t* ntok, const float* ks, int pt, int p1,
+  template <class OFree>
+  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c0, int nc, const int32_t* ntok, const float* ks, int pt, int p1,
                                        bool has_o, OFree&& o_free) {
-    uint32_t s[NC > 1 ? 2 : 1][32];
-    float pg[2 * NC];
-    tc::ld32_issue(ts + 32 * c0, s[0]);
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc) {
-      uint32_t(&x)[32] = s[cc & 1];
-      const int c = c0 + cc, n0 = ntok[2 * c], n1 = ntok[2 * c + 1];
+    uint32_t x[32];
+    tc::ld32_issue(ts + 32 * c0, x);
+#pragma unroll 1
+    for (int c = c0; c < c0 + nc; ++c) {
+      const int2 n = *reinterpret_cast<const int2*>(ntok + 2 * c);
+      float f0 = f, f1 = f;
+      if (FMT == KVQ_FMT_TIERED) {
+        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * c);
+        f0 *= k2.x;
+        f1 *= k2.y;
+      }
       tc::wait_ld(x);
-      if (cc + 1 < NC) tc::ld32_issue(ts + 32 * (c + 1), s[(cc + 1) & 1]);
-      if (n0 != kPage || n1 != kPage) {   // absent tokens
+      if (__builtin_expect(n.x + n.y != 2 * kPage, 0)) {   // absent tokens
 #pragma unroll
         for (int k = 0; k < kPage; ++k) {
-          x[k] = k < n0 ? x[k] : 0xFF800000u;
-          x[kPage + k] = k < n1 ? x[kPage + k] : 0xFF800000u;
+          x[k] = k < n.x ? x[k] : 0xFF800000u;
+          x[kPage + k] = k < n.y ? x[kPage + k] : 0xFF800000u;
         }
       }
-      const float f0 = FMT == KVQ_FMT_TIERED ? f * ks[2 * c] : f, f1 = FMT == KVQ_FMT_TIERED ? f * ks[2 * c + 1] : f;
       float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[kPage]);
 #pragma unroll
-      for (int k = 1; k < kPage; ++k) {
-        mx0 = fmaxf(mx0, __uint_as_float(x[k]));
-        mx1 = fmaxf(mx1, __uint_as_float(x[kPage + k]));
+      for (int k = 1; k < kPage - 1; k += 2) {
+        mx0 = fmaxf(fmaxf(mx0, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
+        mx1 = fmaxf(fmaxf(mx1, __uint_as_float(x[kPage + k])), __uint_as_float(x[kPage + k + 1]));
       }
+      mx0 = fmaxf(mx0, __uint_as_float(x[kPage - 1]));
+      mx1 = fmaxf(mx1, __uint_as_float(x[2 * kPage - 1]));
       const float pm0 = mx0 * f0, pm1 = mx1 * f1, mx = fmaxf(pm0, pm1);
       const bool need = mx > m + kRescaleTh;
-      if (__any_sync(0xffffffffu, need)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
         const float alpha = need ? ex2(m - mx) : 1.f;
         l *= alpha;
         m = need ? mx : m;
         if (has_o) {
           if (!o_free()) return false;
+          has_o = false;   // O is free for the rest of the tile, but may have to be scaled again
           tc::fence_after();
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) scale_columns(to + 32 * k, alpha);
+          o_ready = true;
         }
+        if (o_ready)
 #pragma unroll 1
-        for (int k = 0; k < cc; ++k) scale_p(ts + 16 * (c0 + k), alpha);
+          for (int k = 0; k < D / 16; ++k) scale_columns(to + 16 * k, alpha);
+#pragma unroll 1
+        for (int k = c0; k < c; ++k) scale_p(ts + 16 * k, alpha);
         tc::wait_st();
       }
       const float mb = (m == -INFINITY ? 0.f : m) - kPBias;
+      const uint64_t fa = pack2(f0, f0), fb = pack2(f1, f1), nb = pack2(-mb, -mb);
       uint32_t u[16];
-      float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+      uint64_t sa = 0, sb = 0;   // {0.f, 0.f}
 #pragma unroll
       for (int k = 0; k < kPage; k += 2) {
-        const float p0 = ex2(fmaf(__uint_as_float(x[k]), f0, -mb)), q0 = ex2(fmaf(__uint_as_float(x[k + 1]), f0, -mb));
-        const float p1_ = ex2(fmaf(__uint_as_float(x[kPage + k]), f1, -mb)),
-                    q1 = ex2(fmaf(__uint_as_float(x[kPage + k + 1]), f1, -mb));
-        u[k / 2] = h2_as_u32(__floats2half2_rn(p0, q0));
-        u[8 + k / 2] = h2_as_u32(__floats2half2_rn(p1_, q1));
-        a0 += p0;
-        b0 += q0;
-        a1 += p1_;
-        b1 += q1;
+        const float2 ya = unpack2(fma2(pack2u(x[k], x[k + 1]), fa, nb));
+        const float2 yb = unpack2(fma2(pack2u(x[kPage + k], x[kPage + k + 1]), fb, nb));
+        const float a0 = ex2(ya.x), a1 = ex2(ya.y), b0 = ex2(yb.x), b1 = ex2(yb.y);
+        u[k / 2] = h2_as_u32(__floats2half2_rn(a0, a1));
+        u[8 + k / 2] = h2_as_u32(__floats2half2_rn(b0, b1));
+        sa = add2(sa, pack2(a0, a1));
+        sb = add2(sb, pack2(b0, b1));
       }
-      a0 += b0;
-      a1 += b1;
-      l += a0 + a1;
-      tc::st16(ts + 16 * c, u);
+      const float2 pa = unpack2(sa), pb = unpack2(sb);
+      const float suma = pa.x + pa.y, sumb = pb.x + pb.y;
+      l += suma + sumb;
       if (lse_row) {
-        pg[2 * cc] = page_sum(x, 0, n0, f0, pm0, mb, a0);
-        pg[2 * cc + 1] = page_sum(x, kPage, n1, f1, pm1, mb, a1);
+        const float y0 = page_sum(x, 0, n.x, f0, pm0, mb, suma), y1 = page_sum(x, kPage, n.y, f1, pm1, mb, sumb);
+        const int p = pt + 2 * c;
+        if (vec && p + 1 < p1) {
+          *reinterpret_cast<float2*>(lse_row + p) = make_float2(y0, y1);
+        } else {
+          if (p < p1) lse_row[p] = y0;
+          if (p + 1 < p1) lse_row[p + 1] = y1;
+        }
       }
+      if (c + 1 < c0 + nc) tc::ld32_issue(ts + 32 * (c + 1), x);
+      tc::st16(ts + 16 * c, u);
     }
-    if (lse_row) {
-      float* o = lse_row + pt + 2 * c0;
-      if (vec && NC > 1 && pt + 2 * (c0 + NC) <= p1) {
-#pragma unroll
-        for (int j = 0; j < 2 * NC; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(pg[j], pg[j + 1], pg[j + 2], pg[j + 3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2 * NC; ++j)
-          if (pt + 2 * c0 + j < p1) o[j] = pg[j];
-      }
-    }
+    o_ready = false;
     return true;
   }
 
@@ -411,7 +469,7 @@ struct SoftmaxRow {
   // below the row's maximum that its terms vanish, the sum relative to its own.
   __device__ __forceinline__ float page_sum(const uint32_t (&x)[32], int at, int n, float fk, float pm, float mb, float sum) const {
     float shift = mb;
-    if (pm - mb < -100.f && n > 0) {
+    if (__builtin_expect(pm - mb < -100.f && n > 0, 0)) {
       sum = 0.f;
       shift = pm;
 #pragma unroll
@@ -420,12 +478,11 @@ struct SoftmaxRow {
     return n > 0 ? (__log2f(sum) + shift) * kLn2 : -INFINITY;
   }
   static __device__ __forceinline__ void scale_columns(uint32_t t, float alpha) {
-    uint32_t o[32];
-    tc::ld32_issue(t, o);
-    tc::wait_ld(o);
+    uint32_t o[16];
+    tc::ld16(t, o);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-    tc::st32(t, o);
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+    tc::st16(t, o);
   }
   static __device__ __forceinline__ void scale_p(uint32_t t, float alpha) {   // 16 columns of fp16 pairs
     uint32_t r[16];
@@ -547,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       SoftmaxRow<FMT, D> sr;
       sr.f = f;
       sr.lse_row = a.page_lse && row < rows ? page_lse_row(a, b, h, r0 + row) : nullptr;
-      sr.vec = a.page_lse && (a.P & 3) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 15) == 0;
+      sr.vec = (a.P & 1) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 7) == 0;
       const int chunks = TOK / 32 / rep, c0 = warp / (4 / rep) * chunks;   // this warp's 32-column chunks
       for (int i = 0; i < n_tiles; ++i) {
         ok = __all_sync(0xffffffffu, wait_bar(&s_full[i & 1], (i >> 1) & 1));
@@ -557,11 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         const int slot = (i & (kMeta - 1)) * PAGES, pt = p0 + i * PAGES;
         // PV(i - 1) has to be done before O changes; PV(i - 3), that barrier's phase before, is (S(i - 1) was committed after it)
         auto o_free = [&]() {
-          return i == 0 || __all_sync(0xffffffffu, wait_bar(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
+          return __all_sync(0xffffffffu, wait_bar(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
         };
-        if (TOK == 128 && rep == 1) ok = sr.template tile<4>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
-        else if (TOK / 32 / rep == 2) ok = sr.template tile<2>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
-        else ok = sr.template tile<1>(ts, t_o + lanes, c0, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        ok = sr.tile(ts, t_o + lanes, c0, chunks, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
         if (!ok) break;
         if (rep > 1) {   // the columns of the row's other copies: P = 0
           const uint32_t z[16] = {};
