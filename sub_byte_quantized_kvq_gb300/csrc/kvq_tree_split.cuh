@@ -124,23 +124,40 @@ struct VTile {   // rows = channels, TOK / 64 row groups
   __device__ __forceinline__ uint32_t step(uint32_t row, int, int s) const { return row + s * 2048; }
 };
 
-// The outliers of a side-list over their slots' values: two records at a time,
-// a token a lane.  Records past the prefetched ones come from global memory.
-template <int D, int BLK, class Tile>
-__device__ __forceinline__ void patch_side_list(uint32_t side_s, const uint8_t* side_g, const Tile& tile, int lane) {
-  const int n = min((int)lds8(side_s), D), t = lane & 15;
-  for (int i = lane >> 4; i < n; i += 2) {
-    uint32_t head, value;
-    if (i < kChunk) {
-      head = lds32(side_s + 4 + 20 * i);
-      value = lds8(side_s + 8 + 20 * i + t);
-    } else {
-      head = *reinterpret_cast<const uint32_t*>(side_g + 4 + 20 * i);
-      value = side_g[8 + 20 * i + t];
+// The outliers of a side-list, stored over their slots' values: two records at
+// a time, a token a lane.  The prefetched records are loaded before the codes
+// are expanded (`load`) and stored after them (`store`); later ones, rare, come
+// from global memory.
+template <int D>
+struct SidePatch {
+  uint32_t head[kChunk / 2], value[kChunk / 2];
+  int n;
+  __device__ __forceinline__ void load(uint32_t side_s, int lane) {
+    n = min((int)lds8(side_s), D);
+#pragma unroll
+    for (int k = 0; k < kChunk / 2; ++k) {
+      const uint32_t rec = side_s + 4 + 20 * (2 * k + (lane >> 4));
+      head[k] = lds32(rec);
+      value[k] = lds8(rec + 4 + (lane & 15));
     }
-    if ((head >> (16 + t)) & 1u) sts16(tile.at(t, head & (D - 1)), e4m3x2_to_f16x2(value));
   }
-}
+  template <class Tile, class Side>
+  __device__ __forceinline__ void store(const Tile& tile, int lane, Side&& side_g) {
+    const int t = lane & 15, half = lane >> 4;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kChunk / 2; ++k)
+      if (2 * k + half < n && ((head[k] >> (16 + t)) & 1u))
+        sts16(tile.at(t, head[k] & (D - 1)), e4m3x2_to_f16x2(value[k]));
+    if (__builtin_expect(n > kChunk, 0)) {
+      const uint8_t* side = side_g();
+      for (int i = kChunk + half; i < n; i += 2) {
+        const uint8_t* rec = side + 4 + 20 * i;
+        if ((*reinterpret_cast<const uint16_t*>(rec + 2) >> t) & 1u) sts16(tile.at(t, rec[0] & (D - 1)), e4m3x2_to_f16x2(rec[4 + t]));
+      }
+    }
+  }
+};
 
 // Tokens from `ntok` on as zeros in a V tile (their probability is 0, and stale bytes may stand for anything).
 template <int D, class Tile>
@@ -156,11 +173,11 @@ __device__ __forceinline__ void zero_tokens(const Tile& tile, int ntok, int lane
 // rolled -- the warps of a scheduler run three different loops (softmax, K, V),
 // and unrolled ones spent half the time waiting for instructions.
 //   blk    shared address of the page's slot
-//   gblk   the block in global memory (side-list records past the prefetch)
+//   gblk   a function that gives the block in global memory (side-list records past the prefetch)
 //   tier   the block is an FP8 block
 // K of an FP8 block is left unscaled (its page's scale is applied to the scores).
-template <int FMT, int D, int ROLE, class Tile>
-__device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk, bool tier, const Tile& tile, const Tile& low,
+template <int FMT, int D, int ROLE, class Tile, class GBlk>
+__device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool tier, const Tile& tile, const Tile& low,
                                               int lane) {
   using F = Fmt<FMT>;
   constexpr int NS = D / 16, BLK = F::kMain;
@@ -267,6 +284,8 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk,
       }
     }
   } else if constexpr (BLK == kBlkA3) {
+    SidePatch<D> patch;
+    patch.load(blk + a3_out_off(D), lane);
 #pragma unroll 1
     for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4) {
       const uint2 xw = lds64(blk + 2 * NS * lane + 2 * s0);                       // low code bits, two steps a word
@@ -297,9 +316,10 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk,
         stmatrix4(tile.step(row, lane, k), x);
       }
     }
-    __syncwarp();
-    patch_side_list<D, BLK>(blk + a3_out_off(D), gblk + a3_out_off(D), tile, lane);
+    patch.store(tile, lane, [&]() { return gblk() + a3_out_off(D); });
   } else {   // 2-bit codebooks
+    SidePatch<D> patch;
+    if constexpr (BLK != kBlkCb2s) patch.load(blk + cb2_out_off(D), lane);
     uint32_t book = blk + (F::kGroup ? 0 : cb2_cb_off(D)) + 16 * (ROLE == 0 ? q4 : g);
 #pragma unroll 1
     for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4, book += 512) {
@@ -319,22 +339,15 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, const uint8_t* gblk,
         stmatrix4(tile.step(row, lane, k), x);
       }
     }
-    __syncwarp();
     if constexpr (BLK == kBlkCb2s) {   // the static channels' fp16 values
+      __syncwarp();
       const int n = min((int)lds8(blk + cb2s_hdr_off(D)), kMaxStatic), t = lane & 15;
       for (int i = lane >> 4; i < n; i += 2)
         sts16(tile.at(t, lds8(blk + cb2s_hdr_off(D) + 1 + i) & (D - 1)), lds16(blk + cb2s_val_off(D) + 32 * i + 2 * t));
     } else {
-      patch_side_list<D, BLK>(blk + cb2_out_off(D), gblk + cb2_out_off(D), tile, lane);
+      patch.store(tile, lane, [&]() { return gblk() + cb2_out_off(D); });
     }
   }
-}
-
-template <int FMT, int D>
-__device__ __forceinline__ const uint8_t* tree_block(const TreeArgs& a, int h, int32_t e, int role) {
-  const size_t phys = (uint32_t)e & 0x7FFFFFFFu;
-  if (FMT == KVQ_FMT_TIERED && e < 0) return a.tier_pool + ((phys * a.Hkv + h) * 2 + role) * block_stride(kBlkFp8, D);
-  return a.pool + ((phys * a.Hkv + h) * 2 + role) * block_stride(Fmt<FMT>::kMain, D);
 }
 
 // -inf in page_lse for pages [p_lo, p_hi) of the CTA's rows [r_lo, r_hi).
@@ -375,52 +388,69 @@ template <int FMT, int D>
 struct SoftmaxRow {
   float m = -INFINITY, l = 0.f, f;
   float* lse_row;
-  bool vec;                // lse_row may be written two pages at a time
-  bool o_ready = false;    // this tile has already waited for O
+  bool vec;   // lse_row may be written two pages at a time
 
-  // `nc` chunks of 32 columns (two pages) of S at ts, from chunk c0 on, in one
-  // pass: the chunk's maximum, p, P over S's columns.  A chunk that raises m
-  // by more than kRescaleTh (rare after the first) scales what is there: O
-  // (once o_free says that the MMAs are done with it) and the tile's earlier P.
-  template <class OFree>
-  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c0, int nc, const int32_t* ntok, const float* ks, int pt, int p1,
-                                       bool has_o, OFree&& o_free) {
-    uint32_t x[32];
-    tc::ld32_issue(ts + 32 * c0, x);
-#pragma unroll 1
-    for (int c = c0; c < c0 + nc; ++c) {
-      const int2 n = *reinterpret_cast<const int2*>(ntok + 2 * c);
-      float f0 = f, f1 = f;
-      if (FMT == KVQ_FMT_TIERED) {
-        const float2 k2 = *reinterpret_cast<const float2*>(ks + 2 * c);
-        f0 *= k2.x;
-        f1 *= k2.y;
-      }
-      tc::wait_ld(x);
-      if (__builtin_expect(n.x + n.y != 2 * kPage, 0)) {   // absent tokens
+  // Columns [c_lo, c_hi) of S at ts, W (32 or 64) at a time, in one pass: the
+  // chunk's maximum, p, P over S's columns.  A chunk that raises m by more than
+  // kRescaleTh (rare after the first) scales what is there: O (once o_free says
+  // that the MMAs are done with it) and the tile's earlier P.
+  template <int W, class OFree>
+  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c_lo, int c_hi, const int32_t* ntok, const float* ks, int pt,
+                                       int p1, bool has_o, OFree&& o_free) {
+    constexpr int NP = W / kPage;   // pages of a chunk
+    uint32_t x[W];
+    auto load = [&](int c) {
 #pragma unroll
-        for (int k = 0; k < kPage; ++k) {
-          x[k] = k < n.x ? x[k] : 0xFF800000u;
-          x[kPage + k] = k < n.y ? x[kPage + k] : 0xFF800000u;
+      for (int w = 0; w < W / 32; ++w) tc::ld32_issue(ts + c + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * w));
+    };
+    load(c_lo);
+    bool o_ready = false;
+#pragma unroll 1
+    for (int c = c_lo; c < c_hi; c += W) {
+      const int pg = c / kPage;
+      int n[NP], total = 0;
+      float fk[NP], pm[NP];
+#pragma unroll
+      for (int j = 0; j < NP; j += 2) {
+        const int2 n2 = *reinterpret_cast<const int2*>(ntok + pg + j);
+        n[j] = n2.x;
+        n[j + 1] = n2.y;
+        total += n2.x + n2.y;
+        fk[j] = fk[j + 1] = f;
+        if (FMT == KVQ_FMT_TIERED) {
+          const float2 k2 = *reinterpret_cast<const float2*>(ks + pg + j);
+          fk[j] *= k2.x;
+          fk[j + 1] *= k2.y;
         }
       }
-      float mx0 = __uint_as_float(x[0]), mx1 = __uint_as_float(x[kPage]);
 #pragma unroll
-      for (int k = 1; k < kPage - 1; k += 2) {
-        mx0 = fmaxf(fmaxf(mx0, __uint_as_float(x[k])), __uint_as_float(x[k + 1]));
-        mx1 = fmaxf(fmaxf(mx1, __uint_as_float(x[kPage + k])), __uint_as_float(x[kPage + k + 1]));
+      for (int w = 0; w < W / 32; ++w) tc::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * w));
+      if (__builtin_expect(total != W, 0)) {   // absent tokens
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+          for (int k = 0; k < kPage; ++k) x[kPage * j + k] = k < n[j] ? x[kPage * j + k] : 0xFF800000u;
       }
-      mx0 = fmaxf(mx0, __uint_as_float(x[kPage - 1]));
-      mx1 = fmaxf(mx1, __uint_as_float(x[2 * kPage - 1]));
-      const float pm0 = mx0 * f0, pm1 = mx1 * f1, mx = fmaxf(pm0, pm1);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint32_t* y = x + kPage * j;
+        float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
+#pragma unroll
+        for (int k = 2; k < kPage - 2; k += 4) {
+          m0 = fmaxf(fmaxf(m0, __uint_as_float(y[k])), __uint_as_float(y[k + 2]));
+          m1 = fmaxf(fmaxf(m1, __uint_as_float(y[k + 1])), __uint_as_float(y[k + 3]));
+        }
+        pm[j] = fmaxf(fmaxf(m0, __uint_as_float(y[kPage - 2])), fmaxf(m1, __uint_as_float(y[kPage - 1]))) * fk[j];
+        mx = fmaxf(mx, pm[j]);
+      }
       const bool need = mx > m + kRescaleTh;
       if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
         const float alpha = need ? ex2(m - mx) : 1.f;
         l *= alpha;
         m = need ? mx : m;
-        if (has_o) {
+        if (has_o && !o_ready) {
           if (!o_free()) return false;
-          has_o = false;   // O is free for the rest of the tile, but may have to be scaled again
           tc::fence_after();
           o_ready = true;
         }
@@ -428,52 +458,63 @@ struct SoftmaxRow {
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) scale_columns(to + 16 * k, alpha);
 #pragma unroll 1
-        for (int k = c0; k < c; ++k) scale_p(ts + 16 * k, alpha);
+        for (int k = c_lo / 32; k < c / 32; ++k) scale_p(ts + 16 * k, alpha);
         tc::wait_st();
       }
       const float mb = (m == -INFINITY ? 0.f : m) - kPBias;
-      const uint64_t fa = pack2(f0, f0), fb = pack2(f1, f1), nb = pack2(-mb, -mb);
-      uint32_t u[16];
-      uint64_t sa = 0, sb = 0;   // {0.f, 0.f}
+      const uint64_t nb = pack2(-mb, -mb);
+      uint32_t u[W / 2];
+      uint64_t sum[NP];
 #pragma unroll
-      for (int k = 0; k < kPage; k += 2) {
-        const float2 ya = unpack2(fma2(pack2u(x[k], x[k + 1]), fa, nb));
-        const float2 yb = unpack2(fma2(pack2u(x[kPage + k], x[kPage + k + 1]), fb, nb));
-        const float a0 = ex2(ya.x), a1 = ex2(ya.y), b0 = ex2(yb.x), b1 = ex2(yb.y);
-        u[k / 2] = h2_as_u32(__floats2half2_rn(a0, a1));
-        u[8 + k / 2] = h2_as_u32(__floats2half2_rn(b0, b1));
-        sa = add2(sa, pack2(a0, a1));
-        sb = add2(sb, pack2(b0, b1));
-      }
-      const float2 pa = unpack2(sa), pb = unpack2(sb);
-      const float suma = pa.x + pa.y, sumb = pb.x + pb.y;
-      l += suma + sumb;
-      if (lse_row) {
-        const float y0 = page_sum(x, 0, n.x, f0, pm0, mb, suma), y1 = page_sum(x, kPage, n.y, f1, pm1, mb, sumb);
-        const int p = pt + 2 * c;
-        if (vec && p + 1 < p1) {
-          *reinterpret_cast<float2*>(lse_row + p) = make_float2(y0, y1);
-        } else {
-          if (p < p1) lse_row[p] = y0;
-          if (p + 1 < p1) lse_row[p + 1] = y1;
+      for (int j = 0; j < NP; ++j) {
+        const uint64_t f2 = pack2(fk[j], fk[j]);
+        sum[j] = 0;   // {0.f, 0.f}
+#pragma unroll
+        for (int k = 0; k < kPage; k += 2) {
+          const float2 y = unpack2(fma2(pack2u(x[kPage * j + k], x[kPage * j + k + 1]), f2, nb));
+          const float e0 = ex2(y.x), e1 = ex2(y.y);
+          u[(kPage * j + k) / 2] = h2_as_u32(__floats2half2_rn(e0, e1));
+          sum[j] = add2(sum[j], pack2(e0, e1));
         }
       }
-      if (c + 1 < c0 + nc) tc::ld32_issue(ts + 32 * (c + 1), x);
-      tc::st16(ts + 16 * c, u);
+      float ps[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float2 y = unpack2(sum[j]);
+        ps[j] = y.x + y.y;
+      }
+#pragma unroll
+      for (int j = 0; j < NP; j += 2) l += ps[j] + ps[j + 1];
+      if (lse_row) {
+#pragma unroll
+        for (int j = 0; j < NP; j += 2) {
+          const float y0 = page_sum(x + kPage * j, n[j], fk[j], pm[j], mb, ps[j]);
+          const float y1 = page_sum(x + kPage * (j + 1), n[j + 1], fk[j + 1], pm[j + 1], mb, ps[j + 1]);
+          const int p = pt + pg + j;
+          if (vec && p + 1 < p1) {
+            *reinterpret_cast<float2*>(lse_row + p) = make_float2(y0, y1);
+          } else {
+            if (p < p1) lse_row[p] = y0;
+            if (p + 1 < p1) lse_row[p + 1] = y1;
+          }
+        }
+      }
+      if (c + W < c_hi) load(c + W);
+#pragma unroll
+      for (int w = 0; w < W / 32; ++w) tc::st16(ts + c / 2 + 16 * w, u + 16 * w);
     }
-    o_ready = false;
     return true;
   }
 
   // ln of a page's sum, given sum = sum 2^(s f - mb); where the page lies so far
   // below the row's maximum that its terms vanish, the sum relative to its own.
-  __device__ __forceinline__ float page_sum(const uint32_t (&x)[32], int at, int n, float fk, float pm, float mb, float sum) const {
+  __device__ __forceinline__ float page_sum(const uint32_t* x, int n, float fk, float pm, float mb, float sum) const {
     float shift = mb;
     if (__builtin_expect(pm - mb < -100.f && n > 0, 0)) {
       sum = 0.f;
       shift = pm;
 #pragma unroll
-      for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(__uint_as_float(x[at + k]), fk, -pm));
+      for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(__uint_as_float(x[k]), fk, -pm));
     }
     return n > 0 ? (__log2f(sum) + shift) * kLn2 : -INFINITY;
   }
@@ -616,7 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         auto o_free = [&]() {
           return __all_sync(0xffffffffu, wait_bar(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
         };
-        ok = sr.tile(ts, t_o + lanes, c0, chunks, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        const int lo = 32 * c0, hi = 32 * (c0 + chunks);
+        ok = chunks > 1 ? sr.template tile<64>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, pt, p1, i > 0, o_free)
+                        : sr.template tile<32>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
         if (!ok) break;
         if (rep > 1) {   // the columns of the row's other copies: P = 0
           const uint32_t z[16] = {};
@@ -705,60 +748,67 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       if (good) win = e;
       else if (role == 0) atomicOr(a.status, KVQ_STATUS_BAD_PAGE);
     };
-    auto issue = [&](int k) {   // the copy of the warp's k-th block
-      if (k >= n_mine) return;
+    // where this warp's blocks of physical page 0 lie, and the bytes from a page to the next
+    const size_t main_page = (size_t)a.Hkv * 2 * block_stride(F::kMain, D), tier_page = (size_t)a.Hkv * 2 * block_stride(kBlkFp8, D);
+    const uint8_t* const main_src = a.pool + (size_t)(2 * h + role) * block_stride(F::kMain, D);
+    const uint8_t* const tier_src = FMT == KVQ_FMT_TIERED ? a.tier_pool + (size_t)(2 * h + role) * block_stride(kBlkFp8, D) : nullptr;
+    auto block_at = [&](int32_t e) {
+      return FMT == KVQ_FMT_TIERED && e < 0 ? tier_src + ((uint32_t)e & 0x7FFFFFFFu) * tier_page : main_src + (uint32_t)e * main_page;
+    };
+    auto issue = [&](int k, int slot) {   // the copy of the warp's k-th block
       if (k - win_base >= 32) load_window(k);
       const int32_t e = __shfl_sync(0xffffffffu, win, k - win_base);
-      if (lane != 0) return;
-      ent[k % DEPTH] = e;
-      uint64_t* bar = full + k % DEPTH;
-      uint8_t* dst = ring + (k % DEPTH) * SLOT;
-      if (e == kNoPage) {
-        mbar_arrive(bar);
-        return;
+      if (lane == 0) {
+        ent[slot] = e;
+        uint64_t* bar = full + slot;
+        uint8_t* dst = ring + slot * SLOT;
+        if (e == kNoPage) {
+          mbar_arrive(bar);
+        } else if constexpr (F::kGroup) {
+          const int page = p0 + (i0 + k * kTurns) * PAGES + j, first = page / kGroupPages * kGroupPages;
+          mbar_arrive_expect_tx(bar, 12 * D + kOutPrefetch);
+          bulk_g2s(dst, block_at(pt[first]), 8 * D, bar);
+          bulk_g2s(dst + 8 * D, block_at(e) + 8 * D, 4 * D + kOutPrefetch, bar);
+        } else {
+          const uint32_t bytes = FMT == KVQ_FMT_TIERED && e < 0 ? fetch_bytes<D>(kBlkFp8)
+                                 : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
+                                                               : fetch_bytes<D>(F::kMain);
+          mbar_arrive_expect_tx(bar, bytes);
+          bulk_g2s(dst, block_at(e), bytes, bar);
+        }
       }
-      const uint8_t* src = tree_block<FMT, D>(a, h, e, role);
-      if constexpr (F::kGroup) {
-        const int page = p0 + (i0 + k * kTurns) * PAGES + j, first = page / kGroupPages * kGroupPages;
-        mbar_arrive_expect_tx(bar, 12 * D + kOutPrefetch);
-        bulk_g2s(dst, tree_block<FMT, D>(a, h, pt[first], role), 8 * D, bar);
-        bulk_g2s(dst + 8 * D, src + 8 * D, 4 * D + kOutPrefetch, bar);
-      } else {
-        const uint32_t bytes = FMT == KVQ_FMT_TIERED && e < 0 ? fetch_bytes<D>(kBlkFp8)
-                               : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
-                                                             : fetch_bytes<D>(F::kMain);
-        mbar_arrive_expect_tx(bar, bytes);
-        bulk_g2s(dst, src, bytes, bar);
-      }
+      __syncwarp();
     };
     load_window(0);
-    for (int k = 0; k < DEPTH; ++k) issue(k);
-    __syncwarp();
     int issued = min(DEPTH, n_mine), waited = 0;
+    for (int k = 0; k < issued; ++k) issue(k, k);
+    int slot = 0;
+    uint32_t phase = 0;
     for (int k = 0; k < n_mine; ++k) {
       const int i = i0 + k * kTurns;
-      ok = wait_bar(full + k % DEPTH, (k / DEPTH) & 1);
+      ok = wait_bar(full + slot, phase);
       waited += ok;
       uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
       if (ok && i >= 2) ok = wait_bar(empty, ((i >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int32_t e = ent[k % DEPTH];
+      const int32_t e = ent[slot];
       const int n = e == kNoPage ? 0 : min(kPage, v.len - kPage * (p0 + i * PAGES + j));
       const bool tier = FMT == KVQ_FMT_TIERED && e < 0;
-      const uint32_t blk = smem_u32(ring + (k % DEPTH) * SLOT);
+      const uint32_t blk = smem_u32(ring + slot * SLOT);
       const uint32_t buf = smem_u32(smem) + (i & 1) * P::kBuf;
+      auto gblk = [&]() { return block_at(e); };
       if (role == 0) {
         const KTile<D, TOK> kt{buf, j}, low{buf + (P::kPair ? 2 * P::kTile : 0), j};
         if (lane == 0) {
           ntok[(i & (kMeta - 1)) * PAGES + j] = n;
           if (FMT == KVQ_FMT_TIERED) kscale[(i & (kMeta - 1)) * PAGES + j] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
         }
-        if (n > 0) dequant_block<FMT, D, 0>(blk, tree_block<FMT, D>(a, h, e, 0), tier, kt, low, lane);
+        if (n > 0) dequant_block<FMT, D, 0>(blk, gblk, tier, kt, low, lane);
       } else {
         const VTile<D, TOK> vt{buf + P::kTile, j};
-        if (n > 0) dequant_block<FMT, D, 1>(blk, tree_block<FMT, D>(a, h, e, 1), tier, vt, vt, lane);
-        if (n < kPage) {
+        if (n > 0) dequant_block<FMT, D, 1>(blk, gblk, tier, vt, vt, lane);
+        if (__builtin_expect(n < kPage, 0)) {
           __syncwarp();
           zero_tokens<D>(vt, n, lane);
         }
@@ -766,9 +816,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       fence_proxy_async();   // the tile for the MMAs, and the slot's reads before its next copy
       __syncwarp();
       if (lane == 0) mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
-      issue(k + DEPTH);
-      __syncwarp();
-      issued += k + DEPTH < n_mine;
+      if (k + DEPTH < n_mine) {
+        issue(k + DEPTH, slot);
+        ++issued;
+      }
+      if (++slot == DEPTH) {
+        slot = 0;
+        phase ^= 1u;
+      }
     }
     if (!ok)   // let copies in flight land before the CTA can exit
       for (int k = waited; k < issued; ++k) wait_bar(full + k % DEPTH, (k / DEPTH) & 1);
