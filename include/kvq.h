@@ -359,7 +359,7 @@ kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, 
  *   workspace  device, >= kvq_tree_workspace_bytes(), 16-byte aligned; needs no
  *              initialisation.  Calls that may overlap on the GPU (two streams,
  *              two graphs) need one each.
- * q, k_tree and v_tree must be 16-byte aligned.  What a row does not attend to
+ * q, k_tree, v_tree, out and the cache's staging must be 16-byte aligned.  What a row does not attend to
  * (masked nodes, nodes past the count, stale bytes of a page's unwritten
  * tokens) never reaches it, whatever it holds; K and V that a row does attend
  * to are taken as they are.  A bad page-table entry sets KVQ_STATUS_BAD_PAGE

@@ -482,7 +482,9 @@ kvq_status kvq_tree_attention(const kvq_config* cfg, const kvq_cache* cache, con
     return KVQ_ERR_INVALID_ARG;
   if (!k_tree != !v_tree || (!k_tree && tree_mask) || (mask_per_seq != 0 && mask_per_seq != 1)) return KVQ_ERR_INVALID_ARG;
   if (!std::isfinite(softmax_scale)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(out) || !aligned16(cache->staging) ||
+      !aligned16(workspace))
+    return KVQ_ERR_INVALID_ARG;
   const int S = tree_splits(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
   const size_t rows = tree_rows(cfg, num_q_heads, num_nodes, S);
   if (workspace_bytes < rows * (cfg->head_dim * sizeof(float) + sizeof(float2))) return KVQ_ERR_WORKSPACE;

@@ -5,10 +5,10 @@
 //                                 that t's ancestor word names
 //   out[r]  = sum_j e^a[r][j] v_j / sum_j e^a[r][j]
 //   lse[r]  = ln sum_j e^a[r][j],   page_lse[r][p] = ln sum over page p
-// in two launches: split kernels turn the cached pages into partial states
-// (m, l, o) per (row, split); the merge kernel adds what is not in blocks (the
-// fp32 staging tail and the drafted tokens' bf16 K and V), joins the splits and
-// writes the results.
+// in two launches: a split kernel (kvq_tree_split.cuh) turns the cached pages
+// into partial states (m, l, o) per (row, split); the merge kernel adds what is
+// not in blocks (the fp32 staging tail and the drafted tokens' bf16 K and V),
+// joins the splits and writes the results.
 #include <algorithm>
 #include <mutex>
 
@@ -21,45 +21,58 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// ----------------------------------------------------------------------------- rows on the CUDA cores
-// A warp's state for kWR rows: channel c = 32 i + lane of row w in o[w][i].
-constexpr int kWR = 4;
-template <int D>
+// ----------------------------------------------------------------------------- tail, tree and merge
+// What is not in blocks, and the joining of the splits.  Grid (ceil(R / (8 WR)),
+// Hkv, B), 8 warps of WR rows.
+//
+// The staged tail (up to 15 tokens, 63 for the group format) and the drafted
+// tokens go in chunks of 16 through shared memory in fp32 and are computed on
+// the CUDA cores: K and V of a token that a row does not see never reach the
+// row, so a branch may hold infinities or NaN without touching its siblings,
+// and bf16 K and V keep their whole range.  It is little work (16 nodes: 1/2000
+// of the cached pages' at 32k tokens), done before the split kernel's results
+// are waited for.  The merge reads each partial state once, four or more rows'
+// or splits' loads in flight; splits are joined in ascending order.
+template <int D, int WR>
 struct RowState {
-  float m[kWR], l[kWR], o[kWR][D / 32];
+  float m[WR], l[WR], o[WR][D / 32];   // lane's channels (D / 32) lane ..
 };
-template <int D>
-__device__ __forceinline__ void row_state_init(RowState<D>& st) {
-#pragma unroll
-  for (int w = 0; w < kWR; ++w) {
-    st.m[w] = -INFINITY;
-    st.l[w] = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) st.o[w][i] = 0.f;
-  }
+
+template <int N>
+struct Vec;
+template <>
+struct Vec<2> { using T = float2; };
+template <>
+struct Vec<4> { using T = float4; };
+template <int N>
+__device__ __forceinline__ void load_vec(float (&v)[N], const float* p) {
+  *reinterpret_cast<typename Vec<N>::T*>(v) = *reinterpret_cast<const typename Vec<N>::T*>(p);
 }
 
-// One chunk of up to 16 tokens (ks, vs: fp32 [16][D + 1] in shared memory) for
-// the warp's rows: lane = (half of the channels, token) for the scores, a
-// channel slice for the outputs.  seen[w]: bit t set where row w attends to
-// token t.  page[w] is set to the chunk's log2-sum-exp.  Tokens a row does not
-// see are left out, whatever their K and V hold.
-template <int D>
-__device__ __forceinline__ void rows_chunk(RowState<D>& st, const float (*qs)[D], const float (*ks)[D + 1],
-                                           const float (*vs)[D + 1], const uint32_t (&seen)[kWR], float scale_log2,
-                                           float (&page)[kWR], int lane) {
+// One chunk of up to 16 tokens (ks, vs: fp32 rows of D + 4) for the warp's rows:
+// lane = (half of the channels, token) for the scores, D / 32 channels for the
+// outputs.  seen[w]: bit t set where row w attends to token t.  page[w] is set
+// to the chunk's log2-sum-exp.
+template <int D, int WR>
+__device__ __forceinline__ void rows_chunk(RowState<D, WR>& st, const float (*qs)[D], const float (*ks)[D + 4],
+                                           const float (*vs)[D + 4], const uint32_t (&seen)[WR], float scale_log2,
+                                           float (&page)[WR], int lane) {
+  constexpr int VEC = D / 32;
   const int t = lane & 15, c0 = (lane >> 4) * (D / 2);
-  float s[kWR];
+  float s[WR];
 #pragma unroll
-  for (int w = 0; w < kWR; ++w) s[w] = 0.f;
-#pragma unroll 8
-  for (int c = 0; c < D / 2; ++c) {
-    const float k = ks[t][c0 + c];
+  for (int w = 0; w < WR; ++w) s[w] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c < c0 + D / 2; c += 4) {
+    const float4 k = *reinterpret_cast<const float4*>(&ks[t][c]);
 #pragma unroll
-    for (int w = 0; w < kWR; ++w) s[w] = fmaf(qs[w][c0 + c], k, s[w]);
+    for (int w = 0; w < WR; ++w) {
+      const float4 q = *reinterpret_cast<const float4*>(&qs[w][c]);
+      s[w] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[w]))));
+    }
   }
 #pragma unroll
-  for (int w = 0; w < kWR; ++w) {
+  for (int w = 0; w < WR; ++w) {
     s[w] += __shfl_xor_sync(0xffffffffu, s[w], 16);
     s[w] = (seen[w] >> t) & 1u ? s[w] * scale_log2 : -INFINITY;
     float mx = s[w];
@@ -70,7 +83,7 @@ __device__ __forceinline__ void rows_chunk(RowState<D>& st, const float (*qs)[D]
     float sum = p;
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    page[w] = seen[w] ? mx + log2f(sum) : -INFINITY;
+    page[w] = seen[w] ? mx + __log2f(sum) : -INFINITY;
     // join: the chunk's state relative to its own maximum, the rows' to theirs
     const float mn = fmaxf(st.m[w], mx), mb = mn == -INFINITY ? 0.f : mn;
     const float fo = exp2_approx(st.m[w] - mb), fp = exp2_approx(mp - mb);
@@ -78,112 +91,183 @@ __device__ __forceinline__ void rows_chunk(RowState<D>& st, const float (*qs)[D]
     st.l[w] = st.l[w] * fo + sum * (mx == -INFINITY ? 0.f : fp);
     s[w] = mx == -INFINITY ? 0.f : p * fp;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) st.o[w][i] *= fo;
+    for (int i = 0; i < VEC; ++i) st.o[w][i] *= fo;
   }
-#pragma unroll 4
-  for (int tt = 0; tt < kPage; ++tt) {
-    float v[D / 32];
+  uint32_t any = 0u;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) v[i] = vs[tt][32 * i + lane];
+  for (int w = 0; w < WR; ++w) any |= seen[w];
+  for (; any; any &= any - 1u) {   // tokens that a row of the warp sees (uniform over the warp)
+    const int tt = __ffs((int)any) - 1;
+    float v[VEC];
+    load_vec(v, &vs[tt][VEC * lane]);
 #pragma unroll
-    for (int w = 0; w < kWR; ++w) {
+    for (int w = 0; w < WR; ++w) {
       const float p = __shfl_sync(0xffffffffu, s[w], tt);
-      if ((seen[w] >> tt) & 1u) {   // uniform over the warp
+      if ((seen[w] >> tt) & 1u) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) st.o[w][i] = fmaf(p, v[i], st.o[w][i]);
+        for (int i = 0; i < VEC; ++i) st.o[w][i] = fmaf(p, v[i], st.o[w][i]);
       }
     }
   }
 }
 
-// The CTA's query rows r0 .. r0 + n - 1 in fp32 (zeros past the live rows).
-template <int D>
-__device__ __forceinline__ void load_queries(const TreeArgs& a, int b, int h, int r0, int n, int live, float (*qs)[D]) {
-  for (int i = threadIdx.x; i < n * D; i += blockDim.x) {
-    const int r = r0 + i / D, t = r / a.G, g = r % a.G;
-    qs[i / D][i % D] =
-        r < live ? __bfloat162float(a.q[(((size_t)b * a.T + t) * a.Hq + (size_t)h * a.G + g) * D + i % D]) : 0.f;
+// 8 bf16 as fp32.
+__device__ __forceinline__ void widen8(uint4 x, float* o) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __uint_as_float(u[i] << 16);
+    o[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
 
-// ----------------------------------------------------------------------------- tail, tree and merge
-// Grid (ceil(R / kMRows), Hkv, B), 4 warps of kWR rows: the staged tail and the
-// drafted tokens in chunks of 16 on the CUDA cores (K and V of a token that a
-// row does not see never reach the row, so a branch may hold infinities or NaN
-// without touching its siblings), then the splits in ascending order.
-constexpr int kMRows = 4 * kWR;
-template <int D>
-__global__ void __launch_bounds__(128) tree_merge_kernel(const TreeArgs a) {
-  __shared__ float qs[kMRows][D];
-  __shared__ float kvs[2][kPage][D + 1];
-  const int r0 = blockIdx.x * kMRows, h = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+constexpr int kMergeWarps = 8;
+template <int D, int WR>
+__global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const TreeArgs a) {
+  constexpr int ROWS = kMergeWarps * WR, VEC = D / 32;
+  __shared__ __align__(16) float qs[ROWS][D];
+  __shared__ __align__(16) float kvs[2][kPage][D + 4];
+  const int r0 = blockIdx.x * ROWS, h = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rw = r0 + warp * WR;
   const SeqView v = seq_view(a, b);
   const int live = v.nodes * a.G;
-  load_queries<D>(a, b, h, r0, kMRows, live, qs);
-  RowState<D> st;
-  row_state_init(st);
-  if (r0 < live) {
-    const int staged = v.len - v.blocks * kPage;   // <= 0 for per-token formats
-    const int su = unit_tokens(a.fmt), off = v.blocks * kPage % su;   // rows of staging before the first of them
-    const int cs = staged > 0 ? (staged + kPage - 1) / kPage : 0;
-    const int cn = a.kv[0] ? (v.nodes + kPage - 1) / kPage : 0;
+  RowState<D, WR> st;
+#pragma unroll
+  for (int w = 0; w < WR; ++w) {
+    st.m[w] = -INFINITY;
+    st.l[w] = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) st.o[w][i] = 0.f;
+  }
+  const int staged = staged_tokens(a, v), cs = (staged + kPage - 1) / kPage;
+  const int cn = a.kv[0] ? (v.nodes + kPage - 1) / kPage : 0;
+  if (r0 < live && cs + cn > 0) {
+    for (int i = threadIdx.x; i < ROWS * D / 8; i += 32 * kMergeWarps) {
+      const int r = r0 + i / (D / 8), t = r / a.G;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (r < live)
+        x = *reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + t) * a.Hq + (size_t)h * a.G + r % a.G) * D + i % (D / 8) * 8);
+      widen8(x, &qs[i / (D / 8)][i % (D / 8) * 8]);
+    }
+    const int su = unit_tokens(a.fmt), off = v.blocks * kPage % su;   // rows of staging before the first of the tail
+    uint64_t sees[WR];
+#pragma unroll
+    for (int w = 0; w < WR; ++w) {
+      const int r = rw + w, t = r / a.G;
+      sees[w] = r >= live ? 0ull : a.mask ? a.mask[(size_t)b * a.mask_stride + t] : (2ull << t) - 1ull;
+    }
     for (int ch = 0; ch < cs + cn; ++ch) {
       const bool tail = ch < cs;
       const int t0 = kPage * (tail ? ch : ch - cs), n = min(kPage, (tail ? staged : v.nodes) - t0);
       __syncthreads();
-      for (int i = threadIdx.x; i < 2 * n * D; i += blockDim.x) {
-        const int role = i / (n * D), t = i / D % n, c = i % D;
-        kvs[role][t][c] = tail ? a.staging[((((size_t)b * a.Hkv + h) * 2 + role) * su + off + t0 + t) * D + c]
-                               : __bfloat162float(a.kv[role][(((size_t)b * a.T + t0 + t) * a.Hkv + h) * D + c]);
+      for (int i = threadIdx.x; i < 2 * n * D / 8; i += 32 * kMergeWarps) {
+        const int role = i / (n * D / 8), t = i / (D / 8) % n, c = i % (D / 8) * 8;
+        float x[8];
+        if (tail) {
+          const float* src = a.staging + ((((size_t)b * a.Hkv + h) * 2 + role) * su + off + t0 + t) * D + c;
+          *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+          *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(src + 4);
+        } else {
+          widen8(*reinterpret_cast<const uint4*>(a.kv[role] + (((size_t)b * a.T + t0 + t) * a.Hkv + h) * D + c), x);
+        }
+        *reinterpret_cast<float4*>(&kvs[role][t][c]) = *reinterpret_cast<const float4*>(x);
+        *reinterpret_cast<float4*>(&kvs[role][t][c + 4]) = *reinterpret_cast<const float4*>(x + 4);
       }
       __syncthreads();
-      uint32_t seen[kWR];
-      float page[kWR];
+      uint32_t seen[WR], any = 0u;
 #pragma unroll
-      for (int w = 0; w < kWR; ++w) {
-        const int r = r0 + warp * kWR + w, t = r / a.G;
-        uint32_t bits = (1u << n) - 1u;
-        if (!tail)
-          bits &= (uint32_t)((a.mask ? (r < live ? a.mask[(size_t)b * a.mask_stride + t] : 0ull) : (2ull << t) - 1ull) >> t0);
-        seen[w] = r < live ? bits : 0u;
+      for (int w = 0; w < WR; ++w) {
+        const uint32_t all = (1u << n) - 1u;
+        seen[w] = rw + w >= live ? 0u : tail ? all : (uint32_t)(sees[w] >> t0) & all;
+        any |= seen[w];
       }
-      rows_chunk<D>(st, qs + warp * kWR, kvs[0], kvs[1], seen, a.scale_log2, page, lane);
+      if (!any) continue;   // no row of the warp sees the chunk
+      float page[WR];
+      rows_chunk<D, WR>(st, qs + warp * WR, kvs[0], kvs[1], seen, a.scale_log2, page, lane);
       if (tail && a.page_lse && lane == 0)
 #pragma unroll
-        for (int w = 0; w < kWR; ++w) {
-          const int r = r0 + warp * kWR + w;
-          if (r < live) page_lse_row(a, b, h, r)[v.blocks + ch] = page[w] * kLn2;
-        }
+        for (int w = 0; w < WR; ++w)
+          if (rw + w < live) page_lse_row(a, b, h, rw + w)[v.blocks + ch] = page[w] * kLn2;
+    }
+  }
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the split kernel's partial states
+  const int nr = min(WR, live - rw);   // live rows of the warp
+  if (nr > 0 && v.blocks > 0) {
+    const size_t base = ((size_t)b * a.Hkv + h) * a.S * a.R + rw;
+    float M[WR];
+#pragma unroll
+    for (int w = 0; w < WR; ++w) M[w] = st.m[w];
+    for (int s = lane; s < a.S; s += 32)
+#pragma unroll
+      for (int w = 0; w < WR; ++w)
+        if (w < nr) M[w] = fmaxf(M[w], a.part_ml[base + (size_t)s * a.R + w].x);
+#pragma unroll
+    for (int w = 0; w < WR; ++w) {
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) M[w] = fmaxf(M[w], __shfl_xor_sync(0xffffffffu, M[w], x));
+      const float f = M[w] == -INFINITY ? 0.f : exp2_approx(st.m[w] - M[w]);
+      st.m[w] = M[w];
+      st.l[w] *= f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) st.o[w][i] *= f;
+    }
+    for (int s0 = 0; s0 < a.S; s0 += 32) {
+      float wt[WR];   // split s0 + lane's weight
+#pragma unroll
+      for (int w = 0; w < WR; ++w) {
+        const float2 ml = s0 + lane < a.S && w < nr ? a.part_ml[base + (size_t)(s0 + lane) * a.R + w] : make_float2(-INFINITY, 0.f);
+        wt[w] = ml.x == -INFINITY ? 0.f : exp2_approx(ml.x - M[w]);
+        float sum = wt[w] * ml.y;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        st.l[w] += sum;
+      }
+      const int n = min(32, a.S - s0);
+      constexpr int U = WR >= 4 ? 2 : 8;   // splits in flight
+      for (int s = 0; s < n; s += U) {
+        float x[U][WR][VEC], f[U][WR];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int w = 0; w < WR; ++w) {
+            f[k][w] = s + k < n ? __shfl_sync(0xffffffffu, wt[w], (s + k) & 31) : 0.f;
+            if (f[k][w] != 0.f) load_vec(x[k][w], a.part_o + (base + (size_t)(s0 + s + k) * a.R + w) * D + VEC * lane);
+          }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int w = 0; w < WR; ++w)
+            if (f[k][w] != 0.f)
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) st.o[w][i] = fmaf(f[k][w], x[k][w][i], st.o[w][i]);
+      }
     }
   }
 #pragma unroll
-  for (int w = 0; w < kWR; ++w) {
-    const int r = r0 + warp * kWR + w;
+  for (int w = 0; w < WR; ++w) {
+    const int r = rw + w;
     if (r >= a.R) continue;
-    const size_t base = ((size_t)b * a.Hkv + h) * a.S * a.R + r;
-    if (r < live)
-      for (int s = 0; s < a.S; ++s) {
-        const size_t row = base + (size_t)s * a.R;
-        const float2 ml = a.part_ml[row];
-        if (ml.x == -INFINITY) continue;   // nothing in this split
-        const float mn = fmaxf(st.m[w], ml.x);
-        const float f0 = exp2_approx(st.m[w] - mn), f1 = exp2_approx(ml.x - mn);
-        st.m[w] = mn;
-        st.l[w] = st.l[w] * f0 + ml.y * f1;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          st.o[w][i] = fmaf(a.part_o[row * D + 32 * i + lane], f1, st.o[w][i] * f0);
-      }
     const size_t o = ((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G;
     const bool empty = st.m[w] == -INFINITY;
+    float y[VEC];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const float x = empty ? 0.f : st.o[w][i] / st.l[w];
-      if (a.out_dtype == KVQ_BF16) static_cast<__nv_bfloat16*>(a.out)[o * D + 32 * i + lane] = __float2bfloat16_rn(x);
-      else static_cast<float*>(a.out)[o * D + 32 * i + lane] = x;
+    for (int i = 0; i < VEC; ++i) y[i] = empty ? 0.f : st.o[w][i] / st.l[w];
+    if (a.out_dtype == KVQ_BF16) {
+      uint32_t u[VEC / 2];
+#pragma unroll
+      for (int i = 0; i < VEC; i += 2) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(y[i], y[i + 1]);
+        u[i / 2] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + o * D + VEC * lane);
+      if (VEC == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(u[0], u[VEC / 2 - 1]);
+      else dst[0] = u[0];
+    } else {
+      float* dst = static_cast<float*>(a.out) + o * D + VEC * lane;
+      *reinterpret_cast<typename Vec<VEC>::T*>(dst) = *reinterpret_cast<const typename Vec<VEC>::T*>(y);
     }
-    if (a.lse && lane == 0) a.lse[o] = empty ? -INFINITY : (st.m[w] + log2f(st.l[w])) * kLn2;
+    if (a.lse && lane == 0) a.lse[o] = empty ? -INFINITY : (st.m[w] + __log2f(st.l[w])) * kLn2;
   }
 }
 
@@ -245,8 +329,20 @@ static cudaError_t tree_launch_d(const TreeArgs& a, cudaStream_t st) {
   void* args[] = {const_cast<TreeArgs*>(&a)};
   e = cudaLaunchKernel(k.fn, dim3(a.S, a.Hkv * ((a.R + kTreeRows - 1) / kTreeRows), a.B), dim3(k.threads), args, k.smem, st);
   if (e != cudaSuccess) return e;
-  tree_merge_kernel<D><<<dim3((a.R + kMRows - 1) / kMRows, a.Hkv, a.B), 128, 0, st>>>(a);
-  return cudaGetLastError();
+  // The merge is launched while the last split CTAs run (programmatic dependent launch).  Where there are few
+  // rows a warp takes one, else four, which share the loads of the tail's and the nodes' K and V.
+  const bool few = (long long)a.B * a.Hkv * a.R <= 152 * 8 * 8;
+  const int rows = kMergeWarps * (few ? 1 : 4);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.R + rows - 1) / rows, a.Hkv, a.B);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 1>, a) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, 4>, a);
 }
 cudaError_t tree_launch(const TreeArgs& a, int D, cudaStream_t st) {
   return D == 64 ? tree_launch_d<64>(a, st) : tree_launch_d<128>(a, st);

@@ -67,6 +67,10 @@ __device__ __forceinline__ SeqView seq_view(const TreeArgs& a, int b) {
   v.nodes = a.nodes ? min(max(a.nodes[b], 0), a.T) : a.T;
   return v;
 }
+// Visible tokens that wait in staging (the merge kernel's).
+__device__ __forceinline__ int staged_tokens(const TreeArgs& a, const SeqView& v) {
+  return page_format(a.fmt) ? max(v.len - v.blocks * kPage, 0) : 0;
+}
 __device__ __forceinline__ float* page_lse_row(const TreeArgs& a, int b, int h, int r) {
   return a.page_lse + (((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * a.P;
 }

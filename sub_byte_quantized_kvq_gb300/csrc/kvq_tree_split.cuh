@@ -546,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nmt = (a.R + kM - 1) / kM;
   const int split = blockIdx.x, h = blockIdx.y / nmt, r0 = (blockIdx.y % nmt) * kM, b = blockIdx.z;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const SeqView v = seq_view(a, b);
   const int live = min(v.nodes * a.G, a.R), rows = min(kM, live - r0), r_end = min(r0 + kM, a.R);
   if (split == 0 && blockIdx.y == 0 && tid == 0 && a.seq_lens[b] > a.max_seq_len) atomicOr(a.status, KVQ_STATUS_SEQ_TOO_LONG);
@@ -553,7 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   const int n_tiles = rows > 0 && p1 > p0 ? (p1 - p0 + PAGES - 1) / PAGES : 0;
   if (a.page_lse) {
     fill_page_lse(a, b, h, max(r0, live), r_end, p0, pn);
-    if (rows > 0) fill_page_lse(a, b, h, r0, r0 + rows, max(p0, p1), pn);
+    // (the staged pages of live rows are the merge kernel's)
+    if (rows > 0) fill_page_lse(a, b, h, r0, r0 + rows, max(p0, v.blocks + (staged_tokens(a, v) + kPage - 1) / kPage), pn);
   }
   const size_t part0 = (((size_t)b * a.Hkv + h) * a.S + split) * a.R + r0;
   if (n_tiles == 0) {

@@ -49,7 +49,7 @@ def test_tree_attention_refusals(kvq):
                                                  kvq.KVQ_ERR_CAPACITY)
     c, k = cfg_of(kvq), cache_of(kvq)
     assert tree(kvq, c, k) == WORKSPACE                 # all else is right
-    for bad in (dict(q=None), dict(q=FAKE + 2), dict(out=None), dict(od=kvq.KVQ_F16), dict(ws=None), dict(ws=FAKE + 8),
+    for bad in (dict(q=None), dict(q=FAKE + 2), dict(out=None), dict(out=FAKE + 4), dict(od=kvq.KVQ_F16), dict(ws=None), dict(ws=FAKE + 8),
                 dict(k=None), dict(v=None), dict(k=FAKE + 4), dict(k=None, v=None, mask=FAKE), dict(per_seq=2), dict(Hq=0),
                 dict(Hq=30), dict(T=0), dict(max_len=-1), dict(splits=-1), dict(scale=float("inf")),
                 dict(scale=float("nan"))):
