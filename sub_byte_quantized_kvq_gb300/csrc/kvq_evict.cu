@@ -1,63 +1,74 @@
 // kvq_evict.cu -- the attention mass of the cache's pages, and eviction by it.
+#include <mutex>
+
 #include "kvq_tree.cuh"
 
 namespace kvq {
 
 // ----------------------------------------------------------------------------- page mass
 // out[b][p] = decay * in[b][p] + sum over the marked nodes t and heads h of
-// e^(page_lse[b][t][h][p] - lse[b][t][h]); one thread a page, rows in ascending
-// order.  A row without a token (lse = -inf) adds nothing.
-__global__ void __launch_bounds__(128) page_mass_kernel(const float* __restrict__ lse, const float* __restrict__ page_lse,
-                                                        const uint64_t* __restrict__ nodes, float decay, const float* in,
-                                                        float* out, int T, int Hq, int P, int ppsm) {
-  const int p = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y;
-  if (p >= ppsm) return;
-  const uint64_t on = nodes ? nodes[b] : ~0ull;
-  float w = 0.f;
-  if (p < P)
-    for (int t = 0; t < T; ++t) {
-      if (!((on >> t) & 1ull)) continue;
-      for (int h = 0; h < Hq; ++h) {
-        const size_t r = ((size_t)b * T + t) * Hq + h;
-        const float z = lse[r];
-        if (z != -INFINITY) w += __expf(page_lse[r * P + p] - z);
+// e^(page_lse[b][t][h][p] - lse[b][t][h]).
+//
+// One pass over page_lse, which is all there is to read: a CTA takes 128 pages
+// of a sequence, its 8 warps every 8th marked (node, head) row, four coalesced
+// loads of four rows in flight each; the warps' sums are added in ascending
+// order, so results do not depend on timing.  A row without a token (lse =
+// -inf) adds nothing.
+constexpr int kMassWarps = 8, kMassPages = 128, kMassPer = kMassPages / 32;
+__global__ void __launch_bounds__(32 * kMassWarps) page_mass_kernel(const float* __restrict__ lse,
+                                                                    const float* __restrict__ page_lse,
+                                                                    const uint64_t* __restrict__ nodes, float decay,
+                                                                    const float* in, float* out, int T, int Hq, int P,
+                                                                    int ppsm) {
+  __shared__ int marked[64];
+  __shared__ float part[kMassWarps][kMassPages];
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, p0 = blockIdx.x * kMassPages + lane;
+  const uint64_t on = (nodes ? nodes[b] : ~0ull) & (T == 64 ? ~0ull : (1ull << T) - 1ull);
+  if (threadIdx.x < T && ((on >> threadIdx.x) & 1ull)) marked[__popcll(on & ((1ull << threadIdx.x) - 1ull))] = threadIdx.x;
+  __syncthreads();
+  const int n = blockIdx.x * kMassPages < P ? __popcll(on) * Hq : 0;
+  float w[kMassPer] = {};
+  constexpr int U = 4;
+  for (int i = warp; i < n; i += U * kMassWarps) {
+    float z[U], x[U][kMassPer];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int j = i + k * kMassWarps;
+      z[k] = -INFINITY;
+      if (j < n) {
+        const size_t r = ((size_t)b * T + marked[j / Hq]) * Hq + j % Hq;
+        z[k] = lse[r];
+#pragma unroll
+        for (int c = 0; c < kMassPer; ++c) x[k][c] = p0 + 32 * c < P ? page_lse[r * P + p0 + 32 * c] : -INFINITY;
       }
     }
-  const size_t i = (size_t)b * ppsm + p;
-  out[i] = fmaf(decay, in[i], w);
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (z[k] != -INFINITY)
+#pragma unroll
+        for (int c = 0; c < kMassPer; ++c) w[c] += __expf(x[k][c] - z[k]);
+  }
+#pragma unroll
+  for (int c = 0; c < kMassPer; ++c) part[warp][32 * c + lane] = w[c];
+  __syncthreads();
+  const int p = blockIdx.x * kMassPages + threadIdx.x;
+  if (threadIdx.x < kMassPages && p < ppsm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMassWarps; ++k) sum += part[k][threadIdx.x];
+    const size_t i = (size_t)b * ppsm + p;
+    out[i] = fmaf(decay, in[i], sum);
+  }
 }
 
 cudaError_t page_mass_launch(const float* lse, const float* page_lse, const uint64_t* nodes, float decay, const float* in,
                              float* out, int B, int T, int Hq, int P, int ppsm, cudaStream_t st) {
-  page_mass_kernel<<<dim3((ppsm + 127) / 128, B), 128, 0, st>>>(lse, page_lse, nodes, decay, in, out, T, Hq, P, ppsm);
+  page_mass_kernel<<<dim3((ppsm + kMassPages - 1) / kMassPages, B), 32 * kMassWarps, 0, st>>>(lse, page_lse, nodes, decay, in,
+                                                                                             out, T, Hq, P, ppsm);
   return cudaGetLastError();
 }
 
 // ----------------------------------------------------------------------------- eviction
-constexpr int kEvThreads = 1024;
-
-// Exclusive prefix sum of x over the CTA; `total` gets the sum.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += y;
-  }
-  __syncthreads();   // warp_sums may still be read by the previous call
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < kEvThreads / 32; ++w) {
-    const int y = warp_sums[w];
-    before += w < warp ? y : 0;
-    total += y;
-  }
-  return before + s - x;
-}
-
 // The order of page masses as unsigned keys: larger mass, larger key; -0 as +0,
 // NaN below everything.
 __device__ __forceinline__ uint32_t mass_key(float x) {
@@ -66,21 +77,27 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
   return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// One CTA per sequence.  The row and its masses are first copied to shared
-// memory, so the outputs may be the inputs.  A radix select over 8-bit digits
-// finds the key of the last free unit to stay; ties go to the lowest index.
-__global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
+// One CTA per sequence; latency is all that counts (two words a page to read
+// and to write), so barriers are few.  The row and its masses are first copied
+// to shared memory, so the outputs may be the inputs.  A radix select over
+// 8-bit digits (a histogram by the CTA, its scan by one warp) finds the key of
+// the last free unit to stay; ties go to the lowest index.  One scan over the
+// threads' consecutive units then gives every page its place.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_kernel(const EvictArgs a) {
   extern __shared__ uint8_t dyn[];
   int32_t* row = reinterpret_cast<int32_t*>(dyn);
   float* mass = reinterpret_cast<float*>(row + a.ppsm);
-  __shared__ int hist[256], sums[kEvThreads / 32], pick[2];
-  const int b = blockIdx.x, tid = threadIdx.x;
+  constexpr int W = THREADS / 32;
+  __shared__ int hist[2][256], sums[W], pick[2];
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const size_t at = (size_t)b * a.ppsm;
-  for (int i = tid; i < a.ppsm; i += kEvThreads) {
+  const int L = a.lens_in[b];
+  for (int i = tid; i < a.ppsm; i += THREADS) {
     row[i] = a.table_in[at + i];
     mass[i] = a.mass_in[at + i];
   }
-  const int L = a.lens_in[b];
+  for (int i = tid; i < 256; i += THREADS) hist[1][i] = 0;   // the first digit's (d = 3)
   const int len = min(max(L, 0), a.ppsm * kPage);
   const int used = (len + kPage - 1) / kPage, full = len / (kPage * a.unit);   // full units
   const int first = a.sink, last = full - a.recent;                            // free units: [first, last)
@@ -92,63 +109,77 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   };
   const bool evict = full > a.keep;
   uint32_t cut = 0u;
-  int need = 0;   // units with the cut's own key that stay
-  if (evict) {
-    need = a.keep - a.sink - a.recent;   // free units that stay; >= 0, and fewer than there are
-    for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kEvThreads) hist[i] = 0;
-      __syncthreads();
-      for (int u = first + tid; u < last; u += kEvThreads) {
-        const uint32_t k = key_of(u);
-        if (shift == 24 || (k >> (shift + 8)) == (cut >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
-      }
-      __syncthreads();
-      // digits in descending order, one a thread: the first whose running count reaches `need`
-      int total;
-      const int n = tid < 256 ? hist[255 - tid] : 0;
-      const int before = block_scan(n, sums, total);
-      if (tid < 256 && before < need && before + n >= need) {
-        pick[0] = 255 - tid;
-        pick[1] = need - before;
-      }
-      __syncthreads();
-      cut |= (uint32_t)pick[0] << shift;
-      need = pick[1];
-      __syncthreads();
-    }
-    if (a.keep == a.sink + a.recent) cut = 0xFFFFFFFFu;
-  }
-  // each thread's consecutive units, so that ranks follow the page order
-  const int per = (full + kEvThreads - 1) / kEvThreads, u0 = min(tid * per, full), u1 = min(u0 + per, full);
-  auto is_free = [&](int u) { return evict && u >= first && u < last; };
-  int ties = 0, total, n_kept;
-  for (int u = u0; u < u1; ++u) ties += is_free(u) && key_of(u) == cut;
-  const int tie0 = block_scan(ties, sums, total);
-  int kept = 0, tie = tie0;
-  for (int u = u0; u < u1; ++u) {
-    if (!is_free(u)) ++kept;
-    else {
+  int need = evict ? a.keep - a.sink - a.recent : 0;   // free units that stay: >= 0, and fewer than there are
+  if (evict && need == 0) cut = 0xFFFFFFFFu;           // (above every key)
+  // after each digit, `need` is the number of units to stay among those whose key starts as the cut does
+  for (int d = 3; d >= 0 && need > 0; --d) {
+    int* h = hist[d & 1];
+    const int shift = 8 * d;
+    for (int u = first + tid; u < last; u += THREADS) {
       const uint32_t k = key_of(u);
-      kept += k > cut || (k == cut && tie++ < need);
+      if (d == 3 || (k >> (shift + 8)) == (cut >> (shift + 8))) atomicAdd(&h[(k >> shift) & 255u], 1);
     }
+    for (int i = tid; i < 256; i += THREADS) hist[(d & 1) ^ 1][i] = 0;
+    __syncthreads();
+    if (warp == 0) {   // lane: 8 digits from 255 - 8 lane down; the first digit whose running count reaches `need`
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += c[i] = h[255 - 8 * lane - i];
+      int before = sum;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, x);
+        if (lane >= x) before += y;
+      }
+      before -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < need && before + c[i] >= need) {
+          pick[0] = 255 - 8 * lane - i;
+          pick[1] = need - before;
+        }
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    cut |= (uint32_t)pick[0] << shift;
+    need = pick[1];   // (written again only after the next digit's barrier)
   }
-  const int kept0 = block_scan(kept, sums, n_kept);
-  const int gone = full - n_kept, dropped = gone * a.unit;
-  int k = kept0, e = u0 - kept0;
-  tie = tie0;
+  // each thread's consecutive units, so that ranks follow the page order: those that stay for sure
+  // (low half of the count) and those with the cut's own key (high half), of which the first `need` stay
+  const int per = (full + THREADS - 1) / THREADS, u0 = min(tid * per, full), u1 = min(u0 + per, full);
+  auto kind = [&](int u) -> uint32_t {
+    if (!evict || u < first || u >= last) return 1u;
+    const uint32_t k = key_of(u);
+    return k > cut ? 1u : k == cut ? 0x10000u : 0u;
+  };
+  uint32_t count = 0u;
+  for (int u = u0; u < u1; ++u) count += kind(u);
+  uint32_t before = count;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, before, x);
+    if (lane >= x) before += y;
+  }
+  if (lane == 31) sums[warp] = (int)before;
+  __syncthreads();
+  uint32_t other = lane < warp ? (uint32_t)sums[lane < W ? lane : 0] : 0u;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) other += __shfl_xor_sync(0xffffffffu, other, x);
+  before += other - count;
+  const int dropped = evict ? (full - a.keep) * a.unit : 0;
+  int ties = (int)(before >> 16), kept = (int)(before & 0xFFFFu) + min(ties, need), gone = u0 - kept;
   for (int u = u0; u < u1; ++u) {
-    bool stay = !is_free(u);
-    if (!stay) {
-      const uint32_t key = key_of(u);
-      stay = key > cut || (key == cut && tie++ < need);
-    }
-    const int to = stay ? k++ * a.unit : a.ppsm - dropped + e++ * a.unit;
+    const uint32_t x = kind(u);
+    const bool stay = x == 1u || (x != 0u && ties < need);
+    ties += x >> 16;
+    const int to = stay ? kept++ * a.unit : a.ppsm - dropped + gone++ * a.unit;
     for (int j = 0; j < a.unit; ++j) {
       a.table_out[at + to + j] = row[u * a.unit + j];
       a.mass_out[at + to + j] = stay ? mass[u * a.unit + j] : 0.f;
     }
   }
-  for (int i = full * a.unit + tid; i < a.ppsm; i += kEvThreads) {   // the partial unit, then unused entries
+  for (int i = full * a.unit + tid; i < a.ppsm; i += THREADS) {   // the partial unit, then unused entries
     a.table_out[at + i - dropped] = row[i];
     a.mass_out[at + i - dropped] = i < used ? mass[i] : 0.f;
   }
@@ -158,12 +189,32 @@ __global__ void __launch_bounds__(kEvThreads) evict_kernel(const EvictArgs a) {
   }
 }
 
+// A row beyond 48 KB of shared memory needs the kernel's attribute, set once per device.
+static cudaError_t allow_long_rows() {
+  static std::mutex mutex;
+  static bool done[64] = {};
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (dev < 64 && done[dev]) return cudaSuccess;
+  const cudaError_t f = cudaFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel<1024>),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxPages * 8);
+  if (f == cudaSuccess && dev < 64) done[dev] = true;
+  return f;
+}
+
 cudaError_t evict_launch(const EvictArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)a.ppsm * 8;
-  const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(evict_kernel),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxPages * 8);
-  if (e != cudaSuccess) return e;
-  evict_kernel<<<a.B, kEvThreads, smem, st>>>(a);
+  if (a.ppsm <= 1024) {   // fewer warps, shorter barriers
+    evict_kernel<256><<<a.B, 256, smem, st>>>(a);
+  } else {
+    if (smem > 32 * 1024) {
+      const cudaError_t e = allow_long_rows();
+      if (e != cudaSuccess) return e;
+    }
+    evict_kernel<1024><<<a.B, 1024, smem, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -292,7 +292,8 @@ int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms) {
   const long long tiles = (max_seq_len + kPage * kTreeTilePages - 1) / (kPage * kTreeTilePages);
   const long long units = (long long)B * Hkv * ((R + kTreeRows - 1) / kTreeRows);
   long long best = 1, cost = -1;
-  for (long long s = 1; s <= std::min<long long>(std::max<long long>(tiles, 1), 256); ++s) {
+  const long long most = std::min({std::max(tiles, 1ll), (8ll * sms + units - 1) / units, 256ll});   // (never over 8 waves)
+  for (long long s = 1; s <= most; ++s) {
     const long long c = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
     if (cost < 0 || c < cost) {
       cost = c;

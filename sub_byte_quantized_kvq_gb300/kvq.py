@@ -328,19 +328,39 @@ def kvq_decode_attention_noalloc(cache: QuantizedKVCache, q: torch.Tensor, softm
 KVQ_TREE_MAX_NODES = 64
 
 
-def _check_on(device: torch.device, *tensors):
-    """Every tensor (None apart) lies on `device`, a CUDA device."""
+# These calls are short, so their binding is lean: the checks read each tensor's
+# properties once, and pointers go to ctypes as plain integers.
+def _check_on(index: int, *tensors):
+    """Every tensor (None apart) lies on CUDA device `index`."""
     for t in tensors:
-        if t is not None and (t.device != device or not t.is_cuda):
-            raise ValueError(f"a tensor on {t.device} beside a cache on {device}")
+        if t is not None and (index < 0 or t.get_device() != index):
+            raise ValueError(f"a tensor on {t.device} beside a cache on CUDA device {index}")
 
 
-def _call(device: torch.device, stream, f, *args) -> int:
-    """f(*args, stream) with `device` current; stream None is that device's current stream."""
-    if device.index == torch.cuda.current_device():
-        return f(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return f(*args, _stream(stream))
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _call(what: str, index: int, stream, *args):
+    """The library's function `what` with `args` and the stream, device `index` current; stream None
+    is that device's current stream."""
+    f = getattr(_lib or lib(), what)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = f(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, raw)
+    if status != KVQ_OK:
+        raise KVQError(status, what)
+
+
+def _refs(cache: "QuantizedKVCache"):
+    """References to the cache's C structures, and its device."""
+    r = cache.__dict__.get("_c_refs")
+    if r is None:
+        r = cache._c_refs = (ctypes.byref(cache.cfg), ctypes.byref(cache.c), cache.pool.get_device())
+    return r
 
 
 def _scratch(t: torch.Tensor, stream) -> torch.Tensor:
@@ -391,36 +411,38 @@ def kvq_tree_attention(cache: QuantizedKVCache, q: torch.Tensor, softmax_scale: 
     tree_mask: int64 ancestor words [T] or [num_seqs, T] (None: a chain).  lse fp32
     [num_seqs, T, Hq] and page_lse fp32 [num_seqs, T, Hq, ceil(max_seq_len / 16)] are
     filled when given."""
-    cfg = cache.cfg
-    assert q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 4
-    B, T, Hq, D = q.shape
+    cfg, (pcfg, pcache, index) = cache.cfg, _refs(cache)
+    assert q.dtype is torch.bfloat16 and q.is_contiguous() and q.dim() == 4
+    shape = q.shape
+    B, T, Hq, D = shape
     assert B == cfg.num_seqs and D == cfg.head_dim
     assert (k_tree is None) == (v_tree is None)
-    for t in (k_tree, v_tree):
-        assert t is None or (t.dtype == torch.bfloat16 and t.is_contiguous() and
-                             t.shape == (B, T, cfg.num_kv_heads, D))
+    if k_tree is not None:
+        kv = (B, T, cfg.num_kv_heads, D)
+        assert k_tree.dtype is torch.bfloat16 and k_tree.is_contiguous() and k_tree.shape == kv
+        assert v_tree.dtype is torch.bfloat16 and v_tree.is_contiguous() and v_tree.shape == kv
+    per_seq = 0
     if tree_mask is not None:
-        assert tree_mask.dtype == torch.int64 and tree_mask.is_contiguous()
-        assert tree_mask.shape in ((T,), (B, T))
+        per_seq = tree_mask.dim() - 1
+        assert tree_mask.dtype is torch.int64 and tree_mask.is_contiguous()
+        assert tree_mask.shape == ((B, T) if per_seq else (T,))
     if nodes_per_seq is not None:
-        assert nodes_per_seq.dtype == torch.int32 and nodes_per_seq.is_contiguous() and nodes_per_seq.shape == (B,)
+        assert nodes_per_seq.dtype is torch.int32 and nodes_per_seq.is_contiguous() and nodes_per_seq.shape == (B,)
     if out is None:
-        out = _scratch(torch.empty(q.shape, dtype=out_dtype, device=q.device), stream)
-    assert out.shape == q.shape and out.is_contiguous() and out.dtype in (torch.bfloat16, torch.float32)
+        out = _scratch(torch.empty(shape, dtype=out_dtype, device=q.device), stream)
+    dt = _DTYPE[out.dtype]
+    assert dt != KVQ_F16 and out.is_contiguous() and out.shape == shape
     if lse is not None:
-        assert lse.dtype == torch.float32 and lse.is_contiguous() and lse.shape == (B, T, Hq)
+        assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.shape == (B, T, Hq)
     if page_lse is not None:
         P = (min(max_seq_len, 16 * cfg.pages_per_seq_max) + 15) // 16
-        assert page_lse.dtype == torch.float32 and page_lse.is_contiguous() and page_lse.shape == (B, T, Hq, P)
+        assert page_lse.dtype is torch.float32 and page_lse.is_contiguous() and page_lse.shape == (B, T, Hq, P)
     if workspace is None:
         workspace = _scratch(alloc_tree_workspace(cache, Hq, T, max_seq_len, num_splits), stream)
-    device = cache.pool.device
-    _check_on(device, q, k_tree, v_tree, tree_mask, nodes_per_seq, out, lse, page_lse, workspace)
-    _check(_call(device, stream, lib().kvq_tree_attention, ctypes.byref(cfg), ctypes.byref(cache.c), _ptr(q), Hq, T,
-                 _ptr(k_tree), _ptr(v_tree), _ptr(tree_mask), int(tree_mask is not None and tree_mask.dim() == 2),
-                 _ptr(nodes_per_seq), float(softmax_scale), max_seq_len, num_splits, _ptr(out), _DTYPE[out.dtype],
-                 _ptr(lse), _ptr(page_lse), _ptr(workspace), workspace.numel() * workspace.element_size()),
-           "kvq_tree_attention")
+    _check_on(index, q, k_tree, v_tree, tree_mask, nodes_per_seq, out, lse, page_lse, workspace)
+    _call("kvq_tree_attention", index, stream, pcfg, pcache, q.data_ptr(), Hq, T, _addr(k_tree), _addr(v_tree),
+          _addr(tree_mask), per_seq, _addr(nodes_per_seq), softmax_scale, max_seq_len, num_splits, out.data_ptr(), dt,
+          _addr(lse), _addr(page_lse), workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -431,20 +453,19 @@ def kvq_page_mass(cache: QuantizedKVCache, lse: torch.Tensor, page_lse: torch.Te
     [num_seqs], bit t = node t; None: all).  lse [num_seqs, T, Hq] and page_lse
     [num_seqs, T, Hq, P] as kvq_tree_attention wrote them; mass fp32 [num_seqs,
     pages_per_seq_max], updated in place unless mass_out is given."""
-    cfg = cache.cfg
+    cfg, (pcfg, _, index) = cache.cfg, _refs(cache)
     B, T, Hq, P = page_lse.shape
     if mass_out is None:
         mass_out = mass
-    assert lse.shape == (B, T, Hq) and B == cfg.num_seqs
-    for t in (lse, page_lse, mass, mass_out):
-        assert t.dtype == torch.float32 and t.is_contiguous()
-    assert mass.shape == mass_out.shape == (B, cfg.pages_per_seq_max)
+    f32, shape = torch.float32, (B, cfg.pages_per_seq_max)
+    assert B == cfg.num_seqs and lse.shape == (B, T, Hq) and mass.shape == shape and mass_out.shape == shape
+    assert lse.dtype is f32 and page_lse.dtype is f32 and mass.dtype is f32 and mass_out.dtype is f32
+    assert lse.is_contiguous() and page_lse.is_contiguous() and mass.is_contiguous() and mass_out.is_contiguous()
     if node_mask is not None:
-        assert node_mask.dtype == torch.int64 and node_mask.is_contiguous() and node_mask.shape == (B,)
-    device = cache.pool.device
-    _check_on(device, lse, page_lse, mass, node_mask, mass_out)
-    _check(_call(device, stream, lib().kvq_page_mass, ctypes.byref(cfg), Hq, T, P, _ptr(lse), _ptr(page_lse),
-                 _ptr(node_mask), float(decay), _ptr(mass), _ptr(mass_out)), "kvq_page_mass")
+        assert node_mask.dtype is torch.int64 and node_mask.is_contiguous() and node_mask.shape == (B,)
+    _check_on(index, lse, page_lse, mass, node_mask, mass_out)
+    _call("kvq_page_mass", index, stream, pcfg, Hq, T, P, lse.data_ptr(), page_lse.data_ptr(), _addr(node_mask), decay,
+          mass.data_ptr(), mass_out.data_ptr())
     return mass_out
 
 
@@ -455,23 +476,23 @@ def kvq_evict_pages(cache: QuantizedKVCache, mass: torch.Tensor, keep_pages: int
     """Evict the lightest full pages of every sequence down to keep_pages; returns the int32
     [num_seqs] counts.  Updates cache.page_table, cache.seq_lens and mass in place, each
     unless its output tensor is given."""
-    cfg = cache.cfg
-    shape = (cfg.num_seqs, cfg.pages_per_seq_max)
+    cfg, (pcfg, pcache, index) = cache.cfg, _refs(cache)
+    B = cfg.num_seqs
+    shape = (B, cfg.pages_per_seq_max)
     page_table_out = cache.page_table if page_table_out is None else page_table_out
     seq_lens_out = cache.seq_lens if seq_lens_out is None else seq_lens_out
     mass_out = mass if mass_out is None else mass_out
     if evicted is None:
-        evicted = _scratch(torch.empty(shape[0], dtype=torch.int32, device=cache.device), stream)
-    for t in (mass, mass_out):
-        assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == shape
-    assert page_table_out.dtype == torch.int32 and page_table_out.is_contiguous() and page_table_out.shape == shape
-    for t in (seq_lens_out, evicted):
-        assert t.dtype == torch.int32 and t.is_contiguous() and t.shape == shape[:1]
-    device = cache.pool.device
-    _check_on(device, mass, page_table_out, seq_lens_out, mass_out, evicted)
-    _check(_call(device, stream, lib().kvq_evict_pages, ctypes.byref(cfg), ctypes.byref(cache.c), _ptr(mass), keep_pages,
-                 sink_pages, recent_pages, _ptr(page_table_out), _ptr(seq_lens_out), _ptr(mass_out), _ptr(evicted)),
-           "kvq_evict_pages")
+        evicted = _scratch(torch.empty(B, dtype=torch.int32, device=cache.device), stream)
+    f32, i32 = torch.float32, torch.int32
+    assert mass.dtype is f32 and mass_out.dtype is f32 and mass.is_contiguous() and mass_out.is_contiguous()
+    assert mass.shape == shape and mass_out.shape == shape and page_table_out.shape == shape
+    assert page_table_out.dtype is i32 and seq_lens_out.dtype is i32 and evicted.dtype is i32
+    assert page_table_out.is_contiguous() and seq_lens_out.is_contiguous() and evicted.is_contiguous()
+    assert seq_lens_out.shape == (B,) and evicted.shape == (B,)
+    _check_on(index, mass, page_table_out, seq_lens_out, mass_out, evicted)
+    _call("kvq_evict_pages", index, stream, pcfg, pcache, mass.data_ptr(), keep_pages, sink_pages, recent_pages,
+          page_table_out.data_ptr(), seq_lens_out.data_ptr(), mass_out.data_ptr(), evicted.data_ptr())
     return evicted
 
 
