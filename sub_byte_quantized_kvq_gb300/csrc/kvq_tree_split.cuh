@@ -92,6 +92,27 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((unsigned short)v) : "memory");
 }
 
+// The four bytes of a word, each two e2m1 nibbles, as f16x2.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&x)[4]) {
+  asm("{ .reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d; }"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+      : "r"(w));
+}
+// The four bytes of a word, e4m3, as two f16x2.
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& x, uint32_t& y) {
+  asm("{ .reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(x), "=r"(y)
+      : "r"(w));
+}
+
 // Where a page's values go in a swizzled tile.  A row is 64 fp16 (128 bytes);
 // 16-byte chunk k of row r lies at chunk k ^ (r % 8).
 template <int D, int TOK>
@@ -103,11 +124,12 @@ struct KTile {   // rows = tokens, D / 64 row groups
     const int row = kPage * page + t;
     return tile + (c >> 6) * (TOK * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2;
   }
-  // lane's row address of a group of four steps, and of its step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15)
-  __device__ __forceinline__ uint32_t lane_row(int lane) const { return tile + (kPage * page + (lane & 15)) * 128; }
-  __device__ __forceinline__ uint32_t step(uint32_t row, int lane, int s) const {
-    return row + ((((s * 2) ^ (lane & 7)) ^ (lane >> 4)) << 4);
+  // lane's row address of a group of four steps, and of its step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15;
+  // the swizzled chunk (2 s + half) ^ (row % 8) of a 128-byte row)
+  __device__ __forceinline__ uint32_t lane_row(int lane) const {
+    return tile + (kPage * page + (lane & 15)) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
   }
+  __device__ __forceinline__ uint32_t step(uint32_t row, int s) const { return row ^ (s << 5); }
 };
 template <int D, int TOK>
 struct VTile {   // rows = channels, TOK / 64 row groups
@@ -121,7 +143,7 @@ struct VTile {   // rows = channels, TOK / 64 row groups
   __device__ __forceinline__ uint32_t lane_row(int lane) const {
     return tile + (page >> 2) * (D * 128) + (lane & 15) * 128 + ((((page & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
   }
-  __device__ __forceinline__ uint32_t step(uint32_t row, int, int s) const { return row + s * 2048; }
+  __device__ __forceinline__ uint32_t step(uint32_t row, int s) const { return row + s * 2048; }
 };
 
 // The outliers of a side-list, stored over their slots' values: two records at
@@ -192,14 +214,15 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t x[4];
-        fp8_frag(w[k], x);
+        e4m3x4(w[k].x, x[0], x[1]);
+        e4m3x4(w[k].y, x[2], x[3]);
         if (ROLE == 1)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float2 f = __half22float2(u32_as_h2(x[r]));
             x[r] = h2_as_u32(__floats2half2_rn(f.x * sc, f.y * sc));
           }
-        stmatrix4(tile.step(row, lane, k), x);
+        stmatrix4(tile.step(row, k), x);
       }
     }
     return;
@@ -230,11 +253,11 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
         }
         if constexpr (ROLE == 0) {
           int4_k_frag(w[k], S[0], M[0], S[1], M[1], hi, lo);
-          stmatrix4(low.step(lrow, lane, k), lo);
+          stmatrix4(low.step(lrow, k), lo);
         } else {
           int4_v_frag(w[k], S, M, hi, lo);
         }
-        stmatrix4(tile.step(row, lane, k), hi);
+        stmatrix4(tile.step(row, k), hi);
       }
     }
     __syncwarp();
@@ -251,36 +274,37 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
     for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4) {
       const uint4 w4 = lds128(blk + 4 * NS * lane + 4 * s0);
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      // scales as f16x2.  K: of tokens g (registers 0, 2) and g + 8; V: of tokens 2q, 2q + 1 (registers 0, 1) and + 8
       uint32_t sc[4][ROLE == 0 ? 1 : 2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 4; k += 2) {
         const uint32_t at = blk + e2m1_sc_off(D) + 16 * (s0 + k);
-        if constexpr (ROLE == 0) {   // tokens g (registers 0, 2) and g + 8
-          sc[k][0] = lds8(at + g) | (lds8(at + g + 8) << 8);
-        } else {                     // tokens 2q, 2q + 1 (registers 0, 1) and + 8
-          sc[k][0] = lds16(at + 2 * q4);
-          sc[k][1] = lds16(at + 2 * q4 + 8);
+        if constexpr (ROLE == 0) {
+          const uint32_t lo = prmt(lds8(at + g), lds8(at + g + 8), 0x7740u), hi = prmt(lds8(at + 16 + g), lds8(at + 24 + g), 0x7740u);
+          e4m3x4(prmt(lo, hi, 0x5410u), sc[k][0], sc[k + 1][0]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            e4m3x4(prmt(lds16(at + 16 * i + 2 * q4), lds16(at + 16 * i + 2 * q4 + 8), 0x5410u), sc[k + i][0], sc[k + i][1]);
         }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t x[4];
-        e2m1_frag(w[k], x);
+        e2m1x8(w[k], x);
         if constexpr (ROLE == 0) {
-          const __half2 sh = u32_as_h2(e4m3x2_to_f16x2(sc[k][0]));
-          const __half2 h0 = __low2half2(sh), h1 = __high2half2(sh);
+          const __half2 sh = u32_as_h2(sc[k][0]), h0 = __low2half2(sh), h1 = __high2half2(sh);
           x[0] = h2_as_u32(__hmul2(u32_as_h2(x[0]), h0));
           x[1] = h2_as_u32(__hmul2(u32_as_h2(x[1]), h1));
           x[2] = h2_as_u32(__hmul2(u32_as_h2(x[2]), h0));
           x[3] = h2_as_u32(__hmul2(u32_as_h2(x[3]), h1));
         } else {
-          const uint32_t s01 = e4m3x2_to_f16x2(sc[k][0]), s23 = e4m3x2_to_f16x2(sc[k][1]);
-          x[0] = hmul2u(x[0], s01);
-          x[1] = hmul2u(x[1], s01);
-          x[2] = hmul2u(x[2], s23);
-          x[3] = hmul2u(x[3], s23);
+          x[0] = hmul2u(x[0], sc[k][0]);
+          x[1] = hmul2u(x[1], sc[k][0]);
+          x[2] = hmul2u(x[2], sc[k][1]);
+          x[3] = hmul2u(x[3], sc[k][1]);
         }
-        stmatrix4(tile.step(row, lane, k), x);
+        stmatrix4(tile.step(row, k), x);
       }
     }
   } else if constexpr (BLK == kBlkA3) {
@@ -313,7 +337,7 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
           const bool second = ROLE == 0 ? r >= 2 : (r & 1) != 0;
           x[r] = a3_value(w, yw, k, r, second ? sc[k].y : sc[k].x, second ? zp[k].y : zp[k].x);
         }
-        stmatrix4(tile.step(row, lane, k), x);
+        stmatrix4(tile.step(row, k), x);
       }
     }
     patch.store(tile, lane, [&]() { return gblk() + a3_out_off(D); });
@@ -336,7 +360,7 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
         uint32_t x[4];
         if constexpr (ROLE == 0) cb2_k_expand(kc[k], w16, x);
         else cb2_v_expand(vc[k], w16, x);
-        stmatrix4(tile.step(row, lane, k), x);
+        stmatrix4(tile.step(row, k), x);
       }
     }
     if constexpr (BLK == kBlkCb2s) {   // the static channels' fp16 values
@@ -722,9 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   } else if (warp >= 4 && warp < 4 + kDequantWarps) {
     // ------------------------------------------------------------------ dequantization
     // a warp takes one page's K or V; with 4 pages a tile (INT4) of every other tile
-    constexpr int kTasks = 2 * PAGES, kTurns = kDequantWarps / kTasks;
+    constexpr int kTurns = kDequantWarps / (2 * PAGES);
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
-    const int wi = warp - 4, j = wi % PAGES, role = wi / PAGES % 2, i0 = wi / kTasks;
+    const int wi = warp - 4, j = wi % PAGES, role = wi / PAGES % 2, i0 = wi / (2 * PAGES);
     const int n_mine = i0 < n_tiles ? (n_tiles - i0 + kTurns - 1) / kTurns : 0;   // this warp's tiles i0, i0 + kTurns, ...
     uint64_t* full = raw_full + wi * DEPTH;
     uint8_t* ring = slots + wi * DEPTH * SLOT;
@@ -832,38 +856,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 4 + kDequantWarps && lane == 0) {
-    // ------------------------------------------------------------------ MMA
-    constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);
-    const uint32_t base = smem_u32(smem);
-    auto scores = [&](int i) {
-      if (!wait_bar(&k_full[i & 1], (i >> 1) & 1)) return false;
-      tc::fence_after();
-      const uint32_t kt = base + (i & 1) * P::kBuf;
+      // ---------------------------------------------------------------- MMA
+      constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);
+      const uint64_t buf_desc = tc::desc_sw128(smem_u32(smem));
+      auto scores = [&](int i) {
+        if (!wait_bar(&k_full[i & 1], (i >> 1) & 1)) return false;
+        tc::fence_after();
+        const uint64_t kt = buf_desc + (i & 1) * (P::kBuf >> 4);
 #pragma unroll
-      for (int half = 0; half < (P::kPair ? 2 : 1); ++half)
+        for (int half = 0; half < (P::kPair ? 2 : 1); ++half)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_ta(tmem + (i & 1) * 128, t_q + 8 * k,
-                     tc::desc_sw128(kt + half * 2 * P::kTile + (k >> 2) * (TOK * 128) + (k & 3) * 32), id_s, (half | k) != 0);
-      tc::commit(&s_full[i & 1]);
-      tc::commit(&k_empty[i & 1]);
-      return true;
-    };
-    ok = scores(0);
-    for (int i = 0; i < n_tiles && ok; ++i) {
-      if (i + 1 < n_tiles) ok = scores(i + 1);
-      ok = ok && wait_bar(&p_full[i & 1], (i >> 1) & 1) &&
-           wait_bar(&v_full[i & 1], (i >> 1) & 1);
-      if (!ok) break;
-      tc::fence_after();
-      const uint32_t vt = base + (i & 1) * P::kBuf + P::kTile;
+          for (int k = 0; k < D / 16; ++k)
+            tc::mma_ta(tmem + (i & 1) * 128, t_q + 8 * k,
+                       kt + ((half * 2 * P::kTile + (k >> 2) * (TOK * 128) + (k & 3) * 32) >> 4), id_s, (half | k) != 0);
+        tc::commit(&s_full[i & 1]);
+        tc::commit(&k_empty[i & 1]);
+        return true;
+      };
+      ok = scores(0);
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        if (i + 1 < n_tiles) ok = scores(i + 1);
+        ok = ok && wait_bar(&v_full[i & 1], (i >> 1) & 1) && wait_bar(&p_full[i & 1], (i >> 1) & 1);
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t vt = buf_desc + (((i & 1) * P::kBuf + P::kTile) >> 4);
 #pragma unroll
-      for (int k = 0; k < TOK / 16; ++k)
-        tc::mma_ta(t_o, tmem + (i & 1) * 128 + 8 * k, tc::desc_sw128(vt + (k >> 2) * (D * 128) + (k & 3) * 32), id_o, (i | k) != 0);
-      tc::commit(&v_empty[i & 1]);
-    }
-    tc::commit(done);
-    if (!ok) wait_bar(done, 0);   // tensor memory may be freed once what was issued is done
+        for (int k = 0; k < TOK / 16; ++k)
+          tc::mma_ta(t_o, tmem + (i & 1) * 128 + 8 * k, vt + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), id_o, (i | k) != 0);
+        tc::commit(&v_empty[i & 1]);
+      }
+      tc::commit(done);
+      if (!ok) wait_bar(done, 0);   // tensor memory may be freed once what was issued is done
     }
   }
   if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
