@@ -414,10 +414,12 @@ struct SoftmaxRow {
   float* lse_row;
   bool vec;   // lse_row may be written two pages at a time
 
-  // Columns [c_lo, c_hi) of S at ts, W (32 or 64) at a time, in one pass: the
-  // chunk's maximum, p, P over S's columns.  A chunk that raises m by more than
-  // kRescaleTh (rare after the first) scales what is there: O (once o_free says
-  // that the MMAs are done with it) and the tile's earlier P.
+  // Columns [c_lo, c_hi) of S at ts, W (32 or 64) at a time, in one pass: p, the
+  // pages' sums, P over S's columns.  No maximum is taken: a chunk whose sum
+  // passes 2^15 (rare after the first; a p that fp16 could not hold is among
+  // them) raises m to the row's maximum, scales what is there -- O (once o_free
+  // says that the MMAs are done with it) and the tile's earlier P -- and is
+  // computed again.
   template <int W, class OFree>
   __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c_lo, int c_hi, const int32_t* ntok, const float* ks, int pt,
                                        int p1, bool has_o, OFree&& o_free) {
@@ -433,7 +435,7 @@ struct SoftmaxRow {
     for (int c = c_lo; c < c_hi; c += W) {
       const int pg = c / kPage;
       int n[NP], total = 0;
-      float fk[NP], pm[NP];
+      float fk[NP];
 #pragma unroll
       for (int j = 0; j < NP; j += 2) {
         const int2 n2 = *reinterpret_cast<const int2*>(ntok + pg + j);
@@ -455,24 +457,38 @@ struct SoftmaxRow {
 #pragma unroll
           for (int k = 0; k < kPage; ++k) x[kPage * j + k] = k < n[j] ? x[kPage * j + k] : 0xFF800000u;
       }
-      float mx = -INFINITY;
+      uint32_t u[W / 2];
+      float ps[NP], sum, mb;
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        mb = (m == -INFINITY ? 0.f : m) - kPBias;
+        const uint64_t nb = pack2(-mb, -mb);
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const uint32_t* y = x + kPage * j;
-        float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
+        for (int j = 0; j < NP; ++j) {
+          const uint64_t f2 = pack2(fk[j], fk[j]);
+          uint64_t acc = 0;   // {0.f, 0.f}
 #pragma unroll
-        for (int k = 2; k < kPage - 2; k += 4) {
-          m0 = fmaxf(fmaxf(m0, __uint_as_float(y[k])), __uint_as_float(y[k + 2]));
-          m1 = fmaxf(fmaxf(m1, __uint_as_float(y[k + 1])), __uint_as_float(y[k + 3]));
+          for (int k = 0; k < kPage; k += 2) {
+            const float2 y = unpack2(fma2(pack2u(x[kPage * j + k], x[kPage * j + k + 1]), f2, nb));
+            const float e0 = ex2(y.x), e1 = ex2(y.y);
+            u[(kPage * j + k) / 2] = h2_as_u32(__floats2half2_rn(e0, e1));
+            acc = add2(acc, pack2(e0, e1));
+          }
+          const float2 y = unpack2(acc);
+          ps[j] = y.x + y.y;
         }
-        pm[j] = fmaxf(fmaxf(m0, __uint_as_float(y[kPage - 2])), fmaxf(m1, __uint_as_float(y[kPage - 1]))) * fk[j];
-        mx = fmaxf(mx, pm[j]);
-      }
-      const bool need = mx > m + kRescaleTh;
-      if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
-        const float alpha = need ? ex2(m - mx) : 1.f;
+        sum = ps[0] + ps[1];
+#pragma unroll
+        for (int j = 2; j < NP; j += 2) sum += ps[j] + ps[j + 1];
+        const bool need = !(sum <= 32768.f) || m == -INFINITY;
+        if (__builtin_expect(again || !__any_sync(0xffffffffu, need), 1)) break;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) mx = fmaxf(mx, page_max(x + kPage * j) * fk[j]);
+        const bool up = need && mx > m;
+        const float alpha = up ? ex2(m - mx) : 1.f;
         l *= alpha;
-        m = need ? mx : m;
+        m = up ? mx : m;
         if (has_o && !o_ready) {
           if (!o_free()) return false;
           tc::fence_after();
@@ -485,35 +501,12 @@ struct SoftmaxRow {
         for (int k = c_lo / 32; k < c / 32; ++k) scale_p(ts + 16 * k, alpha);
         tc::wait_st();
       }
-      const float mb = (m == -INFINITY ? 0.f : m) - kPBias;
-      const uint64_t nb = pack2(-mb, -mb);
-      uint32_t u[W / 2];
-      uint64_t sum[NP];
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const uint64_t f2 = pack2(fk[j], fk[j]);
-        sum[j] = 0;   // {0.f, 0.f}
-#pragma unroll
-        for (int k = 0; k < kPage; k += 2) {
-          const float2 y = unpack2(fma2(pack2u(x[kPage * j + k], x[kPage * j + k + 1]), f2, nb));
-          const float e0 = ex2(y.x), e1 = ex2(y.y);
-          u[(kPage * j + k) / 2] = h2_as_u32(__floats2half2_rn(e0, e1));
-          sum[j] = add2(sum[j], pack2(e0, e1));
-        }
-      }
-      float ps[NP];
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const float2 y = unpack2(sum[j]);
-        ps[j] = y.x + y.y;
-      }
-#pragma unroll
-      for (int j = 0; j < NP; j += 2) l += ps[j] + ps[j + 1];
+      l += sum;
       if (lse_row) {
 #pragma unroll
         for (int j = 0; j < NP; j += 2) {
-          const float y0 = page_sum(x + kPage * j, n[j], fk[j], pm[j], mb, ps[j]);
-          const float y1 = page_sum(x + kPage * (j + 1), n[j + 1], fk[j + 1], pm[j + 1], mb, ps[j + 1]);
+          const float y0 = page_sum(x + kPage * j, n[j], fk[j], mb, ps[j]);
+          const float y1 = page_sum(x + kPage * (j + 1), n[j + 1], fk[j + 1], mb, ps[j + 1]);
           const int p = pt + pg + j;
           if (vec && p + 1 < p1) {
             *reinterpret_cast<float2*>(lse_row + p) = make_float2(y0, y1);
@@ -529,18 +522,27 @@ struct SoftmaxRow {
     }
     return true;
   }
+  static __device__ __forceinline__ float page_max(const uint32_t* y) {
+    float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
+#pragma unroll
+    for (int k = 2; k < kPage; k += 2) {
+      m0 = fmaxf(m0, __uint_as_float(y[k]));
+      m1 = fmaxf(m1, __uint_as_float(y[k + 1]));
+    }
+    return fmaxf(m0, m1);
+  }
 
   // ln of a page's sum, given sum = sum 2^(s f - mb); where the page lies so far
   // below the row's maximum that its terms vanish, the sum relative to its own.
-  __device__ __forceinline__ float page_sum(const uint32_t* x, int n, float fk, float pm, float mb, float sum) const {
-    float shift = mb;
-    if (__builtin_expect(pm - mb < -100.f && n > 0, 0)) {
+  __device__ __forceinline__ float page_sum(const uint32_t* x, int n, float fk, float mb, float sum) const {
+    if (__builtin_expect(sum < 0x1p-80f && n > 0, 0)) {
+      mb = page_max(x) * fk;
+      if (mb == -INFINITY) return mb;
       sum = 0.f;
-      shift = pm;
 #pragma unroll
-      for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(__uint_as_float(x[k]), fk, -pm));
+      for (int k = 0; k < kPage; ++k) sum += ex2(fmaf(__uint_as_float(x[k]), fk, -mb));
     }
-    return n > 0 ? (__log2f(sum) + shift) * kLn2 : -INFINITY;
+    return n > 0 ? (__log2f(sum) + mb) * kLn2 : -INFINITY;
   }
   static __device__ __forceinline__ void scale_columns(uint32_t t, float alpha) {
     uint32_t o[16];
