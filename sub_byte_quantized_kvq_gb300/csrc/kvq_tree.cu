@@ -330,9 +330,10 @@ static cudaError_t tree_launch_d(const TreeArgs& a, cudaStream_t st) {
   void* args[] = {const_cast<TreeArgs*>(&a)};
   e = cudaLaunchKernel(k.fn, dim3(a.S, a.Hkv * ((a.R + kTreeRows - 1) / kTreeRows), a.B), dim3(k.threads), args, k.smem, st);
   if (e != cudaSuccess) return e;
-  // The merge is launched while the last split CTAs run (programmatic dependent launch).  Where there are few
-  // rows a warp takes one, else four, which share the loads of the tail's and the nodes' K and V.
-  const bool few = (long long)a.B * a.Hkv * a.R <= 152 * 8 * 8;
+  // The merge is launched while the last split CTAs run (programmatic dependent launch).  A warp takes four rows,
+  // which share the loads of the tail's and the nodes' K and V, or one where that would leave most SMs idle (up to
+  // two CTAs of 8 one-row warps on each of 152; measured with 8 of them: 4096 rows 46 us a call instead of 42).
+  const bool few = (long long)a.B * a.Hkv * a.R <= 152 * 8 * 2;
   const int rows = kMergeWarps * (few ? 1 : 4);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -5,9 +5,9 @@
 // O += P V, and each page's codes are expanded once for all of the rows:
 //
 //   16 dequant warps  each takes one page's K or V of every tile: its own ring of
-//                   bulk asynchronous copies (a single warp issues one copy
-//                   every 90 ns whatever its size, measured, so one producer
-//                   for all would cap the SM at 10-20 bytes a cycle), then
+//                   asynchronous copies (16 bytes a lane; bulk copies are issued
+//                   at one per 33 ns and SM, 90 ns and warp, whatever their size,
+//                   and held the warp up for as long), then
 //                   codes -> fp16 tiles in shared memory, K as [token][channel],
 //                   V transposed as [channel][token], both K-major with 128-byte
 //                   swizzle; the block layout holds mma fragments, which
@@ -58,7 +58,7 @@ struct Plan {
   static constexpr int kBuf = (kPair ? 3 : 2) * kTile;       // one buffer: K [, K low], V
   // a page's slot: its (virtual) block from offset 0 (the group format copies the group's codebook into each)
   static constexpr int kSlot = F::kGroup ? 12 * D + kOutPrefetch : half_slot_bytes<FMT, D>();
-  static constexpr int misc(int depth) { return 8 * (kDequantWarps * depth + 13) + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8; }
+  static constexpr int misc(int depth) { return 8 * 13 + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8; }
   static constexpr int smem(int depth) {   // 1024: alignment slack
     return 1024 + 2 * kBuf + kDequantWarps * depth * kSlot + misc(depth);
   }
@@ -591,8 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
 
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
   uint8_t* slots = smem + 2 * P::kBuf;                                    // [kDequantWarps][DEPTH]
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(slots + kDequantWarps * DEPTH * SLOT);   // [kDequantWarps][DEPTH]
-  uint64_t *k_full = raw_full + kDequantWarps * DEPTH, *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2,
+  uint64_t *k_full = reinterpret_cast<uint64_t*>(slots + kDequantWarps * DEPTH * SLOT), *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2,
            *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
   int32_t* ntok = reinterpret_cast<int32_t*>(done + 1);                   // [kMeta][PAGES] tokens of a tile's pages
   float* kscale = reinterpret_cast<float*>(ntok + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
@@ -603,7 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   const int rep = rows <= 32 && TOK == 128 ? 4 : rows <= 64 ? 2 : 1, row = tid % (kM / rep);
   const int n_sm = rep > 1 ? 4 : (rows + 31) / 32;   // softmax warps with rows
   if (tid == 0) {
-    for (int i = 0; i < kDequantWarps * DEPTH; ++i) mbar_init(&raw_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], PAGES);
       mbar_init(&k_empty[i], 1);
@@ -752,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDequant));
     const int wi = warp - 4, j = wi % PAGES, role = wi / PAGES % 2, i0 = wi / (2 * PAGES);
     const int n_mine = i0 < n_tiles ? (n_tiles - i0 + kTurns - 1) / kTurns : 0;   // this warp's tiles i0, i0 + kTurns, ...
-    uint64_t* full = raw_full + wi * DEPTH;
     uint8_t* ring = slots + wi * DEPTH * SLOT;
     const int32_t* pt = a.page_table + (size_t)b * a.ppsm;
     // The page's entry in this warp's k-th tile: a window of 32 in the lanes.  kNoPage: absent, or bad.
@@ -783,42 +780,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     auto block_at = [&](int32_t e) {
       return FMT == KVQ_FMT_TIERED && e < 0 ? tier_src + ((uint32_t)e & 0x7FFFFFFFu) * tier_page : main_src + (uint32_t)e * main_page;
     };
-    auto issue = [&](int k, int slot) {   // the copy of the warp's k-th block
-      if (k - win_base >= 32) load_window(k);
-      const int32_t e = __shfl_sync(0xffffffffu, win, k - win_base);
-      if (lane == 0) {
-        ent[slot] = e;
-        uint64_t* bar = full + slot;
-        uint8_t* dst = ring + slot * SLOT;
-        if (e == kNoPage) {
-          mbar_arrive(bar);
-        } else if constexpr (F::kGroup) {
-          const int page = p0 + (i0 + k * kTurns) * PAGES + j, first = page / kGroupPages * kGroupPages;
-          mbar_arrive_expect_tx(bar, 12 * D + kOutPrefetch);
-          bulk_g2s(dst, block_at(pt[first]), 8 * D, bar);
-          bulk_g2s(dst + 8 * D, block_at(e) + 8 * D, 4 * D + kOutPrefetch, bar);
-        } else {
-          const uint32_t bytes = FMT == KVQ_FMT_TIERED && e < 0 ? fetch_bytes<D>(kBlkFp8)
-                                 : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
-                                                               : fetch_bytes<D>(F::kMain);
-          mbar_arrive_expect_tx(bar, bytes);
-          bulk_g2s(dst, block_at(e), bytes, bar);
+    auto copy = [&](uint32_t dst, const uint8_t* src, int bytes) {   // 16 bytes a lane at a time
+#pragma unroll 1
+      for (int o = 16 * lane; o < bytes; o += 512)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + o), "l"(src + o) : "memory");
+    };
+    auto issue = [&](int k, int slot) {   // the copy of the warp's k-th block (past the last: an empty group)
+      if (k < n_mine) {
+        if (k - win_base >= 32) load_window(k);
+        const int32_t e = __shfl_sync(0xffffffffu, win, k - win_base);
+        if (lane == 0) ent[slot] = e;
+        if (e != kNoPage) {
+          const uint32_t dst = smem_u32(ring + slot * SLOT);
+          if constexpr (F::kGroup) {
+            const int page = p0 + (i0 + k * kTurns) * PAGES + j, first = page / kGroupPages * kGroupPages;
+            copy(dst, block_at(pt[first]), 8 * D);
+            copy(dst + 8 * D, block_at(e) + 8 * D, 4 * D + kOutPrefetch);
+          } else {
+            copy(dst, block_at(e),
+                 FMT == KVQ_FMT_TIERED && e < 0 ? fetch_bytes<D>(kBlkFp8)
+                 : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
+                                               : fetch_bytes<D>(F::kMain));
+          }
         }
       }
-      __syncwarp();
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     load_window(0);
-    int issued = min(DEPTH, n_mine), waited = 0;
-    for (int k = 0; k < issued; ++k) issue(k, k);
+    for (int k = 0; k < DEPTH; ++k) issue(k, k);
     int slot = 0;
-    uint32_t phase = 0;
     for (int k = 0; k < n_mine; ++k) {
       const int i = i0 + k * kTurns;
-      ok = wait_bar(full + slot, phase);
-      waited += ok;
+      asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
       uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
-      if (ok && i >= 2) ok = wait_bar(empty, ((i >> 1) - 1) & 1);
+      if (i >= 2) ok = wait_bar(empty, ((i >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
+      __syncwarp();   // every lane's part of the copy
       if (!ok) break;
       const int32_t e = ent[slot];
       const int n = e == kNoPage ? 0 : min(kPage, v.len - kPage * (p0 + i * PAGES + j));
@@ -841,20 +838,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           zero_tokens<D>(vt, n, lane);
         }
       }
-      fence_proxy_async();   // the tile for the MMAs, and the slot's reads before its next copy
+      fence_proxy_async();   // the tile for the MMAs
       __syncwarp();
       if (lane == 0) mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
-      if (k + DEPTH < n_mine) {
-        issue(k + DEPTH, slot);
-        ++issued;
-      }
-      if (++slot == DEPTH) {
-        slot = 0;
-        phase ^= 1u;
-      }
+      issue(k + DEPTH, slot);
+      if (++slot == DEPTH) slot = 0;
     }
-    if (!ok)   // let copies in flight land before the CTA can exit
-      for (int k = waited; k < issued; ++k) wait_bar(full + k % DEPTH, (k / DEPTH) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 4 + kDequantWarps && lane == 0) {
