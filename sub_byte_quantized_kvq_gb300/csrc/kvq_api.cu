@@ -443,6 +443,8 @@ static kvq_status tree_shape_ok(const kvq_config* cfg, int32_t num_q_heads, int3
     return KVQ_ERR_INVALID_ARG;
   if (!dim_supported(cfg) || num_q_heads / cfg->num_kv_heads > 16 || num_nodes > KVQ_TREE_MAX_NODES)
     return KVQ_ERR_UNSUPPORTED;
+  const long long tiles = (num_q_heads / cfg->num_kv_heads * num_nodes + kTreeRows - 1) / kTreeRows;
+  if (tiles * cfg->num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;   // the grid's y dimension
   if (num_splits > kMaxSplits) return KVQ_ERR_CAPACITY;
   return KVQ_OK;
 }

@@ -72,14 +72,12 @@ struct Plan {
   static_assert(kDepth >= 2 && kSlot % 16 == 0 && kTile % 1024 == 0, "tree attention plan");
 };
 
-// A bounded mbarrier wait on the SM's own clock (reading the global timer costs
-// a waiting warp about a microsecond): gives up after 2^28 cycles, 130 ms at
-// the highest clock.
+// A bounded mbarrier wait on the SM's own clock: gives up after 2e8 cycles, 100 ms.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait_sleep(bar, parity, 20000u))
-    if (clock64() - t0 > (1ll << 28)) return false;
+    if (clock64() - t0 > 200000000ll) return false;
   return true;
 }
 
@@ -613,59 +611,60 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     mbar_init(done, 1);
     fence_mbar_init();
   }
-  if (warp == 4) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
+  // Each role starts its first global loads before the barrier that publishes the mbarriers and the tensor memory.
   // tensor memory: S tiles (P over them) at columns 0 and 128, O at 256, Q at 384
-  const uint32_t tmem = *tslot, t_o = tmem + 256, t_q = tmem + 384;
-  bool ok = true;
-
-  // ---- each softmax thread's query row into tensor memory
-  float f = 0.f;
-  if (warp < n_sm) {
-    const int r = r0 + row;
-    const bool on = row < rows;
-    const __nv_bfloat16* qr = a.q + (((size_t)b * a.T + (on ? r / a.G : 0)) * a.Hq + (size_t)h * a.G + (on ? r % a.G : 0)) * D;
-    float mx = 0.f;
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 x = reinterpret_cast<const uint4*>(qr)[i];
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
-    }
-    int e = 0;
-    frexpf(mx, &e);
-    const int k = mx > 0.f && mx < INFINITY ? min(max(e - 15, -100), 100) : 0;
-    // the scale's sign goes with the query, so that the score factor f is positive
-    const float qs = on ? copysignf(ldexpf(1.f, -k), a.scale_log2) : 0.f;
-    f = fmaxf(ldexpf(fabsf(a.scale_log2), k), 1e-36f);
-    for (int c = 0; c < D / 64; ++c) {
-      uint32_t w[32];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 x = reinterpret_cast<const uint4*>(qr)[8 * c + i];
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[4 * i + j] = on ? h2_as_u32(__floats2half2_rn(__uint_as_float(u[j] << 16) * qs,
-                                                          __uint_as_float(u[j] & 0xFFFF0000u) * qs))
-                            : 0u;
-      }
-      tc::st32(t_q + ((uint32_t)(32 * warp) << 16) + 32 * c, w);
-    }
-    tc::wait_st();
+  uint32_t tmem = 0, t_o = 0, t_q = 0;
+  auto join = [&]() {
     tc::fence_before();
-  }
-  __syncthreads();
-  tc::fence_after();
+    asm volatile("bar.sync 0;" ::: "memory");
+    tc::fence_after();
+    tmem = *tslot;
+    t_o = tmem + 256;
+    t_q = tmem + 384;
+  };
+  bool ok = true;
 
   if (warp < 4) {
     // ------------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ---- each thread's query row into tensor memory, scaled by a power of two into fp16 range
+    float f = 0.f, qs = 0.f;
+    uint32_t q[D / 2] = {};   // bf16 pairs
+    if (warp < n_sm) {
+      const int r = r0 + row;
+      if (row < rows) {
+        const uint4* qr = reinterpret_cast<const uint4*>(a.q + (((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * D);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = qr[i];
+          q[4 * i] = x.x;
+          q[4 * i + 1] = x.y;
+          q[4 * i + 2] = x.z;
+          q[4 * i + 3] = x.w;
+        }
+      }
+      float mx = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i)
+        mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(q[i] << 16)), fabsf(__uint_as_float(q[i] & 0xFFFF0000u))));
+      int e = 0;
+      frexpf(mx, &e);
+      const int k = mx > 0.f && mx < INFINITY ? max(e - 15, -100) : 0;
+      // the scale's sign goes with the query, so that the score factor f is positive
+      qs = copysignf(ldexpf(1.f, -k), a.scale_log2);
+      f = fmaxf(ldexpf(fabsf(a.scale_log2), k), 1e-36f);
+    }
+    join();
+    if (warp < n_sm) {
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i)
+        q[i] = h2_as_u32(__floats2half2_rn(__uint_as_float(q[i] << 16) * qs, __uint_as_float(q[i] & 0xFFFF0000u) * qs));
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) tc::st32(t_q + ((uint32_t)(32 * warp) << 16) + 32 * c, q + 32 * c);
+      tc::wait_st();
+      tc::fence_before();
+      asm volatile("bar.arrive 3, %0;" ::"r"(32 * n_sm + 32) : "memory");   // (the MMA warp waits)
+    }
     if (warp < n_sm) {
       const uint32_t lanes = (uint32_t)(32 * warp) << 16;
       SoftmaxRow<FMT, D> sr;
@@ -808,6 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     };
     load_window(0);
     for (int k = 0; k < DEPTH; ++k) issue(k, k);
+    if (warp == 4) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    join();
     int slot = 0;
     for (int k = 0; k < n_mine; ++k) {
       const int i = i0 + k * kTurns;
@@ -847,6 +851,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    join();
+    if (warp == 4 + kDequantWarps) {
+      asm volatile("bar.sync 3, %0;" ::"r"(32 * n_sm + 32) : "memory");   // the query rows
+      tc::fence_after();
+    }
     if (warp == 4 + kDequantWarps && lane == 0) {
       // ---------------------------------------------------------------- MMA
       constexpr uint32_t id_s = tc::idesc_f16(kM, TOK), id_o = tc::idesc_f16(kM, D);

@@ -177,6 +177,27 @@ def test_loud_and_quiet_queries():
         assert np.isfinite(got[2][0]).all()
 
 
+@pytest.mark.parametrize("G,T", [(4, 2), (8, 8), (8, 16)])
+def test_running_maximum_rises_all_along(G, T):
+    """Scores that climb by about 40 (natural units) over the context in uneven steps, some rows down instead:
+    the state is rescaled many times, early pages end up far below the maximum, late ones in the other rows."""
+    L, Hkv, D = 900, 2, 128
+    pair = Pair(E2M1, 1, Hkv, D, 64, seed=2)
+    g = torch.Generator().manual_seed(5)
+    u = torch.randn((Hkv, D), generator=g)
+    u = u / u.norm(dim=-1, keepdim=True)
+    height = 40.0 * torch.cumsum(torch.rand(L, generator=g) ** 6, 0) / torch.cumsum(torch.rand(L, generator=g) ** 6, 0)[-1]
+    k = (height[:, None, None] * u)[None] + 0.05 * torch.randn((1, L, Hkv, D), generator=g)
+    v = torch.randn((1, L, Hkv, D), generator=g)
+    pair.append(k, v)
+    q = (D ** 0.5 * u.repeat_interleave(G, 0))[None, None].repeat(1, T, 1, 1)
+    q[:, ::2] *= -1.0
+    q = (q + 0.1 * torch.randn(q.shape, generator=g)).to(torch.bfloat16)
+    for splits in (1, 0, 3):
+        got = run(pair, q, splits=splits)
+        check(got, pair, q)
+
+
 def test_more_queries_than_a_tile_and_many_splits():
     pair = build(E2M1, 128, [700, 333], Hkv=1, P=48)
     q, k, v, parents = draft(21, 2, 64, 1, 16, 128)

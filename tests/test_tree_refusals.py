@@ -57,6 +57,7 @@ def test_tree_attention_refusals(kvq):
     assert tree(kvq, c, k, T=65) == UNSUPPORTED
     assert tree(kvq, c, k, Hq=8 * 17) == UNSUPPORTED
     assert tree(kvq, cfg_of(kvq, D=96), k) == UNSUPPORTED
+    assert tree(kvq, cfg_of(kvq, num_kv_heads=10000), k, Hq=160000, T=64) == UNSUPPORTED   # 80,000 row tiles in the grid
     assert tree(kvq, c, k, splits=257) == CAPACITY
     assert tree(kvq, cfg_of(kvq, 2), k) == INVALID      # a page format without staging
     assert tree(kvq, c, cache_of(kvq, page_table=None)) == INVALID
