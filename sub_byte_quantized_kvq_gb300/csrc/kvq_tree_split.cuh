@@ -30,6 +30,8 @@
 // of the measured HBM rate, next to 64 KB of shared-memory tile writes and
 // reads; fewer rows leave the exponentials out, not the rest.
 #pragma once
+#include <type_traits>
+
 #include "kvq_decode.cuh"
 #include "kvq_tc.cuh"
 #include "kvq_tree.cuh"
@@ -779,10 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     auto block_at = [&](int32_t e) {
       return FMT == KVQ_FMT_TIERED && e < 0 ? tier_src + ((uint32_t)e & 0x7FFFFFFFu) * tier_page : main_src + (uint32_t)e * main_page;
     };
-    auto copy = [&](uint32_t dst, const uint8_t* src, int bytes) {   // 16 bytes a lane at a time
-#pragma unroll 1
-      for (int o = 16 * lane; o < bytes; o += 512)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + o), "l"(src + o) : "memory");
+    auto copy = [&](uint32_t dst, const uint8_t* src, int bytes, auto most) {   // 16 bytes a lane at a time; at most `most`
+      const uint32_t d = dst + 16 * lane;
+      const uint8_t* p = src + 16 * lane;
+#pragma unroll
+      for (int o = 0; o < most.value; o += 512)
+        if (16 * lane + o < bytes) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + o), "l"(p + o) : "memory");
     };
     auto issue = [&](int k, int slot) {   // the copy of the warp's k-th block (past the last: an empty group)
       if (k < n_mine) {
@@ -793,13 +797,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           const uint32_t dst = smem_u32(ring + slot * SLOT);
           if constexpr (F::kGroup) {
             const int page = p0 + (i0 + k * kTurns) * PAGES + j, first = page / kGroupPages * kGroupPages;
-            copy(dst, block_at(pt[first]), 8 * D);
-            copy(dst + 8 * D, block_at(e) + 8 * D, 4 * D + kOutPrefetch);
+            copy(dst, block_at(pt[first]), 8 * D, std::integral_constant<int, 8 * D>{});
+            copy(dst + 8 * D, block_at(e) + 8 * D, 4 * D + kOutPrefetch, std::integral_constant<int, 4 * D + kOutPrefetch>{});
           } else {
             copy(dst, block_at(e),
                  FMT == KVQ_FMT_TIERED && e < 0 ? fetch_bytes<D>(kBlkFp8)
                  : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
-                                               : fetch_bytes<D>(F::kMain));
+                                               : fetch_bytes<D>(F::kMain),
+                 std::integral_constant<int, SLOT>{});
           }
         }
       }
