@@ -272,15 +272,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
 }
 
 // ----------------------------------------------------------------------------- host side
-static TreeKernel tree_kernel(int fmt, int D) {
+static TreeKernel tree_kernel(int fmt, int D, int R) {
   switch (fmt) {
-    case KVQ_FMT_INT4_G32: return tree_kernel_int4(D);
-    case KVQ_FMT_FP4_E2M1_S16: return tree_kernel_e2m1(D);
-    case KVQ_FMT_CB2_OUTLIER: return tree_kernel_cb2(D);
-    case KVQ_FMT_CB2_STATIC: return tree_kernel_cb2s(D);
-    case KVQ_FMT_ASYM3_OUTLIER: return tree_kernel_a3(D);
-    case KVQ_FMT_CB2_GROUP4: return tree_kernel_cb2g(D);
-    default: return tree_kernel_tiered(D);
+    case KVQ_FMT_INT4_G32: return tree_kernel_int4(D, R);
+    case KVQ_FMT_FP4_E2M1_S16: return tree_kernel_e2m1(D, R);
+    case KVQ_FMT_CB2_OUTLIER: return tree_kernel_cb2(D, R);
+    case KVQ_FMT_CB2_STATIC: return tree_kernel_cb2s(D, R);
+    case KVQ_FMT_ASYM3_OUTLIER: return tree_kernel_a3(D, R);
+    case KVQ_FMT_CB2_GROUP4: return tree_kernel_cb2g(D, R);
+    default: return tree_kernel_tiered(D, R);
   }
 }
 
@@ -324,7 +324,7 @@ static cudaError_t allow_smem(const TreeKernel& k) {
 
 template <int D>
 static cudaError_t tree_launch_d(const TreeArgs& a, cudaStream_t st) {
-  const TreeKernel k = tree_kernel(a.fmt, D);
+  const TreeKernel k = tree_kernel(a.fmt, D, a.R);
   cudaError_t e = allow_smem(k);
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<TreeArgs*>(&a)};

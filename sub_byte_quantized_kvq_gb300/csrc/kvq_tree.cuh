@@ -75,19 +75,19 @@ __device__ __forceinline__ float* page_lse_row(const TreeArgs& a, int b, int h, 
   return a.page_lse + (((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * a.P;
 }
 
-// One translation unit per format instantiates its kernels.
+// One translation unit per format instantiates its kernels; the one for R rows:
 struct TreeKernel {
   void* fn;
   size_t smem;
   int threads;
 };
-TreeKernel tree_kernel_int4(int D);
-TreeKernel tree_kernel_e2m1(int D);
-TreeKernel tree_kernel_cb2(int D);
-TreeKernel tree_kernel_tiered(int D);
-TreeKernel tree_kernel_cb2s(int D);
-TreeKernel tree_kernel_a3(int D);
-TreeKernel tree_kernel_cb2g(int D);
+TreeKernel tree_kernel_int4(int D, int R);
+TreeKernel tree_kernel_e2m1(int D, int R);
+TreeKernel tree_kernel_cb2(int D, int R);
+TreeKernel tree_kernel_tiered(int D, int R);
+TreeKernel tree_kernel_cb2s(int D, int R);
+TreeKernel tree_kernel_a3(int D, int R);
+TreeKernel tree_kernel_cb2g(int D, int R);
 
 cudaError_t tree_launch(const TreeArgs& a, int D, cudaStream_t st);
 // Splits tree_launch's first kernel is given when the caller leaves the choice.

@@ -2,7 +2,7 @@
 #include "kvq_tree_split.cuh"
 
 namespace kvq {
-TreeKernel tree_kernel_int4(int D) {
-  return D == 64 ? tree::tree_kernel_info<KVQ_FMT_INT4_G32, 64>() : tree::tree_kernel_info<KVQ_FMT_INT4_G32, 128>();
+TreeKernel tree_kernel_int4(int D, int R) {
+  return D == 64 ? tree::tree_kernel_info<KVQ_FMT_INT4_G32, 64>(R) : tree::tree_kernel_info<KVQ_FMT_INT4_G32, 128>(R);
 }
 }  // namespace kvq

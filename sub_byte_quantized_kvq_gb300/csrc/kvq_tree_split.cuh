@@ -563,7 +563,17 @@ struct SoftmaxRow {
   }
 };
 
+// Most rows of the FEW variant.
 template <int FMT, int D>
+constexpr int few_rows() { return kM / (Plan<FMT, D>::kTok / 32); }
+
+// Few rows: the 128 tensor-memory lanes hold `rep` copies of them, and each
+// copy's warps take their share of a tile's columns (P = 0 in the others), so
+// that the softmax of a tile takes a rep-th of the time.  FEW: a share of 32
+// columns, for up to few_rows(); else one copy or two, 64 columns a step.  Two
+// kernels, because the code that one of them does not run still costs it
+// instruction fetches (4% on 8 rows of the tiered format).
+template <int FMT, int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs a) {
   using F = Fmt<FMT>;
   using P = Plan<FMT, D>;
@@ -597,9 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   float* kscale = reinterpret_cast<float*>(ntok + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
   int32_t* entries = reinterpret_cast<int32_t*>(kscale + kMeta * PAGES);  // [kDequantWarps][DEPTH] page-table entries of the slots
   uint32_t* tslot = reinterpret_cast<uint32_t*>(entries + kDequantWarps * DEPTH);
-  // Few rows: the 128 tensor-memory lanes hold `rep` copies of them, and each copy's warps take their share of a
-  // tile's columns (P = 0 in the others), so that the softmax of a tile takes a rep-th of the time.
-  const int rep = rows <= 32 && TOK == 128 ? 4 : rows <= 64 ? 2 : 1, row = tid % (kM / rep);
+  const int rep = FEW ? TOK / 32 : TOK == 128 && rows <= 64 ? 2 : 1, row = tid % (kM / rep);
   const int n_sm = rep > 1 ? 4 : (rows + 31) / 32;   // softmax warps with rows
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -685,8 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           return __all_sync(0xffffffffu, wait_bar(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
         };
         const int lo = 32 * c0, hi = 32 * (c0 + chunks);
-        ok = chunks > 1 ? sr.template tile<64>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, pt, p1, i > 0, o_free)
-                        : sr.template tile<32>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        ok = sr.template tile<FEW ? 32 : 64>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
         if (!ok) break;
         if (rep > 1) {   // the columns of the row's other copies: P = 0
           const uint32_t z[16] = {};
@@ -904,8 +911,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
 }
 
 template <int FMT, int D>
-static TreeKernel tree_kernel_info() {
-  return {reinterpret_cast<void*>(tree_cache_kernel<FMT, D>), (size_t)Plan<FMT, D>::kSmem, kThreads};
+static TreeKernel tree_kernel_info(int R) {
+  return {R <= few_rows<FMT, D>() ? reinterpret_cast<void*>(tree_cache_kernel<FMT, D, true>)
+                                  : reinterpret_cast<void*>(tree_cache_kernel<FMT, D, false>),
+          (size_t)Plan<FMT, D>::kSmem, kThreads};
 }
 
 }  // namespace tree

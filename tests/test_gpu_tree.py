@@ -347,3 +347,14 @@ def test_no_wait_gives_up_over_many_tiles(fmt):
             if splits == 1:
                 assert torch.equal(out, first)
     assert cache.status_word() == 0
+
+
+@pytest.mark.parametrize("fmt", [INT4, CB2, E2M1], ids=["int4", "cb2", "e2m1"])
+@pytest.mark.parametrize("G,T", [(4, 8), (4, 9), (8, 8), (8, 9), (8, 16), (8, 17)])
+def test_row_counts_at_the_kernels_borders(fmt, G, T):
+    """32, 36, 64, 72, 128 and 136 rows, and fewer live ones in some sequences."""
+    pair = build(fmt, 128, [180, 209, 77, 50])
+    q, k, v, parents = draft(G + T, 4, T, 2, 2 * G, 128)
+    sees = sees_from_parents(parents)
+    for nodes in (None, [T, T // 2, 1, T - 1]):
+        check(run(pair, q, k, v, words(sees), nodes, splits=1), pair, q, k, v, sees, nodes)
