@@ -27,20 +27,30 @@ __global__ void __launch_bounds__(32 * kMassWarps) page_mass_kernel(const float*
   const uint64_t on = (nodes ? nodes[b] : ~0ull) & (T == 64 ? ~0ull : (1ull << T) - 1ull);
   if (threadIdx.x < T && ((on >> threadIdx.x) & 1ull)) marked[__popcll(on & ((1ull << threadIdx.x) - 1ull))] = threadIdx.x;
   __syncthreads();
-  const int n = blockIdx.x * kMassPages < P ? __popcll(on) * Hq : 0;
+  const int n = blockIdx.x * kMassPages < P ? __popcll(on) : 0;   // marked nodes
+  const bool whole = (blockIdx.x + 1) * kMassPages <= P;
   float w[kMassPer] = {};
   constexpr int U = 4;
-  for (int i = warp; i < n; i += U * kMassWarps) {
+  int i = 0, h = warp;   // this warp's next row: head h of the i-th marked node (h may pass Hq: the node's successors)
+  auto settle = [&]() {
+    while (h >= Hq && i < n) {
+      h -= Hq;
+      ++i;
+    }
+  };
+  for (settle(); i < n;) {
     float z[U], x[U][kMassPer];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int j = i + k * kMassWarps;
       z[k] = -INFINITY;
-      if (j < n) {
-        const size_t r = ((size_t)b * T + marked[j / Hq]) * Hq + j % Hq;
+      if (i < n) {
+        const size_t r = ((size_t)b * T + marked[i]) * Hq + h;
+        const float* row = page_lse + r * P + p0;
         z[k] = lse[r];
 #pragma unroll
-        for (int c = 0; c < kMassPer; ++c) x[k][c] = p0 + 32 * c < P ? page_lse[r * P + p0 + 32 * c] : -INFINITY;
+        for (int c = 0; c < kMassPer; ++c) x[k][c] = whole || p0 + 32 * c < P ? row[32 * c] : -INFINITY;
+        h += kMassWarps;
+        settle();
       }
     }
 #pragma unroll
