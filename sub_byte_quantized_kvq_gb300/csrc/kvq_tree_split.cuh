@@ -15,20 +15,22 @@
 //   MMA warp        tcgen05.mma with Q and P from tensor memory, the tiles from
 //                   shared memory; S(i + 1) is issued before PV(i), so the tensor
 //                   cores work while the softmax warps do
-//   4 softmax warps one row a thread (tensor-memory lane): running maximum with
-//                   lazy rescale, p = 2^(s - m), page sums for page_lse; P goes
-//                   over S's own columns
+//   4 softmax warps one row a thread (tensor-memory lane): p = 2^(s - m) with a
+//                   reference m that is raised only when the sums ask for it,
+//                   page sums for page_lse; P goes over S's own columns
 //
 // Precision: Q is scaled by a power of two into fp16 range and exact; K is
 // exact in fp16 (INT4: an fp16 pair, two MMAs); S, m, l and O are fp32.  P is
-// rounded to fp16 (2^-12 relative on average; biased by 2^kPBias so that small
+// rounded to fp16 (at most 2^-11 relative; biased by 2^kPBias so that small
 // p keep their bits), V to fp16 where the format's value has more (INT4, FP8
 // tier): for a bf16 result both are below its own rounding.
 //
-// What bounds it: at 128 rows a tile of 128 tokens takes about 1024 cycles of
-// MMA, 1024 of exponentials (16 a cycle and SM) and 800-1200 of this SM's share
-// of the measured HBM rate, next to 64 KB of shared-memory tile writes and
-// reads; fewer rows leave the exponentials out, not the rest.
+// What bounds it: instruction issue.  A tile of 128 tokens is about 1024 cycles
+// of MMA at 128 rows and 800-1200 of this SM's share of the measured HBM rate,
+// but some 7,000 warp instructions (expansion, exponentials, waits) for four
+// schedulers; measured 16 sequences x 32k tokens: FP4 at 128 rows 392 us (3,300
+// cycles a tile), tiered at 8 rows 315 us.  Addresses that run along with a warp's
+// tiles, instead of computed per tile, gave 1-2% (397 and 321 us before).
 #pragma once
 #include <type_traits>
 
@@ -48,7 +50,7 @@ static_assert(4 * kRegsSoftmax + kDequantWarps * kRegsDequant + 4 * kRegsRest <=
               "setmaxnreg shares exceed what the launch has");
 constexpr int kMeta = 4;                // tiles whose page records are kept: K(i) is written once S(i - 2) is done, whose
                                         // MMAs were issued after the softmax of tile i - 4
-constexpr float kPBias = 6.f;           // p <= 2^(kRescaleTh + kPBias) stays in fp16 range
+constexpr float kPBias = 6.f;           // p = 2^(s f - m + kPBias): small p keep their bits; p <= 2^15 by the check on the sums
 
 template <int FMT, int D>
 struct Plan {
@@ -113,35 +115,33 @@ __device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& x, uint32_t& y) {
       : "r"(w));
 }
 
-// Where a page's values go in a swizzled tile.  A row is 64 fp16 (128 bytes);
-// 16-byte chunk k of row r lies at chunk k ^ (r % 8).
+// Where a page's values go in a swizzled tile, as offsets from its start.  A row
+// is 64 fp16 (128 bytes); 16-byte chunk k of row r lies at chunk k ^ (r % 8).
 template <int D, int TOK>
 struct KTile {   // rows = tokens, D / 64 row groups
   static constexpr int kStep4 = TOK * 128;   // four steps: the next row group
-  uint32_t tile;
   int page;
   __device__ __forceinline__ uint32_t at(int t, int c) const {
     const int row = kPage * page + t;
-    return tile + (c >> 6) * (TOK * 128) + row * 128 + ((((c & 63) >> 3) ^ (row & 7)) << 4) + (c & 7) * 2;
+    return (c >> 6) * (TOK * 128) + row * 128 + (((c >> 3 & 7) ^ (t & 7)) << 4) + (c & 7) * 2;
   }
-  // lane's row address of a group of four steps, and of its step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15;
-  // the swizzled chunk (2 s + half) ^ (row % 8) of a 128-byte row)
+  // lane's row of a group of four steps, and of its step s (matrices: tokens 0-7 / 8-15 x channels 0-7 / 8-15; the
+  // swizzled chunk (2 s + half) ^ (row % 8) of a 128-byte row)
   __device__ __forceinline__ uint32_t lane_row(int lane) const {
-    return tile + (kPage * page + (lane & 15)) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+    return (kPage * page + (lane & 15)) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
   }
   __device__ __forceinline__ uint32_t step(uint32_t row, int s) const { return row ^ (s << 5); }
 };
 template <int D, int TOK>
 struct VTile {   // rows = channels, TOK / 64 row groups
   static constexpr int kStep4 = 4 * 2048;
-  uint32_t tile;
   int page;
   __device__ __forceinline__ uint32_t at(int t, int c) const {
-    return tile + (page >> 2) * (D * 128) + c * 128 + ((((page & 3) * 2 + (t >> 3)) ^ (c & 7)) << 4) + (t & 7) * 2;
+    return (page >> 2) * (D * 128) + c * 128 + ((((page & 3) * 2 + (t >> 3)) ^ (c & 7)) << 4) + (t & 7) * 2;
   }
   // (matrices: channels 0-7 / 8-15 x tokens 0-7 / 8-15)
   __device__ __forceinline__ uint32_t lane_row(int lane) const {
-    return tile + (page >> 2) * (D * 128) + (lane & 15) * 128 + ((((page & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
+    return (page >> 2) * (D * 128) + (lane & 15) * 128 + ((((page & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4);
   }
   __device__ __forceinline__ uint32_t step(uint32_t row, int s) const { return row + s * 2048; }
 };
@@ -164,18 +164,18 @@ struct SidePatch {
     }
   }
   template <class Tile, class Side>
-  __device__ __forceinline__ void store(const Tile& tile, int lane, Side&& side_g) {
+  __device__ __forceinline__ void store(const Tile& tile, uint32_t buf, int lane, Side&& side_g) {
     const int t = lane & 15, half = lane >> 4;
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < kChunk / 2; ++k)
       if (2 * k + half < n && ((head[k] >> (16 + t)) & 1u))
-        sts16(tile.at(t, head[k] & (D - 1)), e4m3x2_to_f16x2(value[k]));
+        sts16(buf + tile.at(t, head[k] & (D - 1)), e4m3x2_to_f16x2(value[k]));
     if (__builtin_expect(n > kChunk, 0)) {
       const uint8_t* side = side_g();
       for (int i = kChunk + half; i < n; i += 2) {
         const uint8_t* rec = side + 4 + 20 * i;
-        if ((*reinterpret_cast<const uint16_t*>(rec + 2) >> t) & 1u) sts16(tile.at(t, rec[0] & (D - 1)), e4m3x2_to_f16x2(rec[4 + t]));
+        if ((*reinterpret_cast<const uint16_t*>(rec + 2) >> t) & 1u) sts16(buf + tile.at(t, rec[0] & (D - 1)), e4m3x2_to_f16x2(rec[4 + t]));
       }
     }
   }
@@ -183,11 +183,11 @@ struct SidePatch {
 
 // Tokens from `ntok` on as zeros in a V tile (their probability is 0, and stale bytes may stand for anything).
 template <int D, class Tile>
-__device__ __forceinline__ void zero_tokens(const Tile& tile, int ntok, int lane) {
+__device__ __forceinline__ void zero_tokens(const Tile& tile, uint32_t buf, int ntok, int lane) {
   for (int c = lane; c < D; c += 32)
 #pragma unroll
     for (int t = 0; t < kPage; ++t)
-      if (t >= ntok) sts16(tile.at(t, c), 0u);
+      if (t >= ntok) sts16(buf + tile.at(t, c), 0u);
 }
 
 // One K block (role 0) or V block (role 1) -> its place in the fp16 tile, four
@@ -197,14 +197,15 @@ __device__ __forceinline__ void zero_tokens(const Tile& tile, int ntok, int lane
 //   blk    shared address of the page's slot
 //   gblk   a function that gives the block in global memory (side-list records past the prefetch)
 //   tier   the block is an FP8 block
+//   buf    the tile (low: the second K tile of INT4)
 // K of an FP8 block is left unscaled (its page's scale is applied to the scores).
 template <int FMT, int D, int ROLE, class Tile, class GBlk>
-__device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool tier, const Tile& tile, const Tile& low,
-                                              int lane) {
+__device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool tier, const Tile& tile, uint32_t buf,
+                                              uint32_t low, int lane) {
   using F = Fmt<FMT>;
   constexpr int NS = D / 16, BLK = F::kMain;
   const int g = lane >> 2, q4 = lane & 3;
-  uint32_t row = tile.lane_row(lane);
+  uint32_t row = buf + tile.lane_row(lane);
   if (FMT == KVQ_FMT_TIERED && tier) {
     const float sc = ROLE == 1 ? ldsf(blk + fp8_sc_off(D)) : 1.f;
 #pragma unroll 1
@@ -229,7 +230,7 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
   }
   if constexpr (BLK == kBlkInt4) {
     constexpr int NG = D / 32, CAP = int4_cap(D), NZ = ROLE == 0 ? 2 : 4;   // NZ: tokens whose scale and minimum the lane needs
-    uint32_t lrow = low.lane_row(lane);
+    uint32_t lrow = low + tile.lane_row(lane);
 #pragma unroll 1
     for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4, lrow += Tile::kStep4) {
       const uint4 w4 = lds128(blk + 4 * NS * lane + 4 * s0);   // one u32 of nibbles per step
@@ -253,7 +254,7 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
         }
         if constexpr (ROLE == 0) {
           int4_k_frag(w[k], S[0], M[0], S[1], M[1], hi, lo);
-          stmatrix4(low.step(lrow, k), lo);
+          stmatrix4(tile.step(lrow, k), lo);
         } else {
           int4_v_frag(w[k], S, M, hi, lo);
         }
@@ -265,8 +266,8 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
       const int t = e / CAP;
       if (e - t * CAP < (int)lds8(blk + int4_cnt_off(D) + t)) {
         const int c = lds8(blk + int4_ch_off(D) + e) & (D - 1);
-        sts16(tile.at(t, c), lds16(blk + int4_val_off(D) + 2 * e));
-        if (ROLE == 0) sts16(low.at(t, c), 0u);
+        sts16(buf + tile.at(t, c), lds16(blk + int4_val_off(D) + 2 * e));
+        if (ROLE == 0) sts16(low + tile.at(t, c), 0u);
       }
     }
   } else if constexpr (BLK == kBlkE2m1) {
@@ -340,7 +341,7 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
         stmatrix4(tile.step(row, k), x);
       }
     }
-    patch.store(tile, lane, [&]() { return gblk() + a3_out_off(D); });
+    patch.store(tile, buf, lane, [&]() { return gblk() + a3_out_off(D); });
   } else {   // 2-bit codebooks
     SidePatch<D> patch;
     if constexpr (BLK != kBlkCb2s) patch.load(blk + cb2_out_off(D), lane);
@@ -367,9 +368,9 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
       __syncwarp();
       const int n = min((int)lds8(blk + cb2s_hdr_off(D)), kMaxStatic), t = lane & 15;
       for (int i = lane >> 4; i < n; i += 2)
-        sts16(tile.at(t, lds8(blk + cb2s_hdr_off(D) + 1 + i) & (D - 1)), lds16(blk + cb2s_val_off(D) + 32 * i + 2 * t));
+        sts16(buf + tile.at(t, lds8(blk + cb2s_hdr_off(D) + 1 + i) & (D - 1)), lds16(blk + cb2s_val_off(D) + 32 * i + 2 * t));
     } else {
-      patch.store(tile, lane, [&]() { return gblk() + cb2_out_off(D); });
+      patch.store(tile, buf, lane, [&]() { return gblk() + cb2_out_off(D); });
     }
   }
 }
@@ -824,41 +825,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     join();
-    int slot = 0;
+    uint64_t* const empty = role ? v_empty : k_empty;
+    uint64_t* const filled = role ? v_full : k_full;
+    const uint32_t base = smem_u32(smem) + role * P::kTile, ring_s = smem_u32(ring);
+    const KTile<D, TOK> kt{j};
+    const VTile<D, TOK> vt{j};
+    int slot = 0, i = i0, left = v.len - kPage * (p0 + i0 * PAGES + j);   // tile; visible tokens from its page on
+#pragma unroll 1
     for (int k = 0; k < n_mine; ++k) {
-      const int i = i0 + k * kTurns;
       asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-      uint64_t* empty = role ? &v_empty[i & 1] : &k_empty[i & 1];
-      if (i >= 2) ok = wait_bar(empty, ((i >> 1) - 1) & 1);
+      if (i >= 2) ok = wait_bar(empty + (i & 1), ((i >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       __syncwarp();   // every lane's part of the copy
       if (!ok) break;
       const int32_t e = ent[slot];
-      const int n = e == kNoPage ? 0 : min(kPage, v.len - kPage * (p0 + i * PAGES + j));
+      const int n = e == kNoPage ? 0 : min(kPage, left);
       const bool tier = FMT == KVQ_FMT_TIERED && e < 0;
-      const uint32_t blk = smem_u32(ring + slot * SLOT);
-      const uint32_t buf = smem_u32(smem) + (i & 1) * P::kBuf;
+      const uint32_t blk = ring_s + slot * SLOT, buf = base + (i & 1) * P::kBuf;
       auto gblk = [&]() { return block_at(e); };
       if (role == 0) {
-        const KTile<D, TOK> kt{buf, j}, low{buf + (P::kPair ? 2 * P::kTile : 0), j};
+        const int at = (i & (kMeta - 1)) * PAGES + j;
         if (lane == 0) {
-          ntok[(i & (kMeta - 1)) * PAGES + j] = n;
-          if (FMT == KVQ_FMT_TIERED) kscale[(i & (kMeta - 1)) * PAGES + j] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
+          ntok[at] = n;
+          if (FMT == KVQ_FMT_TIERED) kscale[at] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
         }
-        if (n > 0) dequant_block<FMT, D, 0>(blk, gblk, tier, kt, low, lane);
+        if (n > 0) dequant_block<FMT, D, 0>(blk, gblk, tier, kt, buf, buf + 2 * P::kTile, lane);
       } else {
-        const VTile<D, TOK> vt{buf + P::kTile, j};
-        if (n > 0) dequant_block<FMT, D, 1>(blk, gblk, tier, vt, vt, lane);
+        if (n > 0) dequant_block<FMT, D, 1>(blk, gblk, tier, vt, buf, 0u, lane);
         if (__builtin_expect(n < kPage, 0)) {
           __syncwarp();
-          zero_tokens<D>(vt, n, lane);
+          zero_tokens<D>(vt, buf, n, lane);
         }
       }
       fence_proxy_async();   // the tile for the MMAs
       __syncwarp();
-      if (lane == 0) mbar_arrive(role ? &v_full[i & 1] : &k_full[i & 1]);
+      if (lane == 0) mbar_arrive(filled + (i & 1));
       issue(k + DEPTH, slot);
-      if (++slot == DEPTH) slot = 0;
+      slot = slot + 1 == DEPTH ? 0 : slot + 1;
+      i += kTurns;
+      left -= kPage * PAGES * kTurns;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
