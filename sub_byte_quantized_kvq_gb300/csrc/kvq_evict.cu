@@ -11,10 +11,11 @@ namespace kvq {
 //
 // One pass over page_lse, which is all there is to read: a CTA takes 128 pages
 // of a sequence, its 16 warps every 16th marked (node, head) row, four
-// coalesced loads of four rows in flight each (8 warps: 19 instead of 15 us for
-// the 67 MB of 16 sequences x 512 rows x 2048 pages, half of them marked); the
-// warps' sums are added in ascending order, so results do not depend on
-// timing.  A row without a token (lse = -inf) adds nothing.
+// coalesced loads of four rows in flight each: 11.5 us for the 67 MB of 16
+// sequences x 512 rows x 2048 pages, half of them marked (15 with a division per
+// row and bounds in every block; 19 so and with 8 warps).  The warps' sums are
+// added in ascending order, so results do not depend on timing.  A row without a
+// token (lse = -inf) adds nothing.
 constexpr int kMassWarps = 16, kMassPages = 128, kMassPer = kMassPages / 32;
 __global__ void __launch_bounds__(32 * kMassWarps) page_mass_kernel(const float* __restrict__ lse,
                                                                     const float* __restrict__ page_lse,

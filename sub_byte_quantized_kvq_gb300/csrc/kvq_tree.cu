@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
     const int r = rw + w;
     if (r >= a.R) continue;
     const size_t o = ((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G;
-    const bool empty = st.m[w] == -INFINITY;
+    const bool empty = st.l[w] == 0.f;   // (a row of NaN scores has no maximum either, but its sum is NaN)
     float y[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) y[i] = empty ? 0.f : st.o[w][i] / st.l[w];

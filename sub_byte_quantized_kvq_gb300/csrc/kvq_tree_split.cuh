@@ -454,9 +454,11 @@ struct SoftmaxRow {
       for (int w = 0; w < W / 32; ++w) tc::wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * w));
       if (__builtin_expect(total != W, 0)) {   // absent tokens
 #pragma unroll
-        for (int j = 0; j < NP; ++j)
+        for (int j = 0; j < NP; ++j) {
+          if (FMT == KVQ_FMT_TIERED && fk[j] == 0.f) fk[j] = 1e-36f;   // a page of zeros: -inf stays -inf
 #pragma unroll
           for (int k = 0; k < kPage; ++k) x[kPage * j + k] = k < n[j] ? x[kPage * j + k] : 0xFF800000u;
+        }
       }
       uint32_t u[W / 2];
       float ps[NP], sum, mb;

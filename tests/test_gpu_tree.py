@@ -358,3 +358,50 @@ def test_row_counts_at_the_kernels_borders(fmt, G, T):
     sees = sees_from_parents(parents)
     for nodes in (None, [T, T // 2, 1, T - 1]):
         check(run(pair, q, k, v, words(sees), nodes, splits=1), pair, q, k, v, sees, nodes)
+
+
+@pytest.mark.parametrize("fmt", [E2M1, CB2], ids=["e2m1", "cb2"])
+def test_a_nan_query_stays_in_its_row(fmt):
+    """A NaN query gives NaN (not an empty row) in its own row, over the cache and over the tree; no other row changes."""
+    pair = build(fmt, 128, [209, 0])
+    T = 6
+    q, k, v, _ = draft(14, 2, T, 2, 8, 128)
+    bad = q.clone()
+    bad[:, 2, 3, 7] = bad[:, 4, 0] = float("nan")
+    keep = np.ones((2, T, 8), bool)
+    keep[:, 2, 3] = keep[:, 4, 0] = False
+    for tree in ((k, v), (None, None)):
+        clean, got = run(pair, q, *tree), run(pair, bad, *tree)
+        live = [0, 1] if tree[0] is not None else [0]
+        for a, e in zip(got, clean):
+            np.testing.assert_array_equal(a[keep], e[keep])
+            for b in live:
+                assert np.isnan(a[b, 2, 3][~np.isneginf(e[b, 2, 3])]).all() and np.isnan(a[b, 4, 0][~np.isneginf(e[b, 4, 0])]).all()
+
+
+@pytest.mark.parametrize("G,T", [(4, 2), (8, 16)])
+def test_zero_keys_in_a_cut_fp8_page(G, T):
+    """A tier page of zeros has scale 0; the bound on the length ends inside it: uniform weights over what is visible."""
+    pair = Pair(TIERED, 2, 2, 128, 8, seed=3, tiers=np.array([[False, True, False, False] * 2] * 2))
+    k, v = make_kv(5, 2, 64, 2, 128, "normal", 4, 8.0)
+    pair.append(torch.zeros_like(k), v)
+    q, kt, vt, _ = draft(2, 2, T, 2, 2 * G, 128)
+    for max_len in (24, 17, 64):
+        got = run(pair, q, max_len=max_len)
+        check(got, pair, q, max_len=max_len)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-30])
+def test_scales_that_are_not_positive(scale):
+    for fmt in (INT4, TIERED):
+        pair = build(fmt, 128, [209, 40])
+        q, k, v, parents = draft(31, 2, 5, 2, 8, 128)
+        sees = sees_from_parents(parents)
+        lse = torch.empty((2, 5, 8), device="cuda")
+        out = kvq.kvq_tree_attention(pair.gpu, q.cuda(), scale, 209, k.cuda(), v.cuda(), torch.from_numpy(words(sees)).cuda(),
+                                     out_dtype=torch.float32, lse=lse)
+        f = lambda x: x.float().numpy()
+        e_out, e_lse, e_page, slack = tree_rows(pair.ref, f(q), scale, f(k), f(v), sees, None, 209)
+        b_out, b_lse, _ = bounds((e_out, e_lse, e_page), slack, abs(scale), 128)
+        assert (np.abs(out.cpu().numpy() - e_out) <= b_out).all()
+        assert (np.abs(lse.cpu().numpy() - e_lse) <= b_lse).all()
