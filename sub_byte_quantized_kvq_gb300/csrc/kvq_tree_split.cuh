@@ -85,6 +85,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
   return true;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3])
@@ -566,6 +567,57 @@ struct SoftmaxRow {
   }
 };
 
+// A segment's partial state from shared memory (xo: [128][D + 4], xml: [128]) to the workspace, by n_sm warps; REP
+// copies of a row are joined.  Rows are taken four at a time, so that their loads are in flight together (one at a
+// time, 128 rows took 6.3 us).
+template <int D, int REP>
+__device__ __forceinline__ void store_partial(const TreeArgs& a, size_t part0, const float* xo, const float2* xml, int rows, int n_sm) {
+  constexpr int XS = D + 4, PER = kM / REP, U = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r0 = warp; r0 < rows; r0 += U * n_sm) {
+    float2 ml[U][REP];
+    float4 x[U][REP];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = min(r0 + u * n_sm, rows - 1);
+#pragma unroll
+      for (int c = 0; c < REP; ++c) {
+        ml[u][c] = xml[c * PER + r];
+        x[u][c] = *reinterpret_cast<const float4*>(xo + (c * PER + r) * XS + 4 * (lane & (D / 4 - 1)));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * n_sm;
+      float M = ml[u][0].x, L = ml[u][0].y;
+      float4 o = x[u][0];
+      if (REP > 1) {
+#pragma unroll
+        for (int c = 1; c < REP; ++c) M = fmaxf(M, ml[u][c].x);
+        L = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < REP; ++c) {
+          const bool has = ml[u][c].x != -INFINITY;
+          const float w = has ? ex2(ml[u][c].x - M) : 0.f;
+          L = fmaf(w, ml[u][c].y, L);
+          if (has) {
+            o.x = fmaf(w, x[u][c].x, o.x);
+            o.y = fmaf(w, x[u][c].y, o.y);
+            o.z = fmaf(w, x[u][c].z, o.z);
+            o.w = fmaf(w, x[u][c].w, o.w);
+          }
+        }
+      }
+      if (r < rows) {
+        if (4 * lane < D) *reinterpret_cast<float4*>(a.part_o + (part0 + r) * D + 4 * lane) = o;
+        if (lane == 0) a.part_ml[part0 + r] = make_float2(M, L);
+      }
+    }
+  }
+}
+
 // Most rows of the FEW variant.
 template <int FMT, int D>
 constexpr int few_rows() { return kM / (Plan<FMT, D>::kTok / 32); }
@@ -586,6 +638,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   const int nmt = (a.R + kM - 1) / kM;
   const int split = blockIdx.x, h = blockIdx.y / nmt, r0 = (blockIdx.y % nmt) * kM, b = blockIdx.z;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  {   // on its way to the L2 cache while the lengths are read: the split's page table and the query rows
+    const int p = split * a.pps + 32 * tid, r = r0 + (tid - 32) / (D / 64);
+    if (tid < 32) {
+      if (p < min(split * a.pps + a.pps, a.ppsm)) prefetch_l2(a.page_table + (size_t)b * a.ppsm + p);
+    } else if (r < min(r0 + kM, a.R)) {
+      prefetch_l2(a.q + (((size_t)b * a.T + r / a.G) * a.Hq + (size_t)h * a.G + r % a.G) * D + (tid - 32) % (D / 64) * 64);
+    }
+  }
   const SeqView v = seq_view(a, b);
   const int live = min(v.nodes * a.G, a.R), rows = min(kM, live - r0), r_end = min(r0 + kM, a.R);
   if (split == 0 && blockIdx.y == 0 && tid == 0 && a.seq_lens[b] > a.max_seq_len) atomicOr(a.status, KVQ_STATUS_SEQ_TOO_LONG);
@@ -730,27 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       }
       asm volatile("bar.sync 1, %0;" ::"r"(n_thr) : "memory");
       if (ok) {
-        const int per = kM / rep;   // threads of one copy
-        for (int r = warp; r < rows; r += n_sm) {
-          float M = -INFINITY, L = 0.f;
-          for (int c = 0; c < rep; ++c) M = fmaxf(M, xml[c * per + r].x);
-          float4 o;
-          const bool mine = 4 * lane < D;
-          o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = 0; c < rep; ++c) {
-            const float2 ml = xml[c * per + r];
-            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            L = fmaf(w, ml.y, L);
-            if (mine && ml.x != -INFINITY) {
-              const float4 x = *reinterpret_cast<const float4*>(xo + (c * per + r) * XS + 4 * lane);
-              o.x = fmaf(w, x.x, o.x);
-              o.y = fmaf(w, x.y, o.y);
-              o.z = fmaf(w, x.z, o.z);
-              o.w = fmaf(w, x.w, o.w);
-            }
-          }
-          if (mine) *reinterpret_cast<float4*>(a.part_o + (part0 + r) * D + 4 * lane) = o;
-          if (lane == 0) a.part_ml[part0 + r] = make_float2(M, L);
+        if constexpr (FEW) {
+          store_partial<D, TOK / 32>(a, part0, xo, xml, rows, n_sm);
+        } else {
+          if (rep == 1) store_partial<D, 1>(a, part0, xo, xml, rows, n_sm);
+          else store_partial<D, 2>(a, part0, xo, xml, rows, n_sm);
         }
       }
     }
