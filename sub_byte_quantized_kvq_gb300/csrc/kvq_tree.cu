@@ -285,16 +285,17 @@ static TreeKernel tree_kernel(int fmt, int D, int R) {
 }
 
 // One CTA runs per SM, so the cached pages of the call take
-// waves(S) x (tiles of a split + what a CTA costs besides, about three tiles:
-// barriers, tensor memory, the query, the pipeline's fill and drain, the
-// partial state) -- the smallest product, and among equals the fewest splits.
+// waves(S) x (tiles of a split + what a CTA costs besides: barriers, tensor
+// memory, the query, the pipeline's fill and drain, the partial state; measured
+// 4 us or three tiles with 8 rows, 8 us or five and a half with 128) -- the
+// smallest product, and among equals the fewest splits.
 int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms) {
   const long long tiles = (max_seq_len + kPage * kTreeTilePages - 1) / (kPage * kTreeTilePages);
   const long long units = (long long)B * Hkv * ((R + kTreeRows - 1) / kTreeRows);
   long long best = 1, cost = -1;
   const long long most = std::min({std::max(tiles, 1ll), (8ll * sms + units - 1) / units, 256ll});   // (never over 8 waves)
   for (long long s = 1; s <= most; ++s) {
-    const long long c = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + 3);
+    const long long c = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + 5);
     if (cost < 0 || c < cost) {
       cost = c;
       best = s;
