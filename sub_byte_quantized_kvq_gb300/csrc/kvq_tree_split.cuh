@@ -27,7 +27,7 @@
 //
 // What bounds it: instruction issue.  A tile of 128 tokens is about 1024 cycles
 // of MMA at 128 rows and 800-1200 of this SM's share of the measured HBM rate,
-// but some 7,000 warp instructions (expansion, exponentials, waits) for four
+// but some 6,700 warp instructions (expansion, exponentials, waits) for four
 // schedulers; measured 16 sequences x 32k tokens: FP4 at 128 rows 360 us, tiered
 // at 8 rows 317 us.  Addresses that run along with a warp's tiles, instead of
 // computed per tile, gave 1-2%.
