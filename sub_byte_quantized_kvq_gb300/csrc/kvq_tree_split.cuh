@@ -13,8 +13,9 @@
 //                   swizzle; the block layout holds mma fragments, which
 //                   stmatrix turns into rows; outliers are stored over their slots
 //   MMA warp        tcgen05.mma with Q and P from tensor memory, the tiles from
-//                   shared memory; S(i + 1) is issued before PV(i), so the tensor
-//                   cores work while the softmax warps do
+//                   shared memory; S(i + 1) is issued before PV(i), once PV(i - 1)
+//                   is done with P(i - 1) in its columns, so the tensor cores work
+//                   while the softmax warps do
 //   4 softmax warps one row a thread (tensor-memory lane): p = 2^(s - m) with a
 //                   reference m that is raised only when the sums ask for it,
 //                   page sums for page_lse; P goes over S's own columns
@@ -925,6 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       const uint64_t buf_desc = tc::desc_sw128(smem_u32(smem));
       auto scores = [&](int i) {
         if (!wait_bar(&k_full[i & 1], (i >> 1) & 1)) return false;
+        // S(i) goes over P(i - 2), which PV(i - 2) reads: MMAs with different accumulators have no order of their own
+        if (i >= 2 && !wait_bar(&v_empty[i & 1], ((i >> 1) - 1) & 1)) return false;
         tc::fence_after();
         const uint64_t kt = buf_desc + (i & 1) * (P::kBuf >> 4);
 #pragma unroll
