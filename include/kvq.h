@@ -147,8 +147,9 @@ typedef struct {
 /* The cache.  All pointers are device memory owned by the caller.
  *   pool        main pool: block (phys, head, role) at
  *               ((phys * Hkv + head) * 2 + role) * kvq_block_bytes(cfg, 0); role 0 = K, 1 = V.
- *               Zero-fill it once before first use.
+ *               Zero-fill it once before first use.  16-byte aligned.
  *   tier_pool   FP8 pool (TIERED only, else NULL), blocks of kvq_block_bytes(cfg, 1).
+ *               16-byte aligned.
  *   page_table  int32 [num_seqs][pages_per_seq_max]: physical page of each
  *               logical page; bit 31 selects the tier pool (TIERED only).
  *               Entries are read only for pages a call touches.

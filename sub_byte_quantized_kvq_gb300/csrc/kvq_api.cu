@@ -122,8 +122,10 @@ static bool paged_format(int f) {
   return f == KVQ_FMT_CB2_OUTLIER || f == KVQ_FMT_TIERED || f == KVQ_FMT_CB2_STATIC || f == KVQ_FMT_ASYM3_OUTLIER ||
          f == KVQ_FMT_CB2_GROUP4;
 }
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 static bool cache_ok(const kvq_config* c, const kvq_cache* k) {
   if (!k || !k->pool || !k->page_table || !k->seq_lens || !k->status) return false;
+  if (!aligned16(k->pool) || !aligned16(k->tier_pool)) return false;   // blocks are copied and written 16 bytes at a time
   if (paged_format(c->format) && !k->staging) return false;
   if (c->format == KVQ_FMT_CB2_STATIC && !k->static_mask) return false;
   if (c->format == KVQ_FMT_TIERED && c->num_tier_pages > 0 && !k->tier_pool) return false;
@@ -247,8 +249,6 @@ kvq_status kvq_quantize_append(const kvq_config* cfg, const kvq_cache* cache, co
   a.in_dtype = in_dtype;
   return cuda_status(append_launch(a, cfg->head_dim, static_cast<cudaStream_t>(stream)));
 }
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 kvq_status kvq_project_append(const kvq_config* cfg, const kvq_cache* cache, const void* x, int32_t hidden,
                               const void* w_k, const void* w_v, int32_t t_new, const int32_t* t_per_seq,

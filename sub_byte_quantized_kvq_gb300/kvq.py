@@ -161,12 +161,16 @@ class QuantizedKVCache:
                      sigma: float = 3.0, lloyd_iters: int = 16, decode_math: int = KVQ_DECODE_AUTO) -> "QuantizedKVCache":
         """A handle on device buffers the caller owns (page_table int32
         [num_seqs, pages_per_seq_max], seq_lens int32 [num_seqs], status int32
-        [1], pool / tier_pool uint8 of whole blocks, staging fp32); nothing is
-        allocated or copied, and the pools' sizes give the page counts."""
+        [1], pool / tier_pool uint8 of whole blocks, 16-byte aligned, staging
+        fp32); nothing is allocated or copied, and the pools' sizes give the
+        page counts."""
         num_seqs, ppsm = page_table.shape
         buffers = [pool, page_table, seq_lens, status, staging, tier_pool, static_mask]
         assert all(t is None or (t.is_contiguous() and t.device == pool.device) for t in buffers)
         assert page_table.dtype == seq_lens.dtype == status.dtype == torch.int32 and seq_lens.numel() == num_seqs
+        for t in (pool, tier_pool):
+            assert t is None or (t.dtype == torch.uint8 and t.data_ptr() % 16 == 0)
+        assert static_mask is None or static_mask.dtype == torch.uint8
         self = cls.__new__(cls)
         self.cfg = kvq_config(num_seqs, num_kv_heads, head_dim, ppsm, 1, 1 if tier_pool is not None else 0, fmt,
                               lloyd_iters, sigma, static_mask.shape[-1] if static_mask is not None else 0, decode_math)
