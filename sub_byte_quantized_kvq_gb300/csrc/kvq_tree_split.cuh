@@ -24,7 +24,8 @@
 // exact in fp16 (INT4: an fp16 pair, two MMAs); S, m, l and O are fp32.  P is
 // rounded to fp16 (at most 2^-11 relative; biased by 2^kPBias so that small
 // p keep their bits), V to fp16 where the format's value has more (INT4, FP8
-// tier): for a bf16 result both are below its own rounding.
+// tier): for a bf16 result both are below its own rounding.  An FP8 page's V may
+// have any magnitude: v_shift moves a power of two of its scale to P.
 //
 // What bounds it: instruction issue.  A tile of 128 tokens is about 1024 cycles
 // of MMA at 128 rows and 800-1200 of this SM's share of the measured HBM rate,
@@ -63,7 +64,11 @@ struct Plan {
   static constexpr int kBuf = (kPair ? 3 : 2) * kTile;       // one buffer: K [, K low], V
   // a page's slot: its (virtual) block from offset 0 (the group format copies the group's codebook into each)
   static constexpr int kSlot = F::kGroup ? 12 * D + kOutPrefetch : half_slot_bytes<FMT, D>();
-  static constexpr int misc(int depth) { return 8 * 13 + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8; }
+  static constexpr bool kShift = FMT == KVQ_FMT_TIERED;      // pages have a V shift
+  static constexpr int misc(int depth) {
+    return 8 * 13 + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8 +
+           (kShift ? kMeta * kPages * 8 + 4 * kDequantWarps * depth : 0);
+  }
   static constexpr int smem(int depth) {   // 1024: alignment slack
     return 1024 + 2 * kBuf + kDequantWarps * depth * kSlot + misc(depth);
   }
@@ -116,6 +121,21 @@ __device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t& x, uint32_t& y) {
       : "=r"(x), "=r"(y)
       : "r"(w));
 }
+
+// The power of two b of an FP8 page's V scale that goes to P instead of the fp16
+// tile: P holds p 2^b, the tile v 2^-b.  With a scale of 2^e to 2^(e+1) and codes of
+// 2^-9 to 448, e - b in -5..6 keeps every element in fp16's normal range (rounded
+// once, by 2^-11 at most), so b follows e outside -9..2; inside (a page's largest
+// |v| between 0.9 and 3584) it stays at -4, and CB2 pages have 0.  The reference m
+// of a row is of p 2^b, and the fp32 sums are of p: b is held to -48..48, which leaves
+// the heaviest p above 2^-90 whatever the other pages have.  So elements of a page
+// whose largest |v| is below 5e-14 are off by up to 2^-73, and one above 1.6e19 is
+// infinite.  A scale of 0 has b = -4.
+__device__ __forceinline__ int v_shift(float scale) {
+  const int e = scale == 0.f ? 0 : (int)((__float_as_uint(scale) >> 23) & 255u) - 127;
+  return max(-48, min(48, min(max(-4, e - 6), e + 5)));
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }   // |e| < 127
 
 // Where a page's values go in a swizzled tile, as offsets from its start.  A row
 // is 64 fp16 (128 bytes); 16-byte chunk k of row r lies at chunk k ^ (r % 8).
@@ -200,7 +220,7 @@ __device__ __forceinline__ void zero_tokens(const Tile& tile, uint32_t buf, int 
 //   gblk   a function that gives the block in global memory (side-list records past the prefetch)
 //   tier   the block is an FP8 block
 //   buf    the tile (low: the second K tile of INT4)
-// K of an FP8 block is left unscaled (its page's scale is applied to the scores).
+// K of an FP8 block is left unscaled (its page's scale is applied to the scores), V is scaled by all but v_shift's power.
 template <int FMT, int D, int ROLE, class Tile, class GBlk>
 __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool tier, const Tile& tile, uint32_t buf,
                                               uint32_t low, int lane) {
@@ -209,7 +229,11 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
   const int g = lane >> 2, q4 = lane & 3;
   uint32_t row = buf + tile.lane_row(lane);
   if (FMT == KVQ_FMT_TIERED && tier) {
-    const float sc = ROLE == 1 ? ldsf(blk + fp8_sc_off(D)) : 1.f;
+    float sc = 1.f;
+    if (ROLE == 1) {
+      sc = ldsf(blk + fp8_sc_off(D));
+      sc *= exp2_int(-v_shift(sc));
+    }
 #pragma unroll 1
     for (int s0 = 0; s0 < NS; s0 += 4, row += Tile::kStep4) {
       const uint4 w0 = lds128(blk + 8 * NS * lane + 8 * s0), w1 = lds128(blk + 8 * NS * lane + 8 * s0 + 16);
@@ -410,9 +434,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A softmax thread's row: m in log2 units, p = 2^(s f - m + kPBias), l the fp32 sum of p.
+// A softmax thread's row: m in log2 units, p = 2^(s f - m + kPBias), l the fp32 sum of p.  A page with a V shift b:
+// P = p 2^b, and m is raised by what P needs.
 template <int FMT, int D>
 struct SoftmaxRow {
+  static constexpr bool kShift = Plan<FMT, D>::kShift;
   float m = -INFINITY, l = 0.f, f;
   float* lse_row;
   bool vec;   // lse_row may be written two pages at a time
@@ -424,8 +450,8 @@ struct SoftmaxRow {
   // says that the MMAs are done with it) and the tile's earlier P -- and is
   // computed again.
   template <int W, class OFree>
-  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c_lo, int c_hi, const int32_t* ntok, const float* ks, int pt,
-                                       int p1, bool has_o, OFree&& o_free) {
+  __device__ __forceinline__ bool tile(uint32_t ts, uint32_t to, int c_lo, int c_hi, const int32_t* ntok, const float* ks,
+                                       uint32_t vs, int pt, int p1, bool has_o, OFree&& o_free) {
     constexpr int NP = W / kPage;   // pages of a chunk
     uint32_t x[W];
     auto load = [&](int c) {
@@ -467,10 +493,15 @@ struct SoftmaxRow {
 #pragma unroll 1
       for (bool again = false;; again = true) {
         mb = (m == -INFINITY ? 0.f : m) - kPBias;
-        const uint64_t nb = pack2(-mb, -mb);
+        const uint64_t nb0 = pack2(-mb, -mb);
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
           const uint64_t f2 = pack2(fk[j], fk[j]);
+          uint64_t nb = nb0;
+          if constexpr (kShift) {
+            const float b = shift(vs, pg + j) - mb;
+            nb = pack2(b, b);
+          }
           uint64_t acc = 0;   // {0.f, 0.f}
 #pragma unroll
           for (int k = 0; k < kPage; k += 2) {
@@ -489,7 +520,7 @@ struct SoftmaxRow {
         if (__builtin_expect(again || !__any_sync(0xffffffffu, need), 1)) break;
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) mx = fmaxf(mx, page_max(x + kPage * j) * fk[j]);
+        for (int j = 0; j < NP; ++j) mx = fmaxf(mx, kShift ? fmaf(page_max(x + kPage * j), fk[j], shift(vs, pg + j)) : page_max(x + kPage * j) * fk[j]);
         const bool up = need && mx > m;
         const float alpha = up ? ex2(m - mx) : 1.f;
         l *= alpha;
@@ -506,12 +537,20 @@ struct SoftmaxRow {
         for (int k = c_lo / 32; k < c / 32; ++k) scale_p(ts + 16 * k, alpha);
         tc::wait_st();
       }
+      if constexpr (kShift) {
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NP; j += 2) {
+          const uint4 v4 = lds128(vs + 8 * (pg + j));
+          sum = fmaf(ps[j + 1], __uint_as_float(v4.w), fmaf(ps[j], __uint_as_float(v4.y), sum));
+        }
+      }
       l += sum;
       if (lse_row) {
 #pragma unroll
         for (int j = 0; j < NP; j += 2) {
-          const float y0 = page_sum(x + kPage * j, n[j], fk[j], mb, ps[j]);
-          const float y1 = page_sum(x + kPage * (j + 1), n[j + 1], fk[j + 1], mb, ps[j + 1]);
+          const float y0 = page_sum(x + kPage * j, n[j], fk[j], kShift ? mb - shift(vs, pg + j) : mb, ps[j]);
+          const float y1 = page_sum(x + kPage * (j + 1), n[j + 1], fk[j + 1], kShift ? mb - shift(vs, pg + j + 1) : mb, ps[j + 1]);
           const int p = pt + pg + j;
           if (vec && p + 1 < p1) {
             *reinterpret_cast<float2*>(lse_row + p) = make_float2(y0, y1);
@@ -527,6 +566,9 @@ struct SoftmaxRow {
     }
     return true;
   }
+  // A page's V shift, read from shared memory (vs: the tile's [PAGES] of b, 2^-b) wherever it is used: in registers
+  // they cost the kernel of many rows 90 bytes of spills.
+  static __device__ __forceinline__ float shift(uint32_t vs, int page) { return ldsf(vs + 8 * page); }
   static __device__ __forceinline__ float page_max(const uint32_t* y) {
     float m0 = __uint_as_float(y[0]), m1 = __uint_as_float(y[1]);
 #pragma unroll
@@ -665,12 +707,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
 
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
   uint8_t* slots = smem + 2 * P::kBuf;                                    // [kDequantWarps][DEPTH]
-  uint64_t *k_full = reinterpret_cast<uint64_t*>(slots + kDequantWarps * DEPTH * SLOT), *k_empty = k_full + 2, *v_full = k_empty + 2, *v_empty = v_full + 2,
-           *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
+  float2* vshift = reinterpret_cast<float2*>(slots + kDequantWarps * DEPTH * SLOT);   // [kMeta][PAGES] b, 2^-b of an FP8 page's V (tiered only)
+  uint64_t *k_full = reinterpret_cast<uint64_t*>(vshift + (P::kShift ? kMeta * PAGES : 0)), *k_empty = k_full + 2, *v_full = k_empty + 2,
+           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
   int32_t* ntok = reinterpret_cast<int32_t*>(done + 1);                   // [kMeta][PAGES] tokens of a tile's pages
   float* kscale = reinterpret_cast<float*>(ntok + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
   int32_t* entries = reinterpret_cast<int32_t*>(kscale + kMeta * PAGES);  // [kDequantWarps][DEPTH] page-table entries of the slots
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(entries + kDequantWarps * DEPTH);
+  float* vscales = reinterpret_cast<float*>(entries + kDequantWarps * DEPTH);   // [kDequantWarps][DEPTH] V scales of a K warp's FP8 pages (tiered only)
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(vscales + (P::kShift ? kDequantWarps * DEPTH : 0));
   const int rep = FEW ? TOK / 32 : TOK == 128 && rows <= 64 ? 2 : 1, row = tid % (kM / rep);
   const int n_sm = rep > 1 ? 4 : (rows + 31) / 32;   // softmax warps with rows
   if (tid == 0) {
@@ -743,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       const uint32_t lanes = (uint32_t)(32 * warp) << 16;
       SoftmaxRow<FMT, D> sr;
       sr.f = f;
+      const uint32_t vshift_s = smem_u32(vshift);
       sr.lse_row = a.page_lse && row < rows ? page_lse_row(a, b, h, r0 + row) : nullptr;
       sr.vec = (a.P & 1) == 0 && (reinterpret_cast<uintptr_t>(a.page_lse) & 7) == 0;
       const int chunks = TOK / 32 / rep, c0 = warp / (4 / rep) * chunks;   // this warp's 32-column chunks
@@ -757,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           return __all_sync(0xffffffffu, wait_bar(&v_empty[(i - 1) & 1], ((i - 1) >> 1) & 1));
         };
         const int lo = 32 * c0, hi = 32 * (c0 + chunks);
-        ok = sr.template tile<FEW ? 32 : 64>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, pt, p1, i > 0, o_free);
+        ok = sr.template tile<FEW ? 32 : 64>(ts, t_o + lanes, lo, hi, ntok + slot, kscale + slot, vshift_s + 8 * slot, pt, p1, i > 0, o_free);
         if (!ok) break;
         if (rep > 1) {   // the columns of the row's other copies: P = 0
           const uint32_t z[16] = {};
@@ -811,6 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     // The page's entry in this warp's k-th tile: a window of 32 in the lanes.  kNoPage: absent, or bad.
     // The group format looks at the whole of the page's group, which the bound on the length may cut.
     int32_t* ent = entries + wi * DEPTH;
+    float* vsc = vscales + wi * DEPTH;
     int win_base = 0, win = kNoPage;
     auto load_window = [&](int base) {
       win_base = base;
@@ -860,6 +906,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
                  : F::kMain == kBlkCb2s        ? 12 * D + 16 + 32 * a.n_static
                                                : fetch_bytes<D>(F::kMain),
                  std::integral_constant<int, SLOT>{});
+            if (P::kShift && role == 0 && e < 0 && lane == 0)   // the V block's scale, beside the K block
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(vsc + slot)),
+                           "l"(block_at(e) + block_stride(kBlkFp8, D) + fp8_sc_off(D))
+                           : "memory");
           }
         }
       }
@@ -894,7 +944,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         const int at = (i & (kMeta - 1)) * PAGES + j;
         if (lane == 0) {
           ntok[at] = n;
-          if (FMT == KVQ_FMT_TIERED) kscale[at] = tier ? ldsf(blk + fp8_sc_off(D)) : 1.f;
+          if (P::kShift) {
+            kscale[at] = 1.f;
+            vshift[at] = make_float2(0.f, 1.f);
+            if (tier) {
+              const int sh = v_shift(vsc[slot]);
+              kscale[at] = ldsf(blk + fp8_sc_off(D));
+              vshift[at] = make_float2((float)sh, exp2_int(-sh));
+            }
+          }
         }
         if (n > 0) dequant_block<FMT, D, 0>(blk, gblk, tier, kt, buf, buf + 2 * P::kTile, lane);
       } else {
