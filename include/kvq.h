@@ -324,8 +324,9 @@ kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const kvq_cache* 
 /* Most nodes of a tree (one bit each in a 64-bit ancestor word). */
 #define KVQ_TREE_MAX_NODES 64
 
-/* Workspace bytes kvq_tree_attention needs for (num_q_heads, num_nodes,
- * max_seq_len, num_splits); num_splits = 0 asks for the library's choice. */
+/* Workspace bytes that are enough for kvq_tree_attention with num_q_heads heads,
+ * up to num_nodes nodes and any bound on the lengths up to max_seq_len, at
+ * num_splits splits; num_splits = 0: at the library's choice for each call. */
 kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, int32_t num_nodes, int32_t max_seq_len,
                                     int32_t num_splits, size_t* bytes);
 

@@ -468,8 +468,17 @@ kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, 
   if (!bytes) return KVQ_ERR_INVALID_ARG;
   const kvq_status st = tree_shape_ok(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
   if (st != KVQ_OK) return st;
-  const int S = tree_splits(cfg, num_q_heads, num_nodes, max_seq_len, num_splits);
-  *bytes = tree_rows(cfg, num_q_heads, num_nodes, S) * (cfg->head_dim * sizeof(float) + sizeof(float2));
+  // The library's choice is no monotone function of the length and the nodes (a shorter bound may take more splits),
+  // so its workspace is that of the most splits any smaller call takes: at most about eight waves of CTAs' states.
+  const int sms = std::max(num_sms(), 1);
+  size_t rows = 0;
+  for (int t = num_splits ? num_nodes : 1; t <= num_nodes; ++t) {
+    const int S = num_splits ? num_splits
+                             : tree_most_splits(cfg->num_seqs, cfg->num_kv_heads, num_q_heads / cfg->num_kv_heads * t,
+                                                visible_bound(cfg, max_seq_len), sms);
+    rows = std::max(rows, tree_rows(cfg, num_q_heads, t, S));
+  }
+  *bytes = rows * (cfg->head_dim * sizeof(float) + sizeof(float2));
   return KVQ_OK;
 }
 

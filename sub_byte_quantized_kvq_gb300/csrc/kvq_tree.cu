@@ -289,11 +289,18 @@ static TreeKernel tree_kernel(int fmt, int D, int R) {
 // memory, the query, the pipeline's fill and drain, the partial state; measured
 // 4 us or three tiles with 8 rows, 8 us or five and a half with 128) -- the
 // smallest product, and among equals the fewest splits.
+static long long tree_tiles(int max_seq_len) {
+  return (max_seq_len + kPage * kTreeTilePages - 1) / (kPage * kTreeTilePages);
+}
+static long long tree_units(int B, int Hkv, int R) { return (long long)B * Hkv * ((R + kTreeRows - 1) / kTreeRows); }
+int tree_most_splits(int B, int Hkv, int R, int max_seq_len, int sms) {   // (never over 8 waves)
+  const long long units = tree_units(B, Hkv, R);
+  return (int)std::min({std::max(tree_tiles(max_seq_len), 1ll), (8ll * sms + units - 1) / units, 256ll});
+}
 int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms) {
-  const long long tiles = (max_seq_len + kPage * kTreeTilePages - 1) / (kPage * kTreeTilePages);
-  const long long units = (long long)B * Hkv * ((R + kTreeRows - 1) / kTreeRows);
+  const long long tiles = tree_tiles(max_seq_len), units = tree_units(B, Hkv, R);
+  const long long most = tree_most_splits(B, Hkv, R, max_seq_len, sms);
   long long best = 1, cost = -1;
-  const long long most = std::min({std::max(tiles, 1ll), (8ll * sms + units - 1) / units, 256ll});   // (never over 8 waves)
   for (long long s = 1; s <= most; ++s) {
     const long long c = (units * s + sms - 1) / sms * ((tiles + s - 1) / s + 5);
     if (cost < 0 || c < cost) {

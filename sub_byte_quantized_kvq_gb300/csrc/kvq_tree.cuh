@@ -92,6 +92,8 @@ TreeKernel tree_kernel_cb2g(int D, int R);
 cudaError_t tree_launch(const TreeArgs& a, int D, cudaStream_t st);
 // Splits tree_launch's first kernel is given when the caller leaves the choice.
 int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms);
+// The largest count that choice takes for any bound on the lengths up to max_seq_len (grows with it).
+int tree_most_splits(int B, int Hkv, int R, int max_seq_len, int sms);
 
 cudaError_t page_mass_launch(const float* lse, const float* page_lse, const uint64_t* nodes, float decay, const float* in,
                              float* out, int B, int T, int Hq, int P, int ppsm, cudaStream_t st);
