@@ -367,10 +367,17 @@ def _refs(cache: "QuantizedKVCache"):
     return r
 
 
-def _scratch(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor allocated here for a call on `stream`: its memory is not handed on before that stream is done with it."""
-    if stream is not None:
-        t.record_stream(stream)
+def _made_on(stream, make, returned: bool = False) -> torch.Tensor:
+    """make(), a tensor allocated here for a call on `stream` (None: the current stream), from that stream's
+    memory: what another stream's pending work still uses is never handed to it.  returned: the caller
+    goes on with it on the current stream."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(here)
     return t
 
 
@@ -433,7 +440,7 @@ def kvq_tree_attention(cache: QuantizedKVCache, q: torch.Tensor, softmax_scale: 
     if nodes_per_seq is not None:
         assert nodes_per_seq.dtype is torch.int32 and nodes_per_seq.is_contiguous() and nodes_per_seq.shape == (B,)
     if out is None:
-        out = _scratch(torch.empty(shape, dtype=out_dtype, device=q.device), stream)
+        out = _made_on(stream, lambda: torch.empty(shape, dtype=out_dtype, device=q.device), returned=True)
     dt = _DTYPE[out.dtype]
     assert dt != KVQ_F16 and out.is_contiguous() and out.shape == shape
     if lse is not None:
@@ -442,7 +449,7 @@ def kvq_tree_attention(cache: QuantizedKVCache, q: torch.Tensor, softmax_scale: 
         P = (min(max_seq_len, 16 * cfg.pages_per_seq_max) + 15) // 16
         assert page_lse.dtype is torch.float32 and page_lse.is_contiguous() and page_lse.shape == (B, T, Hq, P)
     if workspace is None:
-        workspace = _scratch(alloc_tree_workspace(cache, Hq, T, max_seq_len, num_splits), stream)
+        workspace = _made_on(stream, lambda: alloc_tree_workspace(cache, Hq, T, max_seq_len, num_splits))
     _check_on(index, q, k_tree, v_tree, tree_mask, nodes_per_seq, out, lse, page_lse, workspace)
     _call("kvq_tree_attention", index, stream, pcfg, pcache, q.data_ptr(), Hq, T, _addr(k_tree), _addr(v_tree),
           _addr(tree_mask), per_seq, _addr(nodes_per_seq), softmax_scale, max_seq_len, num_splits, out.data_ptr(), dt,
@@ -487,7 +494,7 @@ def kvq_evict_pages(cache: QuantizedKVCache, mass: torch.Tensor, keep_pages: int
     seq_lens_out = cache.seq_lens if seq_lens_out is None else seq_lens_out
     mass_out = mass if mass_out is None else mass_out
     if evicted is None:
-        evicted = _scratch(torch.empty(B, dtype=torch.int32, device=cache.device), stream)
+        evicted = _made_on(stream, lambda: torch.empty(B, dtype=torch.int32, device=cache.device), returned=True)
     f32, i32 = torch.float32, torch.int32
     assert mass.dtype is f32 and mass_out.dtype is f32 and mass.is_contiguous() and mass_out.is_contiguous()
     assert mass.shape == shape and mass_out.shape == shape and page_table_out.shape == shape

@@ -37,3 +37,58 @@ def test_one_workspace_for_shorter_calls(B, Hkv, G, T, L):
         one = kvq.alloc_tree_workspace(cache, Hkv * G, T, L, 1)
         kvq.kvq_tree_attention(cache, q, 0.1, L, num_splits=2, out=out, workspace=one)
     assert cache.status_word() == 0
+
+
+def pointers(monkeypatch, name, position, call):
+    """The pointer that `call` hands to the library as argument `position` of `name` (nothing is launched)."""
+    seen = []
+    monkeypatch.setattr(kvq, "_call", lambda what, index, stream, *args: seen.append((what, args)))
+    result = call()
+    monkeypatch.undo()
+    assert [w for w, _ in seen] == [name]
+    return seen[0][1][position], result
+
+
+def test_memory_made_for_another_stream_is_that_streams_own(monkeypatch):
+    """What a call on another stream allocates does not come from blocks that the current stream has just given
+    up (its pending work may still use them), and what it returns is held for the current stream."""
+    cache = empty_cache(4, 2, 4096)
+    side = torch.cuda.Stream()
+    q = torch.zeros((4, 8, 8, 64), dtype=torch.bfloat16, device="cuda")
+    mass = torch.zeros((4, 256), device="cuda")
+    tree = lambda: kvq.kvq_tree_attention(cache, q, 0.1, 4096, stream=side)
+    for name, position, nbytes, call in (("kvq_tree_attention", 13, q.nbytes, tree),
+                                         ("kvq_tree_attention", 17, kvq.alloc_tree_workspace(cache, 8, 8, 4096).nbytes, tree),
+                                         ("kvq_evict_pages", 9, 16, lambda: kvq.kvq_evict_pages(cache, mass, 8, stream=side))):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        held = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        given_up = {t.data_ptr() for t in held}
+        del held
+        ptr, result = pointers(monkeypatch, name, position, call)
+        assert ptr and ptr not in given_up
+        if position != 17:
+            assert result.data_ptr() == ptr
+
+
+def test_call_on_another_stream_beside_pending_work():
+    """Work pending on the current stream reads memory that was given up; a call on another stream, its tensors made
+    inside, leaves it alone and gives the same bits."""
+    cache = kvq.QuantizedKVCache(E2M1, 2, 2, 64, 16, 32)
+    k, v = [torch.randn((2, 200, 2, 64), device="cuda") for _ in range(2)]
+    kvq.kvq_quantize_append(cache, k, v)
+    q = torch.randn((2, 4, 8, 64), device="cuda").to(torch.bfloat16)
+    want = kvq.kvq_tree_attention(cache, q, 0.125, 200)
+    nbytes = kvq.alloc_tree_workspace(cache, 8, 4, 200).nbytes
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for n in (want.nbytes, nbytes):
+        x = torch.full((n // 2,), 3, dtype=torch.int16, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)           # about 10 ms
+        total = x.sum()
+        del x
+        got = kvq.kvq_tree_attention(cache, q, 0.125, 200, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want)
+        assert int(total) == 3 * (n // 2)
