@@ -110,6 +110,20 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made_on(stream, make, returned: bool = False) -> torch.Tensor:
+    """make(), a tensor allocated here for a call on `stream` (None: the current stream), from that stream's
+    memory: what another stream's pending work still uses is never handed to it.  returned: the caller
+    goes on with it on the current stream."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned:
+        t.record_stream(here)
+    return t
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -213,7 +227,8 @@ def kvq_quantize_append(cache: QuantizedKVCache, k_new: torch.Tensor, v_new: tor
     assert k_new.shape == v_new.shape and k_new.dtype == v_new.dtype and k_new.is_contiguous() and v_new.is_contiguous()
     assert k_new.dim() == 4 and k_new.shape[0] == cache.cfg.num_seqs
     if t_per_seq is not None:
-        t_per_seq = t_per_seq.to(torch.int32).contiguous()
+        given = t_per_seq
+        t_per_seq = _made_on(stream, lambda: given.to(torch.int32).contiguous())
     _check(lib().kvq_quantize_append(ctypes.byref(cache.cfg), ctypes.byref(cache.c), _ptr(k_new), _ptr(v_new),
                                      _DTYPE[k_new.dtype], k_new.shape[1], _ptr(t_per_seq), _stream(stream)),
            "kvq_quantize_append")
@@ -234,7 +249,8 @@ def kvq_project_append(cache: QuantizedKVCache, x: torch.Tensor, w_k: torch.Tens
         assert kv_out.dtype == torch.float32 and kv_out.is_contiguous()
         assert kv_out.shape == (2, cfg.num_seqs, x.shape[1], cfg.num_kv_heads, cfg.head_dim)
     if t_per_seq is not None:
-        t_per_seq = t_per_seq.to(torch.int32).contiguous()
+        given = t_per_seq
+        t_per_seq = _made_on(stream, lambda: given.to(torch.int32).contiguous())
     _check(lib().kvq_project_append(ctypes.byref(cfg), ctypes.byref(cache.c), _ptr(x), hidden, _ptr(w_k), _ptr(w_v),
                                     x.shape[1], _ptr(t_per_seq), _ptr(kv_out), _stream(stream)),
            "kvq_project_append")
@@ -262,9 +278,9 @@ def kvq_decode_attention(cache: QuantizedKVCache, q: torch.Tensor, softmax_scale
     assert q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 3
     Hq = q.shape[1]
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _made_on(stream, lambda: torch.empty(q.shape, dtype=out_dtype, device=q.device), returned=True)
     if workspace is None:
-        workspace = alloc_workspace(cache, Hq, max_seq_len, num_splits)
+        workspace = _made_on(stream, lambda: alloc_workspace(cache, Hq, max_seq_len, num_splits))   # (zeroed on `stream`)
     _check(lib().kvq_decode_attention(ctypes.byref(cache.cfg), ctypes.byref(cache.c), _ptr(q), Hq,
                                       float(softmax_scale), max_seq_len, num_splits, _ptr(out), _DTYPE[out.dtype],
                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -317,7 +333,7 @@ def kvq_decode_attention_noalloc(cache: QuantizedKVCache, q: torch.Tensor, softm
     different streams share that scratch and must be serialised."""
     assert q.dtype == torch.bfloat16 and q.is_contiguous() and q.dim() == 3
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _made_on(stream, lambda: torch.empty(q.shape, dtype=out_dtype, device=q.device), returned=True)
     st = lib().kvq_decode_attention_noalloc(ctypes.byref(cache.cfg), ctypes.byref(cache.c), _ptr(q), q.shape[1],
                                             float(softmax_scale), max_seq_len, num_splits, _ptr(out),
                                             _DTYPE[out.dtype], _stream(stream))
@@ -365,20 +381,6 @@ def _refs(cache: "QuantizedKVCache"):
     if r is None:
         r = cache._c_refs = (ctypes.byref(cache.cfg), ctypes.byref(cache.c), cache.pool.get_device())
     return r
-
-
-def _made_on(stream, make, returned: bool = False) -> torch.Tensor:
-    """make(), a tensor allocated here for a call on `stream` (None: the current stream), from that stream's
-    memory: what another stream's pending work still uses is never handed to it.  returned: the caller
-    goes on with it on the current stream."""
-    if stream is None:
-        return make()
-    here = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        t = make()
-    if returned:
-        t.record_stream(here)
-    return t
 
 
 def kvq_tree_workspace_bytes(cache: QuantizedKVCache, num_q_heads: int, num_nodes: int, max_seq_len: int,
@@ -511,7 +513,8 @@ def kvq_dequantize(cache: QuantizedKVCache, seq: int, kv_head: int, which: int, 
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Values tokens [tok_begin, tok_end) of (seq, kv_head, K=0 / V=1) stand for, fp32 [n, D]."""
     if out is None:
-        out = torch.empty((max(tok_end - tok_begin, 0), cache.head_dim), dtype=torch.float32, device=cache.device)
+        shape = (max(tok_end - tok_begin, 0), cache.head_dim)
+        out = _made_on(stream, lambda: torch.empty(shape, dtype=torch.float32, device=cache.device), returned=True)
     _check(lib().kvq_dequantize(ctypes.byref(cache.cfg), ctypes.byref(cache.c), seq, kv_head, which, tok_begin,
                                 tok_end, _ptr(out), _stream(stream)), "kvq_dequantize")
     return out
