@@ -377,10 +377,7 @@ def _call(what: str, index: int, stream, *args):
 
 def _refs(cache: "QuantizedKVCache"):
     """References to the cache's C structures, and its device."""
-    r = cache.__dict__.get("_c_refs")
-    if r is None:
-        r = cache._c_refs = (ctypes.byref(cache.cfg), ctypes.byref(cache.c), cache.pool.get_device())
-    return r
+    return ctypes.byref(cache.cfg), ctypes.byref(cache.c), cache.pool.get_device()
 
 
 def kvq_tree_workspace_bytes(cache: QuantizedKVCache, num_q_heads: int, num_nodes: int, max_seq_len: int,

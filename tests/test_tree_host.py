@@ -77,3 +77,14 @@ def test_misaligned_pools_are_refused(kvq, field):
         assert L.kvq_decode_attention(c, k, A, 32, z, 100, 2, A, 0, A, 0, None) == kvq.KVQ_ERR_INVALID_ARG
         assert L.kvq_quantize_append(c, k, A, A, 0, 0, None, None) == kvq.KVQ_ERR_INVALID_ARG
         assert L.kvq_project_append(c, k, A, 128, A, A, 0, None, None, None) == kvq.KVQ_ERR_INVALID_ARG
+
+
+def test_a_handle_whose_structures_are_replaced(kvq):
+    """Calls read the handle's present cfg and c, not those of an earlier call."""
+    b, _, _ = buffers(kvq, kvq.KVQ_FMT_FP4_E2M1_S16)
+    cache = kvq.QuantizedKVCache.from_buffers(kvq.KVQ_FMT_FP4_E2M1_S16, 2, 64, **b)
+    assert kvq._refs(cache)[0]._obj is cache.cfg and kvq._refs(cache)[1]._obj is cache.c
+    c = kvq.kvq_cache.from_buffer_copy(cache.c)
+    cfg = kvq.kvq_config.from_buffer_copy(cache.cfg)
+    cache.c, cache.cfg = c, cfg
+    assert kvq._refs(cache)[0]._obj is cfg and kvq._refs(cache)[1]._obj is c
