@@ -367,7 +367,9 @@ kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, 
  * to are taken as they are (V of an FP8 tier page within a relative 2^-11 per
  * element while the page's largest |v| lies in 5e-14..1.6e19, within 2^-73 below,
  * and infinite above).  A bad page-table entry sets KVQ_STATUS_BAD_PAGE
- * and its page (group, for KVQ_FMT_CB2_GROUP4) is left out.  Two launches. */
+ * and its page (group, for KVQ_FMT_CB2_GROUP4) is left out.  A call that sets
+ * KVQ_STATUS_TIMEOUT leaves NaN in out and lse of every row that a wait gave up
+ * on, and in page_lse of the pages concerned.  Two launches. */
 kvq_status kvq_tree_attention(const kvq_config* cfg, const kvq_cache* cache, const void* q, int32_t num_q_heads,
                               int32_t num_nodes, const void* k_tree, const void* v_tree, const uint64_t* tree_mask,
                               int32_t mask_per_seq, const int32_t* nodes_per_seq, float softmax_scale,

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) tree_merge_kernel(const Tree
       for (int i = 0; i < VEC; ++i) st.o[w][i] *= f;
     }
     for (int s0 = 0; s0 < a.S; s0 += 32) {
-      float wt[WR];   // split s0 + lane's weight
+      float wt[WR];   // split s0 + lane's weight (0 without tokens: its sum is 0, or NaN where a wait gave up)
 #pragma unroll
       for (int w = 0; w < WR; ++w) {
         const float2 ml = s0 + lane < a.S && w < nr ? a.part_ml[base + (size_t)(s0 + lane) * a.R + w] : make_float2(-INFINITY, 0.f);

@@ -401,13 +401,14 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
   }
 }
 
-// -inf in page_lse for pages [p_lo, p_hi) of the CTA's rows [r_lo, r_hi).
-__device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, int r_lo, int r_hi, int p_lo, int p_hi) {
+// x in page_lse for pages [p_lo, p_hi) of the CTA's rows [r_lo, r_hi).
+__device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, int r_lo, int r_hi, int p_lo, int p_hi,
+                                              float x = -INFINITY) {
   const int n = p_hi - p_lo;
   if (n <= 0) return;
   for (int r = r_lo + (int)(threadIdx.x >> 5); r < r_hi; r += kThreads / 32) {
     float* row = page_lse_row(a, b, h, r);
-    for (int p = p_lo + (int)(threadIdx.x & 31); p < p_hi; p += 32) row[p] = -INFINITY;
+    for (int p = p_lo + (int)(threadIdx.x & 31); p < p_hi; p += 32) row[p] = x;
   }
 }
 
@@ -1015,7 +1016,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     }
   }
   if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
-  __syncthreads();
+  if (__syncthreads_or(!ok)) {
+    // A wait gave up: NaN stands where the CTA's results would have been, never what an earlier call left there.  (The
+    // merge kernel gives m = -inf the weight 0, and 0 x NaN makes the row's sum, out and lse NaN.)
+    for (int r = tid; r < rows; r += kThreads) a.part_ml[part0 + r] = make_float2(-INFINITY, NAN);
+    if (a.page_lse) fill_page_lse(a, b, h, r0, r0 + rows, p0, p1, NAN);
+  }
   if (warp == 4) {
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
