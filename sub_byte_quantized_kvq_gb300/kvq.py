@@ -451,7 +451,7 @@ def kvq_tree_attention(cache: QuantizedKVCache, q: torch.Tensor, softmax_scale: 
         workspace = _made_on(stream, lambda: alloc_tree_workspace(cache, Hq, T, max_seq_len, num_splits))
     _check_on(index, q, k_tree, v_tree, tree_mask, nodes_per_seq, out, lse, page_lse, workspace)
     _call("kvq_tree_attention", index, stream, pcfg, pcache, q.data_ptr(), Hq, T, _addr(k_tree), _addr(v_tree),
-          _addr(tree_mask), per_seq, _addr(nodes_per_seq), softmax_scale, max_seq_len, num_splits, out.data_ptr(), dt,
+          _addr(tree_mask), per_seq, _addr(nodes_per_seq), float(softmax_scale), max_seq_len, num_splits, out.data_ptr(), dt,
           _addr(lse), _addr(page_lse), workspace.data_ptr(), workspace.nbytes)
     return out
 
@@ -474,7 +474,7 @@ def kvq_page_mass(cache: QuantizedKVCache, lse: torch.Tensor, page_lse: torch.Te
     if node_mask is not None:
         assert node_mask.dtype is torch.int64 and node_mask.is_contiguous() and node_mask.shape == (B,)
     _check_on(index, lse, page_lse, mass, node_mask, mass_out)
-    _call("kvq_page_mass", index, stream, pcfg, Hq, T, P, lse.data_ptr(), page_lse.data_ptr(), _addr(node_mask), decay,
+    _call("kvq_page_mass", index, stream, pcfg, Hq, T, P, lse.data_ptr(), page_lse.data_ptr(), _addr(node_mask), float(decay),
           mass.data_ptr(), mass_out.data_ptr())
     return mass_out
 

@@ -5,6 +5,7 @@ import ctypes
 import os
 import shutil
 
+import numpy as np
 import pytest
 import torch
 
@@ -88,3 +89,19 @@ def test_a_handle_whose_structures_are_replaced(kvq):
     cfg = kvq.kvq_config.from_buffer_copy(cache.cfg)
     cache.c, cache.cfg = c, cfg
     assert kvq._refs(cache)[0]._obj is cfg and kvq._refs(cache)[1]._obj is c
+
+
+@pytest.mark.parametrize("number", [0.5, 1, np.float32(0.5), np.float64(0.5), torch.tensor(0.5)], ids=str)
+def test_scales_of_any_number_type(kvq, monkeypatch, number):
+    """The scale and the decay are taken as decode attention takes its scale: anything that is a number."""
+    b, _, _ = buffers(kvq, kvq.KVQ_FMT_FP4_E2M1_S16)
+    cache = kvq.QuantizedKVCache.from_buffers(kvq.KVQ_FMT_FP4_E2M1_S16, 2, 64, **b)
+    seen = []
+    monkeypatch.setattr(kvq, "_check_on", lambda *a: None)   # (the tensors lie on the host)
+    monkeypatch.setattr(kvq, "_call", lambda what, index, stream, *args: seen.append(args))
+    kvq.kvq_tree_attention(cache, torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16), number, 64)
+    mass = torch.zeros((2, 4))
+    kvq.kvq_page_mass(cache, torch.zeros((2, 1, 4)), torch.zeros((2, 1, 4, 4)), mass, decay=number)
+    for args, types in zip(seen, (kvq.lib().kvq_tree_attention.argtypes, kvq.lib().kvq_page_mass.argtypes)):
+        floats = [a for a, t in zip(args, types) if t is ctypes.c_float]
+        assert len(floats) == 1 and type(floats[0]) is float and floats[0] == float(number)
