@@ -350,7 +350,11 @@ kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, 
  *              nodes_per_seq[b] nodes (clamped to 0..num_nodes); the rows of
  *              the others are written as empty rows.
  *   out        device [num_seqs][num_nodes][num_q_heads][D] in out_dtype (bf16
- *              or f32).  A row that attends to nothing is 0.
+ *              or f32).  A row that attends to nothing is 0.  In either type the
+ *              cached tokens' weights are rounded to fp16 (2^-11 relative), and
+ *              so are values of V that have more bits (INT4, FP8 tier pages):
+ *              an f32 result is good to about 2^-10 of sum_j p_j |v_j|, where
+ *              kvq_decode_attention keeps fp16 pairs.
  *   lse        NULL, or device fp32 [num_seqs][num_nodes][num_q_heads]:
  *              ln sum_j e^a_j, -inf for an empty row.
  *   page_lse   NULL, or device fp32 [num_seqs][num_nodes][num_q_heads][P],
@@ -407,7 +411,10 @@ kvq_status kvq_page_mass(const kvq_config* cfg, int32_t num_q_heads, int32_t num
  *   mass_out[b] = the masses of the pages that stay, at their new places, then 0.
  *   evicted    NULL, or device int32 [num_seqs]: pages evicted.
  * cache->page_table, cache->seq_lens and mass are read; the outputs may be the
- * same arrays (in place) or other ones, but may not overlap in part.  Keys were
+ * same arrays (in place) or other ones, but may not overlap in part.  No page is
+ * counted or copied: where several entries name one physical page (sequences that
+ * share a prefix), an append that runs into an evicted entry overwrites it for all
+ * of them; the caller replaces such entries, the last evicted[b], before.  Keys were
  * rotated (if at all) before they were cached, so kept tokens keep their
  * positions.  Requires keep_pages >= sink_pages + recent_pages >= 0, and at
  * most 28,672 pages per sequence (KVQ_ERR_UNSUPPORTED beyond). */

@@ -284,11 +284,6 @@ static TreeKernel tree_kernel(int fmt, int D, int R) {
   }
 }
 
-// One CTA runs per SM, so the cached pages of the call take
-// waves(S) x (tiles of a split + what a CTA costs besides: barriers, tensor
-// memory, the query, the pipeline's fill and drain, the partial state; measured
-// 4 us or three tiles with 8 rows, 8 us or five and a half with 128) -- the
-// smallest product, and among equals the fewest splits.
 static long long tree_tiles(int max_seq_len) {
   return (max_seq_len + kPage * kTreeTilePages - 1) / (kPage * kTreeTilePages);
 }
@@ -297,6 +292,12 @@ int tree_most_splits(int B, int Hkv, int R, int max_seq_len, int sms) {   // (ne
   const long long units = tree_units(B, Hkv, R);
   return (int)std::min({std::max(tree_tiles(max_seq_len), 1ll), (8ll * sms + units - 1) / units, 256ll});
 }
+// One CTA runs per SM, so the cached pages of the call take
+// waves(S) x (tiles of a split + what a CTA costs besides: barriers, tensor
+// memory, the query, the pipeline's fill and drain, the partial state; measured
+// 4 us or three tiles with 8 rows, 8 us or five and a half with 128; counted as
+// five for any rows and any format, INT4 with its tiles of 64 tokens included) --
+// the smallest product, and among equals the fewest splits.
 int tree_auto_splits(int B, int Hkv, int R, int max_seq_len, int sms) {
   const long long tiles = tree_tiles(max_seq_len), units = tree_units(B, Hkv, R);
   const long long most = tree_most_splits(B, Hkv, R, max_seq_len, sms);
@@ -338,7 +339,8 @@ static cudaError_t tree_launch_d(const TreeArgs& a, cudaStream_t st) {
   void* args[] = {const_cast<TreeArgs*>(&a)};
   e = cudaLaunchKernel(k.fn, dim3(a.S, a.Hkv * ((a.R + kTreeRows - 1) / kTreeRows), a.B), dim3(k.threads), args, k.smem, st);
   if (e != cudaSuccess) return e;
-  // The merge is launched while the last split CTAs run (programmatic dependent launch).  A warp takes four rows,
+  // The merge is launched while the split kernel runs (programmatic dependent launch): that hides its launch, and its work
+  // on the tail and the nodes where an SM has no split CTA (beside one, no merge CTA fits).  A warp takes four rows,
   // which share the loads of the tail's and the nodes' K and V, or one where that would leave most SMs idle (up to
   // two CTAs of 8 one-row warps on each of 152; measured with 8 of them: 4096 rows 46 us a call instead of 42).
   const bool few = (long long)a.B * a.Hkv * a.R <= 152 * 8 * 2;

@@ -27,12 +27,16 @@
 // tier): for a bf16 result both are below its own rounding.  An FP8 page's V may
 // have any magnitude: v_shift moves a power of two of its scale to P.
 //
-// What bounds it: instruction issue.  A tile of 128 tokens is about 1024 cycles
-// of MMA at 128 rows and 800-1200 of this SM's share of the measured HBM rate,
-// but some 6,700 warp instructions (expansion, exponentials, waits) for four
-// schedulers; measured 16 sequences x 32k tokens: FP4 at 128 rows 360 us, tiered
-// at 8 rows 317 us.  Addresses that run along with a warp's tiles, instead of
-// computed per tile, gave 1-2%.
+// What bounds it: no unit alone.  A tile of 128 tokens is about 1024 cycles of MMA
+// at 128 rows, 800-1200 of this SM's share of the measured HBM rate, and 6,600
+// (FP4) to 7,400 (tiered) warp instructions, which take four schedulers 1,650 to
+// 1,850 cycles; measured, it takes about 2,950 (16 sequences x 32k tokens: FP4 at
+// 128 rows 367 us, tiered at 8 rows 330 us), with 55% and 67% of the issue slots
+// used.  So the roles wait for one another over a tile; which for which has not
+// been measured.  Addresses that run along with a warp's tiles, instead of computed
+// per tile, gave 1-2%.  The kernels of more than 32 rows spill up to 32 bytes (124
+// loaded) at the 80 registers a thread that the launch has, those of fewer rows none
+// (INT4 with D = 64: 4).
 #pragma once
 #include <type_traits>
 
