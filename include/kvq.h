@@ -36,8 +36,8 @@
  *     skipped, nothing outside the caller's buffers is touched, and the host
  *     reads the word whenever it chooses.  No call ever traps or spins forever:
  *     every wait in device code (for the asynchronous copies of a page, for a
- *     tensor-memory copy or MMA to complete) gives up after 100 ms and sets
- *     KVQ_STATUS_TIMEOUT.
+ *     tensor-memory copy or MMA to complete) gives up after 100 ms (500 ms for
+ *     the last one of tree attention) and sets KVQ_STATUS_TIMEOUT.
  *   - No C++ exception crosses this interface.
  */
 #ifndef KVQ_H_
@@ -373,7 +373,8 @@ kvq_status kvq_tree_workspace_bytes(const kvq_config* cfg, int32_t num_q_heads, 
  * and infinite above).  A bad page-table entry sets KVQ_STATUS_BAD_PAGE
  * and its page (group, for KVQ_FMT_CB2_GROUP4) is left out.  A call that sets
  * KVQ_STATUS_TIMEOUT leaves NaN in out and lse of every row that a wait gave up
- * on, and in page_lse of the pages concerned.  Two launches. */
+ * on, and its page_lse unwritten in part (kvq_page_mass of such a row is NaN).
+ * Two launches. */
 kvq_status kvq_tree_attention(const kvq_config* cfg, const kvq_cache* cache, const void* q, int32_t num_q_heads,
                               int32_t num_nodes, const void* k_tree, const void* v_tree, const uint64_t* tree_mask,
                               int32_t mask_per_seq, const int32_t* nodes_per_seq, float softmax_scale,

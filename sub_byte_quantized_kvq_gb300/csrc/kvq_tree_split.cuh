@@ -29,12 +29,12 @@
 //
 // What bounds it: no unit alone.  A tile of 128 tokens is about 1024 cycles of MMA
 // at 128 rows, 800-1200 of this SM's share of the measured HBM rate, and 6,600
-// (FP4) to 7,400 (tiered) warp instructions, which take four schedulers 1,650 to
-// 1,850 cycles; measured, it takes about 2,950 (16 sequences x 32k tokens: FP4 at
-// 128 rows 367 us, tiered at 8 rows 330 us), with 55% and 67% of the issue slots
-// used.  So the roles wait for one another over a tile; which for which has not
+// (FP4) to 7,200 (tiered) warp instructions, which take four schedulers 1,650 to
+// 1,800 cycles; measured, it takes about 2,950 (FP4 at 128 rows) and 2,700 (tiered
+// at 8 rows) with a CTA's start and end spread over 64 tiles, and 56% and 66% of the
+// issue slots are used (16 sequences x 32k tokens: 360 and 327 us).  So the roles wait for one another over a tile; which for which has not
 // been measured.  Addresses that run along with a warp's tiles, instead of computed
-// per tile, gave 1-2%.  The kernels of more than 32 rows spill up to 32 bytes (124
+// per tile, gave 1-2%.  The kernels of more than 32 rows spill up to 32 bytes (120
 // loaded) at the 80 registers a thread that the launch has, those of fewer rows none
 // (INT4 with D = 64: 4).
 #pragma once
@@ -70,7 +70,7 @@ struct Plan {
   static constexpr int kSlot = F::kGroup ? 12 * D + kOutPrefetch : half_slot_bytes<FMT, D>();
   static constexpr bool kShift = FMT == KVQ_FMT_TIERED;      // pages have a V shift
   static constexpr int misc(int depth) {
-    return 8 * 13 + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8 +
+    return 8 * 14 + 2 * kMeta * kPages * 4 + 4 * kDequantWarps * depth + 8 +
            (kShift ? kMeta * kPages * 8 + 4 * kDequantWarps * depth : 0);
   }
   static constexpr int smem(int depth) {   // 1024: alignment slack
@@ -87,11 +87,11 @@ struct Plan {
 };
 
 // A bounded mbarrier wait on the SM's own clock: gives up after 2e8 cycles, 100 ms.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long limit = 200000000ll) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait_sleep(bar, parity, 20000u))
-    if (clock64() - t0 > 200000000ll) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
 }
 
@@ -405,14 +405,13 @@ __device__ __forceinline__ void dequant_block(uint32_t blk, GBlk&& gblk, bool ti
   }
 }
 
-// x in page_lse for pages [p_lo, p_hi) of the CTA's rows [r_lo, r_hi).
-__device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, int r_lo, int r_hi, int p_lo, int p_hi,
-                                              float x = -INFINITY) {
+// -inf in page_lse for pages [p_lo, p_hi) of the CTA's rows [r_lo, r_hi).
+__device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, int r_lo, int r_hi, int p_lo, int p_hi) {
   const int n = p_hi - p_lo;
   if (n <= 0) return;
   for (int r = r_lo + (int)(threadIdx.x >> 5); r < r_hi; r += kThreads / 32) {
     float* row = page_lse_row(a, b, h, r);
-    for (int p = p_lo + (int)(threadIdx.x & 31); p < p_hi; p += 32) row[p] = x;
+    for (int p = p_lo + (int)(threadIdx.x & 31); p < p_hi; p += 32) row[p] = -INFINITY;
   }
 }
 
@@ -714,8 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
   uint8_t* slots = smem + 2 * P::kBuf;                                    // [kDequantWarps][DEPTH]
   float2* vshift = reinterpret_cast<float2*>(slots + kDequantWarps * DEPTH * SLOT);   // [kMeta][PAGES] b, 2^-b of an FP8 page's V (tiered only)
   uint64_t *k_full = reinterpret_cast<uint64_t*>(vshift + (P::kShift ? kMeta * PAGES : 0)), *k_empty = k_full + 2, *v_full = k_empty + 2,
-           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2;
-  int32_t* ntok = reinterpret_cast<int32_t*>(done + 1);                   // [kMeta][PAGES] tokens of a tile's pages
+           *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2, *done = p_full + 2, *drained = done + 1;
+  int32_t* ntok = reinterpret_cast<int32_t*>(drained + 1);                // [kMeta][PAGES] tokens of a tile's pages
   float* kscale = reinterpret_cast<float*>(ntok + kMeta * PAGES);         // [kMeta][PAGES] FP8 pages' K scale, else 1
   int32_t* entries = reinterpret_cast<int32_t*>(kscale + kMeta * PAGES);  // [kDequantWarps][DEPTH] page-table entries of the slots
   float* vscales = reinterpret_cast<float*>(entries + kDequantWarps * DEPTH);   // [kDequantWarps][DEPTH] V scales of a K warp's FP8 pages (tiered only)
@@ -732,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
       mbar_init(&p_full[i], n_sm);
     }
     mbar_init(done, 1);
+    mbar_init(drained, 1);
     fence_mbar_init();
   }
   // Each role starts its first global loads before the barrier that publishes the mbarriers and the tensor memory.
@@ -819,7 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[i & 1]);
       }
-      ok = ok && __all_sync(0xffffffffu, wait_bar(done, 0));
+      // Where any role's wait gave up, the MMA warp's did too (it waits for all of them) and `done` never comes: no softmax
+      // warp stores, and the rows keep the NaN of the start.  The limit is above the four waits that the MMA warp may have left.
+      ok = ok && __all_sync(0xffffffffu, wait_bar(done, 0, 1000000000ll));
       // ---- the partial state, through shared memory (the tiles are done): copies of a row are joined, rows stored whole
       constexpr int XS = D + 4;
       float* xo = reinterpret_cast<float*>(smem);                       // [128][XS], thread's row of O
@@ -978,6 +980,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    // Until the partial states are stored they are NaN, so that nothing that an earlier call left in the workspace is taken
+    // for them.  (The merge kernel gives m = -inf the weight 0, and 0 x NaN makes the row's sum, out and lse NaN.)
+    if (warp > 4 + kDequantWarps)
+      for (int r = tid - 32 * (5 + kDequantWarps); r < rows; r += 96) a.part_ml[part0 + r] = make_float2(-INFINITY, NAN);
     join();
     if (warp == 4 + kDequantWarps) {
       asm volatile("bar.sync 3, %0;" ::"r"(32 * n_sm + 32) : "memory");   // the query rows
@@ -1015,17 +1021,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_cache_kernel(const TreeArgs 
           tc::mma_ta(t_o, tmem + (i & 1) * 128 + 8 * k, vt + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4), id_o, (i | k) != 0);
         tc::commit(&v_empty[i & 1]);
       }
-      tc::commit(done);
-      if (!ok) wait_bar(done, 0);   // tensor memory may be freed once what was issued is done
+      tc::commit(ok ? done : drained);
+      if (!ok) wait_bar(drained, 0);   // tensor memory may be freed once what was issued is done
     }
   }
   if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
-  if (__syncthreads_or(!ok)) {
-    // A wait gave up: NaN stands where the CTA's results would have been, never what an earlier call left there.  (The
-    // merge kernel gives m = -inf the weight 0, and 0 x NaN makes the row's sum, out and lse NaN.)
-    for (int r = tid; r < rows; r += kThreads) a.part_ml[part0 + r] = make_float2(-INFINITY, NAN);
-    if (a.page_lse) fill_page_lse(a, b, h, r0, r0 + rows, p0, p1, NAN);
-  }
+  __syncthreads();
   if (warp == 4) {
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
