@@ -32,11 +32,11 @@
 // (FP4) to 7,200 (tiered) warp instructions, which take four schedulers 1,650 to
 // 1,800 cycles; measured, it takes about 2,950 (FP4 at 128 rows) and 2,700 (tiered
 // at 8 rows) with a CTA's start and end spread over 64 tiles, and 56% and 66% of the
-// issue slots are used (16 sequences x 32k tokens: 360 and 327 us).  So the roles wait for one another over a tile; which for which has not
-// been measured.  Addresses that run along with a warp's tiles, instead of computed
-// per tile, gave 1-2%.  The kernels of more than 32 rows spill up to 32 bytes (120
-// loaded) at the 80 registers a thread that the launch has, those of fewer rows none
-// (INT4 with D = 64: 4).
+// issue slots are used (16 sequences x 32k tokens: 360 and 327 us).  So the roles
+// wait for one another over a tile; which for which has not been measured.
+// Addresses that run along with a warp's tiles, instead of computed per tile, gave
+// 1-2%.  The kernels of more than 32 rows spill up to 32 bytes (120 loaded) at the 80
+// registers a thread that the launch has, those of fewer rows none.
 #pragma once
 #include <type_traits>
 
@@ -524,7 +524,10 @@ struct SoftmaxRow {
         if (__builtin_expect(again || !__any_sync(0xffffffffu, need), 1)) break;
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NP; ++j) mx = fmaxf(mx, kShift ? fmaf(page_max(x + kPage * j), fk[j], shift(vs, pg + j)) : page_max(x + kPage * j) * fk[j]);
+        for (int j = 0; j < NP; ++j) {
+          const float top = page_max(x + kPage * j);
+          mx = fmaxf(mx, kShift ? fmaf(top, fk[j], shift(vs, pg + j)) : top * fk[j]);
+        }
         const bool up = need && mx > m;
         const float alpha = up ? ex2(m - mx) : 1.f;
         l *= alpha;
