@@ -244,7 +244,7 @@ def _prompt_own(s):
     c = s["case"]
     cache = _handle(s, kvq)
     if c["packed"]:
-        kvq.kvq_prompt_attention(cache, s["q"], s["k"], s["v"], s["scale"], t_per_seq=s["n"], first=s["first"], t_new=c["N"],
+        kvq.kvq_prompt_attention(cache, s["q"], s["k"], s["v"], s["scale"], t_per_seq=s["n"], first_row=s["first"], t_new=c["N"],
                                  causal=c["causal"], out=s["out"], lse=s["lse"])
     else:
         q, k, v, out, lse = [s[x].unflatten(0, (c["B"], c["N"])) for x in ("q", "k", "v", "out", "lse")]
