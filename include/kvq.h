@@ -128,6 +128,7 @@ typedef enum { KVQ_DECODE_AUTO = 0, KVQ_DECODE_TENSOR_CORES = 1, KVQ_DECODE_CUDA
 #define KVQ_STATUS_CAPACITY     0x2u  /* append past pages_per_seq_max pages: sequence skipped */
 #define KVQ_STATUS_SEQ_TOO_LONG 0x4u  /* decode: seq_lens[b] > max_seq_len: tokens beyond ignored */
 #define KVQ_STATUS_TIMEOUT      0x8u  /* a bounded device wait gave up */
+#define KVQ_STATUS_BAD_ROWS     0x10u /* prompt attention: a sequence's rows do not fit the call: skipped */
 
 typedef struct {
     int32_t num_seqs;           /* B: sequences (rows of the page table) */
@@ -422,6 +423,76 @@ kvq_status kvq_page_mass(const kvq_config* cfg, int32_t num_q_heads, int32_t num
 kvq_status kvq_evict_pages(const kvq_config* cfg, const kvq_cache* cache, const float* mass, int32_t keep_pages,
                            int32_t sink_pages, int32_t recent_pages, int32_t* page_table_out, int32_t* seq_lens_out,
                            float* mass_out, int32_t* evicted, void* stream);
+
+/* ---- Before the cache: what a layer's projection wrote is normalised and
+ * rotated (at prompt time and for each decoded token: the cache holds rotated
+ * keys, and decode and tree attention take rotated queries), and a prompt
+ * attends to itself while its K and V are appended.  The pages leave both to the
+ * model; these two calls are this library's own.
+ *
+ * Their rows are tokens, `stride` elements apart, each of heads x D contiguous
+ * values: [num_seqs][t_new][heads][D] as append takes it, packed sequences, or
+ * the q, k and v parts of one projection's rows.  Pointers are 16-byte aligned,
+ * strides multiples of 16 bytes. */
+
+/* Per-head RMS norm of queries and keys and their rotary positions, in one pass:
+ * for each row r, head and channel c of a role's x (role: q with num_q_heads
+ * heads, k with cfg->num_kv_heads), w its gains,
+ *   n_c = x_c w_c / sqrt(1/D sum x^2 + eps)                  (eps < 0: n = x)
+ *   y_a = n_a cos(phi) - n_b sin(phi),  y_b = n_b cos(phi) + n_a sin(phi)
+ * for the pairs i < rot_dim / 2 of the first rot_dim channels, (a, b) =
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved = 1, and
+ *   phi = positions[pair_axis[i]][r] * inv_freq[i]
+ * (the product is not rounded to binary32: within 2^-22 of a turn at any int32
+ * position for |inv_freq| < 2 pi); the channels from rot_dim on are n.
+ *   q, k        device, in_dtype (bf16, f16, f32); either may be NULL (its gains
+ *               and output are then not read).  The squares of a row must add up
+ *               within binary32.
+ *   num_rows    rows of q and of k (>= 0).
+ *   q_weight, k_weight  device fp32 [D], or NULL: ones.  NULL both when eps < 0.
+ *   positions   device int32 [num_axes][num_rows]; num_axes 1 for text, e.g. 3 for
+ *               time, height and width.  For a decode step of tokens about to be
+ *               appended, cache->seq_lens (unless pages were evicted).
+ *   inv_freq    device fp32 [rot_dim / 2], finite.
+ *   rot_dim     a multiple of 16, 0..D (0: positions and inv_freq are not read).
+ *   pair_axis   host uint8 [rot_dim / 2], each below num_axes, or NULL: axis 0.
+ *   q_out, k_out  device, out_dtype.  May be q and k themselves (same type, same
+ *               stride), else may not overlap the inputs or each other.
+ * One launch. */
+kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride, int32_t num_q_heads, const void* k,
+                         int64_t k_stride, kvq_dtype in_dtype, int32_t num_rows, const float* q_weight,
+                         const float* k_weight, float eps, const int32_t* positions, int32_t num_axes,
+                         const float* inv_freq, int32_t rot_dim, const uint8_t* pair_axis, int32_t interleaved,
+                         void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, kvq_dtype out_dtype,
+                         void* stream);
+
+/* Attention of whole prompts, each sequence over its own tokens:
+ *   a_ij = softmax_scale * q_i . k_j for j <= i (causal = 1) or for every token j
+ *   of the sequence (causal = 0),   out_i = sum_j e^a_ij v_j / sum_j e^a_ij
+ * with grouped heads as kvq_decode_attention (at most 16 query heads a kv head).
+ *   q, k, v     device, dtype (bf16 or f16), num_rows rows each of num_q_heads, Hkv
+ *               and Hkv heads.
+ *   first_row   device int32 [num_seqs] or NULL: sequence b's tokens are rows
+ *               first_row[b], first_row[b] + 1, ...; NULL = b * t_new (a padded
+ *               batch, as append's).  Sequences may not share rows.
+ *   t_per_seq   device int32 [num_seqs] or NULL: sequence b has t_per_seq[b] tokens
+ *               (none if <= 0); NULL = t_new each.
+ *   t_new       host bound on the lengths (sizes the grid).  A sequence that is
+ *               longer, or whose rows are not all in 0..num_rows - 1, is skipped and
+ *               sets KVQ_STATUS_BAD_ROWS.
+ *   out         device, rows of num_q_heads heads, in out_dtype (dtype or f32).
+ *   lse         NULL, or device fp32 [num_rows][num_q_heads]: ln sum_j e^a_ij.
+ *   status      device word, OR-ed with KVQ_STATUS_* bits (a cache's status).
+ * Rows of out and lse that belong to no sequence are not written; rows of q, k and
+ * v that a token does not attend to (later tokens, other sequences, rows of none)
+ * never reach it, whatever they hold.  Weights are rounded to the inputs' type
+ * (2^-9 relative for bf16, 2^-11 for f16), the sums are fp32.  A token whose
+ * scores are all -inf gets 0 and lse -inf.  One launch. */
+kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, kvq_dtype dtype, int32_t num_q_heads, int32_t num_rows,
+                                const int32_t* first_row, const int32_t* t_per_seq, int32_t t_new, float softmax_scale,
+                                int32_t causal, void* out, int64_t out_stride, kvq_dtype out_dtype, float* lse,
+                                uint32_t* status, void* stream);
 
 /* The static channel mask of KVQ_FMT_CB2_STATIC ([P4] "Key Production
  * Engineering Takeaways" item 2: the top 1% channels by absolute magnitude stay

@@ -5,6 +5,7 @@
 
 #include "kvq_block.cuh"
 #include "kvq_project.cuh"
+#include "kvq_prompt.cuh"
 #include "kvq_tree.cuh"
 
 namespace kvq {
@@ -572,6 +573,100 @@ kvq_status kvq_evict_pages(const kvq_config* cfg, const kvq_cache* cache, const 
   a.sink = sink_pages / a.unit;
   a.recent = recent_pages / a.unit;
   return cuda_status(evict_launch(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ----------------------------------------------------------------------------- before the cache
+static int dtype_bytes(int t) { return t == KVQ_BF16 || t == KVQ_F16 ? 2 : t == KVQ_F32 ? 4 : 0; }
+// Rows of `width` elements of `es` bytes, `stride` elements apart: 16-byte aligned, and (written ones) apart from one another.
+static bool rows_ok(const void* p, int64_t stride, int es, int64_t width, bool written) {
+  if (!p || !aligned16(p) || stride < (written ? width : 0) || stride > (1ll << 37)) return false;
+  return stride * es % 16 == 0;
+}
+
+kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride, int32_t num_q_heads, const void* k,
+                         int64_t k_stride, kvq_dtype in_dtype, int32_t num_rows, const float* q_weight,
+                         const float* k_weight, float eps, const int32_t* positions, int32_t num_axes,
+                         const float* inv_freq, int32_t rot_dim, const uint8_t* pair_axis, int32_t interleaved, void* q_out,
+                         int64_t q_out_stride, void* k_out, int64_t k_out_stride, kvq_dtype out_dtype, void* stream) {
+  const int ei = dtype_bytes(in_dtype), eo = dtype_bytes(out_dtype);
+  if (!cfg_ok(cfg) || (!q && !k) || !ei || !eo || num_rows < 0 || (interleaved != 0 && interleaved != 1)) return KVQ_ERR_INVALID_ARG;
+  if (q && (num_q_heads <= 0 || num_q_heads % cfg->num_kv_heads)) return KVQ_ERR_INVALID_ARG;
+  if (std::isnan(eps) || std::isinf(eps) || (eps < 0.f && (q_weight || k_weight))) return KVQ_ERR_INVALID_ARG;
+  if (!dim_supported(cfg)) return KVQ_ERR_UNSUPPORTED;
+  const int D = cfg->head_dim;
+  if (rot_dim < 0 || rot_dim > D || rot_dim % 16 || num_axes < 1 || num_axes > 255) return KVQ_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !inv_freq)) return KVQ_ERR_INVALID_ARG;
+  NormRopeArgs a = {};
+  for (int i = 0; pair_axis && i < rot_dim / 2; ++i) {
+    if (pair_axis[i] >= num_axes) return KVQ_ERR_INVALID_ARG;
+    a.pair_axis[i] = pair_axis[i];
+  }
+  const void* in[2] = {q, k};
+  void* out[2] = {q_out, k_out};
+  const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
+  const float* w[2] = {q_weight, k_weight};
+  for (int r = 0; r < 2; ++r) {
+    if (!in[r]) continue;
+    const int heads = r ? cfg->num_kv_heads : num_q_heads;
+    if (!rows_ok(in[r], is[r], ei, (int64_t)heads * D, false) || !rows_ok(out[r], os[r], eo, (int64_t)heads * D, true))
+      return KVQ_ERR_INVALID_ARG;
+    if (in[r] == out[r] && (in_dtype != out_dtype || is[r] != os[r])) return KVQ_ERR_INVALID_ARG;
+    a.in[r] = in[r];
+    a.out[r] = out[r];
+    a.in_stride[r] = is[r];
+    a.out_stride[r] = os[r];
+    a.heads[r] = heads;
+    a.weight[r] = w[r];
+  }
+  if (num_rows == 0) return KVQ_OK;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.rows = num_rows;
+  a.axes = num_axes;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.eps = eps;
+  return cuda_status(norm_rope_launch(a, D, in_dtype, out_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const void* v, int64_t v_stride, kvq_dtype dtype, int32_t num_q_heads, int32_t num_rows,
+                                const int32_t* first_row, const int32_t* t_per_seq, int32_t t_new, float softmax_scale,
+                                int32_t causal, void* out, int64_t out_stride, kvq_dtype out_dtype, float* lse,
+                                uint32_t* status, void* stream) {
+  if (!cfg_ok(cfg) || !status || num_q_heads <= 0 || num_q_heads % cfg->num_kv_heads || num_rows < 0 || t_new < 0 ||
+      (causal != 0 && causal != 1) || !std::isfinite(softmax_scale))
+    return KVQ_ERR_INVALID_ARG;
+  if ((dtype != KVQ_BF16 && dtype != KVQ_F16) || (out_dtype != dtype && out_dtype != KVQ_F32)) return KVQ_ERR_INVALID_ARG;
+  const int G = num_q_heads / cfg->num_kv_heads;
+  if (!dim_supported(cfg) || G > 16) return KVQ_ERR_UNSUPPORTED;
+  const int64_t wq = (int64_t)num_q_heads * cfg->head_dim, wk = (int64_t)cfg->num_kv_heads * cfg->head_dim;
+  if (!rows_ok(q, q_stride, 2, wq, false) || !rows_ok(k, k_stride, 2, wk, false) || !rows_ok(v, v_stride, 2, wk, false) ||
+      !rows_ok(out, out_stride, dtype_bytes(out_dtype), wq, true))
+    return KVQ_ERR_INVALID_ARG;
+  if (t_new == 0 || num_rows == 0) return KVQ_OK;
+  PromptArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.first = first_row;
+  a.lens = t_per_seq;
+  a.status = status;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out_stride = out_stride;
+  a.B = cfg->num_seqs;
+  a.Hkv = cfg->num_kv_heads;
+  a.Hq = num_q_heads;
+  a.G = G;
+  a.rows = num_rows;
+  a.t_new = t_new;
+  a.causal = causal;
+  a.scale = softmax_scale;
+  return cuda_status(prompt_launch(a, cfg->head_dim, dtype, out_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t kvq_last_cuda_error(void) { return g_last_cuda_error; }

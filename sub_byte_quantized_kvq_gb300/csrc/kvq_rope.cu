@@ -1,0 +1,250 @@
+// kvq_rope.cu -- per-head RMS norms of queries and keys and their rotary
+// positions, in one pass over the rows.
+//
+//   n_c = x_c w_c / sqrt(1/D sum x^2 + eps)
+//   pair (a, b) of the first R channels, phi = position[axis] * inv_freq:
+//   y_a = n_a cos phi - n_b sin phi,  y_b = n_b cos phi + n_a sin phi
+//
+// Angles: a product in binary32 would be off by 2^-24 phi radians, 0.008 at 128k
+// tokens.  Only phi modulo a turn counts, so a pair's frequency is turned once
+// into a 64-bit fixed-point fraction of a turn per position (in binary64, off by
+// at most 2^-55), and position x fraction modulo 2^64 is one integer product:
+// the phase is good to 2^-24 of a turn at position 2^31 and 2^-40 at 32k.  Its
+// top bits give the quadrant, the rest an angle within an eighth of a turn.
+//
+// What bounds it: memory.  Each value is read once and written once, 16 bytes a
+// lane; D / 16 lanes hold a head (chunks of 8 channels l and l + R / 16, so a
+// pair's two channels are in one lane in either order of pairs), so a warp does
+// 32 / (D / 16) heads a step and shares the sines and cosines of its row, each
+// computed by one lane.
+#include <algorithm>
+
+#include "kvq_prompt.cuh"
+
+namespace kvq {
+
+constexpr int kRopeWarps = 8;
+
+template <int DT>
+struct Elem;
+template <>
+struct Elem<KVQ_F32> { static constexpr int kWords = 8; };    // 32-bit words of 8 values
+template <>
+struct Elem<KVQ_F16> { static constexpr int kWords = 4; };
+template <>
+struct Elem<KVQ_BF16> { static constexpr int kWords = 4; };
+
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint32_t (&u)[Elem<DT>::kWords], float* x) {
+#pragma unroll
+  for (int i = 0; i < Elem<DT>::kWords; ++i) {
+    if (DT == KVQ_F32) {
+      x[i] = __uint_as_float(u[i]);
+    } else if (DT == KVQ_BF16) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(u32_as_h2(u[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+template <int DT>
+__device__ __forceinline__ void pack8(const float* x, uint32_t (&u)[Elem<DT>::kWords]) {
+#pragma unroll
+  for (int i = 0; i < Elem<DT>::kWords; ++i) {
+    if (DT == KVQ_F32) {
+      u[i] = __float_as_uint(x[i]);
+    } else if (DT == KVQ_BF16) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&p);
+    } else {
+      u[i] = h2_as_u32(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&u)[N], const uint8_t* p) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(u + i) = *reinterpret_cast<const uint4*>(p + 4 * i);
+}
+template <int N>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(p + 4 * i) = *reinterpret_cast<const uint4*>(u + i);
+}
+
+// A frequency as a fraction of a turn per position, modulo 2^64.
+__device__ __forceinline__ uint64_t turn_per_position(float inv_freq) {
+  const double t = (double)inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
+  return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+}
+// sin and cos of position * frequency.
+__device__ __forceinline__ void turn_sincos(int pos, uint64_t per, float& s, float& c) {
+  const int32_t turn = (int32_t)(((uint64_t)(int64_t)pos * per + 0x80000000ull) >> 32);   // in 2^-32 turns
+  const int32_t quad = (int32_t)((uint32_t)turn + 0x20000000u) >> 30;                     // the nearest quarter
+  const float rest = (float)(int32_t)((uint32_t)turn - ((uint32_t)quad << 30)) * 0x1p-31f;   // within +-1/4, in half turns
+  float a, b;
+  sincospif(rest, &a, &b);
+  const bool odd = quad & 1;
+  s = odd ? b : a;
+  c = odd ? a : b;
+  if (quad & 2) s = -s;
+  if ((quad + 1) & 2) c = -c;
+}
+
+// Item (row, g) is 32 / (D / 16) heads of one row: q's groups first, then k's.  A warp takes every S-th group of
+// its rows; the next item's loads are in flight while one is computed.
+template <int D, int IN, int OUT>
+__global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int S) {
+  constexpr int LPH = D / 16, HPW = 32 / LPH, PER = 8 / HPW;   // lanes a head, heads a step, pairs whose phase a lane computes
+  constexpr int EI = IN == KVQ_F32 ? 4 : 2, EO = OUT == KVQ_F32 ? 4 : 2;
+  __shared__ __align__(16) float gain[2][D];
+  const int lane = threadIdx.x & 31, l = lane % LPH, hg = lane / LPH;
+  const bool norm = a.eps >= 0.f;
+  if (norm)
+    for (int i = threadIdx.x; i < 2 * D; i += 32 * kRopeWarps) gain[i / D][i % D] = a.weight[i / D] ? a.weight[i / D][i % D] : 1.f;
+  const int rc = a.rot / 16;                                   // chunks that hold a half of the rotated channels
+  const bool turned = l < rc;
+  const int c0 = turned ? l : 2 * rc + 2 * (l - rc), c1 = turned ? l + rc : c0 + 1;   // the lane's chunks of 8 channels
+  // pair j = 0..7 of the lane: its index, and in registers x[j], y[j]: halves (c0, c1), or neighbours
+  auto pair_of = [&](int j) { return a.interleaved ? 4 * (j < 4 ? c0 : c1) + (j & 3) : 8 * c0 + j; };
+  uint64_t per[PER];
+  const int32_t* where[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int p = turned ? pair_of(hg * PER + i) : 0;
+    per[i] = turned ? turn_per_position(a.inv_freq[p]) : 0ull;
+    where[i] = turned ? a.positions + (size_t)a.pair_axis[p] * a.rows : nullptr;
+  }
+  __syncthreads();
+  const int gq = (a.heads[0] + HPW - 1) / HPW, groups = gq + (a.heads[1] + HPW - 1) / HPW;
+  const long long warps = (long long)gridDim.x * kRopeWarps, w = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int g0 = (int)(w % S);
+  uint32_t u0[Elem<IN>::kWords], u1[Elem<IN>::kWords];
+  int h = 0, role = 0;
+  auto place = [&](int g, int& r, int& head) {
+    r = g >= gq;
+    head = (g - (r ? gq : 0)) * HPW + hg;
+    return head < a.heads[r];
+  };
+  auto fetch = [&](long long row, int g) {
+    if (place(g, role, h)) {
+      const uint8_t* p = static_cast<const uint8_t*>(a.in[role]) + (row * a.in_stride[role] + (long long)h * D) * EI;
+      load_words(u0, p + 8 * EI * c0);
+      load_words(u1, p + 8 * EI * c1);
+    }
+  };
+  long long row = w / S;
+  const long long step = warps / S;
+  if (g0 >= groups || row >= a.rows || w >= step * S) return;
+  fetch(row, g0);
+  for (; row < a.rows; row += step) {
+    float cs[8], sn[8];
+    {
+      float s[PER], c[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        s[i] = 0.f;
+        c[i] = 1.f;
+        if (turned) turn_sincos(where[i][row], per[i], s[i], c[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sn[j] = __shfl_sync(0xffffffffu, s[j % PER], j / PER * LPH + l);
+        cs[j] = __shfl_sync(0xffffffffu, c[j % PER], j / PER * LPH + l);
+      }
+    }
+    for (int g = g0; g < groups; g += S) {
+      float x[8], y[8];
+      unpack8<IN>(u0, x);
+      unpack8<IN>(u1, y);
+      int r, head;
+      const bool live = place(g, r, head);
+      if (g + S < groups) fetch(row, g + S);
+      else if (row + step < a.rows) fetch(row + step, g0);
+      if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], fmaf(y[j], y[j], ss));
+#pragma unroll
+        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float m = fmaf(ss, 1.f / D, a.eps);
+        float f = rsqrtf(m);
+        if (m > 0.f && m < INFINITY) f = fmaf(0.5f * f, fmaf(-m * f, f, 1.f), f);   // one Newton step: rsqrtf alone is good to 2^-22.9
+        float wx[8], wy[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          *reinterpret_cast<float4*>(wx + j) = *reinterpret_cast<const float4*>(&gain[r][8 * c0 + j]);
+          *reinterpret_cast<float4*>(wy + j) = *reinterpret_cast<const float4*>(&gain[r][8 * c1 + j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = x[j] * f * wx[j];
+          y[j] = y[j] * f * wy[j];
+        }
+      }
+      if (turned) {
+        if (a.interleaved) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float& p = j < 4 ? x[2 * j & 7] : y[2 * j & 7];
+            float& q = j < 4 ? x[(2 * j + 1) & 7] : y[(2 * j + 1) & 7];
+            const float t = fmaf(p, cs[j], -q * sn[j]);
+            q = fmaf(q, cs[j], p * sn[j]);
+            p = t;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t = fmaf(x[j], cs[j], -y[j] * sn[j]);
+            y[j] = fmaf(y[j], cs[j], x[j] * sn[j]);
+            x[j] = t;
+          }
+        }
+      }
+      if (live) {
+        uint32_t o[Elem<OUT>::kWords];
+        uint8_t* p = static_cast<uint8_t*>(a.out[r]) + (row * a.out_stride[r] + (long long)head * D) * EO;
+        pack8<OUT>(x, o);
+        store_words(p + 8 * EO * c0, o);
+        pack8<OUT>(y, o);
+        store_words(p + 8 * EO * c1, o);
+      }
+    }
+  }
+}
+
+template <int D, int IN, int OUT>
+static cudaError_t launch(const NormRopeArgs& a, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  constexpr int HPW = 32 / (D / 16);
+  const int groups = (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW;
+  // a row to a warp where there are rows enough for every SM's resident warps, else a row's heads over several
+  const long long slots = (long long)sms * 4 * kRopeWarps;
+  const int S = (int)std::min<long long>(groups, std::max<long long>(1, slots / a.rows));
+  const long long ctas = std::min<long long>(((long long)a.rows * S + kRopeWarps - 1) / kRopeWarps, slots / kRopeWarps);
+  norm_rope_kernel<D, IN, OUT><<<(unsigned)ctas, 32 * kRopeWarps, 0, st>>>(a, S);
+  return cudaGetLastError();
+}
+template <int D, int IN>
+static cudaError_t launch_out(const NormRopeArgs& a, int out_dtype, cudaStream_t st) {
+  return out_dtype == KVQ_BF16 ? launch<D, IN, KVQ_BF16>(a, st)
+       : out_dtype == KVQ_F16  ? launch<D, IN, KVQ_F16>(a, st)
+                               : launch<D, IN, KVQ_F32>(a, st);
+}
+template <int D>
+static cudaError_t launch_in(const NormRopeArgs& a, int in_dtype, int out_dtype, cudaStream_t st) {
+  return in_dtype == KVQ_BF16 ? launch_out<D, KVQ_BF16>(a, out_dtype, st)
+       : in_dtype == KVQ_F16  ? launch_out<D, KVQ_F16>(a, out_dtype, st)
+                              : launch_out<D, KVQ_F32>(a, out_dtype, st);
+}
+cudaError_t norm_rope_launch(const NormRopeArgs& a, int D, int in_dtype, int out_dtype, cudaStream_t st) {
+  return D == 64 ? launch_in<64>(a, in_dtype, out_dtype, st) : launch_in<128>(a, in_dtype, out_dtype, st);
+}
+
+}  // namespace kvq

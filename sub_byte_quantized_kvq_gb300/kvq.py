@@ -21,6 +21,7 @@ KVQ_BF16, KVQ_F16, KVQ_F32 = 0, 1, 2
 KVQ_DECODE_AUTO, KVQ_DECODE_TENSOR_CORES, KVQ_DECODE_CUDA_CORES = 0, 1, 2
 KVQ_TIER_BIT = 1 << 31
 KVQ_STATUS_BAD_PAGE, KVQ_STATUS_CAPACITY, KVQ_STATUS_SEQ_TOO_LONG, KVQ_STATUS_TIMEOUT = 1, 2, 4, 8
+KVQ_STATUS_BAD_ROWS = 16
 KVQ_OK, KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_WORKSPACE, KVQ_ERR_CAPACITY, KVQ_ERR_CUDA = range(6)
 
 _DTYPE = {torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16, torch.float32: KVQ_F32}
@@ -55,7 +56,8 @@ EXPORTS = ("kvq_block_bytes", "kvq_cache_bytes", "kvq_quantize_append", "kvq_pro
            "kvq_decode_workspace_bytes",
            "kvq_decode_num_splits", "kvq_decode_split", "kvq_decode_combine", "kvq_decode_attention",
            "kvq_decode_attention_noalloc", "kvq_tree_workspace_bytes", "kvq_tree_attention", "kvq_page_mass",
-           "kvq_evict_pages", "kvq_select_static_channels", "kvq_dequantize", "kvq_status_string",
+           "kvq_evict_pages", "kvq_norm_rope", "kvq_prompt_attention", "kvq_select_static_channels", "kvq_dequantize",
+           "kvq_status_string",
            "kvq_last_cuda_error", "kvq_cuda_error_name", "kvq_version")
 
 
@@ -67,7 +69,7 @@ def lib() -> ctypes.CDLL:
             if not os.path.exists(LIB_PATH):
                 raise KVQError(-1, f"CUDA library not built: {LIB_PATH} is missing")
             L = ctypes.CDLL(LIB_PATH)
-            P, I, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+            P, I, S, L64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64
             pcfg, pcache = ctypes.POINTER(kvq_config), ctypes.POINTER(kvq_cache)
             sig = {
                 "kvq_block_bytes": (I, [pcfg, I, ctypes.POINTER(S)]),
@@ -85,6 +87,10 @@ def lib() -> ctypes.CDLL:
                                            P]),
                 "kvq_page_mass": (I, [pcfg, I, I, I, P, P, P, ctypes.c_float, P, P, P]),
                 "kvq_evict_pages": (I, [pcfg, pcache, P, I, I, I, P, P, P, P, P]),
+                "kvq_norm_rope": (I, [pcfg, P, L64, I, P, L64, I, I, P, P, ctypes.c_float, P, I, P, I, P, I, P, L64, P, L64, I,
+                                      P]),
+                "kvq_prompt_attention": (I, [pcfg, P, L64, P, L64, P, L64, I, I, I, P, P, I, ctypes.c_float, I, P, L64, I, P, P,
+                                             P]),
                 "kvq_select_static_channels": (I, [pcfg, P, P, I, I, P, P]),
                 "kvq_dequantize": (I, [pcfg, pcache, I, I, I, I, I, P, P]),
                 "kvq_status_string": (ctypes.c_char_p, [I]),
@@ -504,6 +510,128 @@ def kvq_evict_pages(cache: QuantizedKVCache, mass: torch.Tensor, keep_pages: int
     _call("kvq_evict_pages", index, stream, pcfg, pcache, mass.data_ptr(), keep_pages, sink_pages, recent_pages,
           page_table_out.data_ptr(), seq_lens_out.data_ptr(), mass_out.data_ptr(), evicted.data_ptr())
     return evicted
+
+
+def _token_rows(t: torch.Tensor, heads: int, D: int):
+    """(rows, elements from a row to the next) of a tensor [..., heads, D] whose last two dimensions are
+    dense and whose others step evenly: a contiguous tensor, or a part of one projection's rows."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 3 or shape[-2:] != (heads, D):
+        raise ValueError(f"a tensor of shape {tuple(shape)} where [..., {heads}, {D}] is wanted")
+    rows, step = 1, None
+    for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+        if n != 1:
+            if step is None:
+                step = s
+            elif s != step * rows:
+                raise ValueError(f"rows of a tensor with strides {tuple(strides)} are not evenly spaced")
+        rows *= n
+    if rows and (strides[-1] != 1 or (heads > 1 and strides[-2] != D)):
+        raise ValueError(f"a tensor with strides {tuple(strides)}: the heads of a row have to be contiguous")
+    return rows, heads * D if step is None else step
+
+
+def kvq_norm_rope(cache: QuantizedKVCache, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None,
+                  inv_freq: torch.Tensor | None, q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                  eps: float | None = 1e-6, interleaved: bool = False, pair_axis=None, q_out: torch.Tensor | None = None,
+                  k_out: torch.Tensor | None = None, out_dtype=None, stream=None):
+    """Per-head RMS norm (eps None: none) of q [..., Hq, D] and k [..., Hkv, D] (bf16, f16 or f32; either may be
+    None) and their rotary positions in one pass; returns (q_out, k_out).  positions: int32, one a row ([rows] or
+    q's leading shape), or [axes, rows] with pair_axis, the axis of each of the rot_dim / 2 pairs (a list).
+    inv_freq: fp32 [rot_dim / 2] (None: norms alone).  q_weight, k_weight: fp32 [D] gains (None: ones).  The outputs
+    may be the inputs."""
+    cfg, (pcfg, _, index) = cache.cfg, _refs(cache)
+    D, f32 = cfg.head_dim, torch.float32
+    x = q if q is not None else k
+    if x is None or (q is not None and k is not None and q.dtype is not k.dtype):
+        raise ValueError("q or k, of one type, is wanted")
+    Hq = q.shape[-2] if q is not None else 0
+    given = [out for src, out in ((q, q_out), (k, k_out)) if src is not None and out is not None]
+    if out_dtype is None:
+        out_dtype = given[0].dtype if given else x.dtype
+    if any(t.dtype is not out_dtype for t in given):
+        raise ValueError("q_out and k_out have to be of one type, out_dtype")
+    args, rows = [], None
+    for src, out, heads in ((q, q_out, Hq), (k, k_out, cfg.num_kv_heads)):
+        if src is None:
+            args.append((None, 0, None, None, 0))
+            continue
+        n, step = _token_rows(src, heads, D)
+        if rows not in (None, n):
+            raise ValueError(f"{rows} rows of q and {n} of k")
+        rows = n
+        if out is None:
+            shape = src.shape
+            out = _made_on(stream, lambda: torch.empty(shape, dtype=out_dtype, device=src.device), returned=True)
+        m, out_step = _token_rows(out, heads, D)
+        if m != n:
+            raise ValueError(f"{n} rows in, {m} out")
+        args.append((src.data_ptr(), step, out, out.data_ptr(), out_step))
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    axes = 1
+    if rot:
+        assert inv_freq.dtype is f32 and inv_freq.is_contiguous() and inv_freq.dim() == 1
+        assert positions is not None and positions.dtype is torch.int32 and positions.is_contiguous()
+        axes = positions.shape[0] if pair_axis is not None else 1
+        if positions.numel() != axes * rows:
+            raise ValueError(f"{positions.numel()} positions for {rows} rows of {axes} axes")
+    for w in (q_weight, k_weight):
+        assert w is None or (w.dtype is f32 and w.is_contiguous() and w.shape == (D,))
+    pairs = None
+    if pair_axis is not None:
+        pair_axis = [int(p) for p in pair_axis]
+        if len(pair_axis) != rot // 2 or any(not 0 <= p < axes for p in pair_axis):
+            raise ValueError(f"pair_axis: an axis below {axes} for each of the {rot // 2} pairs")
+        pairs = bytes(pair_axis)
+    if eps is not None and not eps >= 0:
+        raise ValueError("eps has to be at least 0 (None: no norm)")
+    (qp, qs, qo, qop, qos), (kp, ks, ko, kop, kos) = args
+    _check_on(index, q, k, qo, ko, positions if rot else None, inv_freq, q_weight, k_weight)
+    if rows:
+        _call("kvq_norm_rope", index, stream, pcfg, qp, qs, Hq, kp, ks, _DTYPE[x.dtype], rows, _addr(q_weight), _addr(k_weight),
+              -1.0 if eps is None else float(eps), _addr(positions) if rot else None, axes, _addr(inv_freq) if rot else None, rot,
+              pairs, int(interleaved), qop, qos, kop, kos, _DTYPE[out_dtype])
+    return qo, ko
+
+
+def kvq_prompt_attention(cache: QuantizedKVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float,
+                         t_per_seq: torch.Tensor | None = None, first_row: torch.Tensor | None = None, t_new: int | None = None,
+                         causal: bool = True, out: torch.Tensor | None = None, out_dtype=None, lse: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Attention of whole prompts, each over its own tokens (causal or full).  A padded batch: q [num_seqs, t_new,
+    Hq, D], k and v [num_seqs, t_new, Hkv, D] (bf16 or f16), sequence b's first t_per_seq[b] tokens (int32
+    [num_seqs]; None: all).  Packed sequences: q [rows, Hq, D], ..., first_row and t_per_seq int32 [num_seqs] on the
+    device, t_new a bound on the lengths.  lse: fp32 of q's leading shape x Hq, filled when given.  Rows of no
+    sequence are left as they were (an `out` made here: uninitialised)."""
+    cfg, (pcfg, _, index) = cache.cfg, _refs(cache)
+    B, Hkv, D = cfg.num_seqs, cfg.num_kv_heads, cfg.head_dim
+    Hq, packed = q.shape[-2], first_row is not None
+    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype is not q.dtype or v.dtype is not q.dtype:
+        raise ValueError("q, k and v have to be of one type, bf16 or f16")
+    if packed:
+        if t_per_seq is None or t_new is None:
+            raise ValueError("packed sequences: t_per_seq and t_new are wanted")
+        assert q.dim() == 3 and first_row.dtype is torch.int32 and first_row.is_contiguous() and first_row.shape == (B,)
+    else:
+        assert q.dim() == 4 and q.shape[0] == B and t_new in (None, q.shape[1])
+        t_new = q.shape[1]
+    assert k.shape == q.shape[:-2] + (Hkv, D) and v.shape == k.shape
+    if t_per_seq is not None:
+        assert t_per_seq.dtype is torch.int32 and t_per_seq.is_contiguous() and t_per_seq.shape == (B,)
+    (rows, qs), (_, ks), (_, vs) = _token_rows(q, Hq, D), _token_rows(k, Hkv, D), _token_rows(v, Hkv, D)
+    if out is None:
+        shape, made = q.shape, out_dtype or q.dtype
+        out = _made_on(stream, lambda: torch.empty(shape, dtype=made, device=q.device), returned=True)
+    assert out.shape == q.shape and out.dtype in (q.dtype, torch.float32) and out_dtype in (None, out.dtype)
+    _, outs = _token_rows(out, Hq, D)
+    if lse is not None:
+        assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:-1]
+    _check_on(index, q, k, v, t_per_seq, first_row, out, lse)
+    if rows:
+        _call("kvq_prompt_attention", index, stream, pcfg, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPE[q.dtype], Hq,
+              rows, _addr(first_row), _addr(t_per_seq), t_new, float(softmax_scale), int(causal), out.data_ptr(), outs,
+              _DTYPE[out.dtype], _addr(lse), cache.status.data_ptr())
+    return out
 
 
 def kvq_dequantize(cache: QuantizedKVCache, seq: int, kv_head: int, which: int, tok_begin: int, tok_end: int,

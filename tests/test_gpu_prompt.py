@@ -1,0 +1,247 @@
+"""kvq_prompt_attention against its 64-bit definition."""
+import math
+
+import pytest
+import torch
+
+import _prompt_reference as ref
+from sub_byte_quantized_kvq_gb300 import kvq
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+NAN = float("nan")
+
+
+def handle(B, Hkv, D):
+    return kvq.QuantizedKVCache(kvq.KVQ_FMT_FP4_E2M1_S16, B, Hkv, D, 1, 1)
+
+
+def inputs(rows, Hq, Hkv, D, dtype, seed, fused=False):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    wide = torch.randn((rows, (Hq + 2 * Hkv) * D), generator=gen, device="cuda")
+    wide[:, :Hq * D] *= 1.5
+    parts = [p.unflatten(1, (-1, D)) for p in wide.to(dtype).split([Hq * D, Hkv * D, Hkv * D], 1)]
+    return parts if fused else [p.contiguous() for p in parts]
+
+
+def check(out, lse, q, k, v, scale, causal):
+    """One sequence's rows."""
+    n = q.shape[0]
+    if n == 0:
+        return
+    y, z, size, reach = ref.prompt(q, k, v, scale, causal)
+    bound, zbound = ref.prompt_bounds(y, z, size, reach, float(v.double().abs().max()), n, q.shape[-1], q.dtype, out.dtype)
+    err = (out.double() - y).abs()
+    assert (err <= bound).all(), float((err / bound).max())
+    if lse is not None:
+        assert ((lse.double() - z).abs() <= zbound).all(), float(((lse.double() - z).abs() / zbound).max())
+
+
+def run(lens, Hkv, G, D, dtype=BF, causal=True, packed=True, fused=False, out_dtype=None, seed=0, scale=None, change=None, gap=3):
+    """Sequences of `lens` tokens in one call; rows of none hold NaN.  change(q, k, v, first): further edits of the inputs."""
+    B, Hq = len(lens), Hkv * G
+    live = [max(n, 0) for n in lens]
+    if packed:   # out of order, with gaps
+        order = list(range(1, B)) + [0]
+        first, at = [0] * B, 2
+        for b in order:
+            first[b] = at
+            at += live[b] + gap
+        rows, t_new = at, max(live + [1])
+    else:
+        t_new = max(live + [1]) + 1
+        first, rows = [b * t_new for b in range(B)], B * t_new
+    q, k, v = inputs(rows, Hq, Hkv, D, dtype, seed, fused)
+    used = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for f, n in zip(first, live):
+        used[f:f + n] = True
+    if change:
+        change(q, k, v, first)
+    for x in (q, k, v):
+        x[~used] = NAN
+    scale = D ** -0.5 if scale is None else scale
+    cache = handle(B, Hkv, D)
+    out = torch.full((rows, Hq, D), 7.0, dtype=out_dtype or dtype, device="cuda")
+    lse = torch.full((rows, Hq), 7.0, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if packed:
+        got = kvq.kvq_prompt_attention(cache, q, k, v, scale, t_per_seq=n, first_row=torch.tensor(first, dtype=torch.int32, device="cuda"),
+                                       t_new=t_new, causal=causal, out=out, lse=lse)
+        assert got is out
+    else:
+        kvq.kvq_prompt_attention(cache, *[x.unflatten(0, (B, t_new)) for x in (q, k, v)], scale, t_per_seq=n, causal=causal,
+                                 out=out.unflatten(0, (B, t_new)), lse=lse.unflatten(0, (B, t_new)))
+    assert cache.status_word() == 0
+    assert (out[~used] == 7).all() and (lse[~used] == 7).all()   # rows of no sequence
+    return out, lse, q, k, v, first, scale
+
+
+def run_and_check(lens, *args, causal=True, **kw):
+    out, lse, q, k, v, first, scale = run(lens, *args, causal=causal, **kw)
+    for f, n in zip(first, lens):
+        s = slice(f, f + max(n, 0))
+        check(out[s], lse[s], q[s], k[s], v[s], scale, causal)
+
+
+LENGTHS = [[1], [2, 1, 3], [15, 16, 17, 0, 5, 31, 32, 33], [63, 64, 65, -3, 127], [128], [129, 1, 128], [255, 256, 257], [300, 511],
+           [513, 640], [1000], [1, 1500, 7, 384]]
+
+
+@pytest.mark.parametrize("lens", LENGTHS, ids=lambda x: "-".join(map(str, x)))
+@pytest.mark.parametrize("Hkv,G,D", [(2, 4, 128), (1, 8, 64), (2, 1, 64), (1, 3, 128), (1, 16, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_lengths(lens, Hkv, G, D, causal):
+    run_and_check(lens, Hkv, G, D, causal=causal, seed=len(lens))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("packed,fused,out", [(True, True, None), (False, False, None), (False, True, F32)])
+@pytest.mark.parametrize("G", [1, 2, 5, 6, 7, 12])
+def test_types_layouts_and_groups(dtype, D, packed, fused, out, G):
+    run_and_check([200, 0, 333, 64], 2, G, D, dtype=dtype, packed=packed, fused=fused, out_dtype=out, seed=G)
+
+
+@pytest.mark.parametrize("n,Hkv,G,D,dtype", [(4133, 1, 2, 128, BF), (2999, 2, 4, 64, HF), (6001, 1, 1, 64, BF)])
+def test_many_tiles(n, Hkv, G, D, dtype):
+    run_and_check([n, 700], Hkv, G, D, dtype=dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("causal", [True, False])
+def test_growing_scores(D, dtype, causal):
+    """Scores that rise (and fall) along the keys by far more than the exponential's range: the maximum has to follow."""
+    def change(q, k, v, first):
+        n = q.shape[0]
+        ramp = torch.linspace(-12, 12, n, device="cuda")
+        q[..., 0], k[..., 0] = 16.0, ramp[:, None].to(k.dtype)
+        q[::2, ..., 0] = -16.0
+    run_and_check([700, 400], 1, 4, D, dtype=dtype, causal=causal, scale=1.0, change=change)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.25, 3.0])
+def test_any_scale(scale):
+    run_and_check([300, 40], 2, 2, 64, scale=scale)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), NAN])
+@pytest.mark.parametrize("D,G", [(128, 1), (64, 8)])
+def test_later_tokens_do_not_reach_earlier_ones(bad, D, G):
+    """Infinities and NaN in K and V of some tokens: what does not attend to them is as without them, what does is not finite
+    in V's channel."""
+    lens, at = [290, 130], {0: [289, 150, 131], 1: [129]}
+    clean = run(lens, 1, G, D, seed=4)
+    def change_v(q, k, v, first):
+        for b, js in at.items():
+            for j in js:
+                v[first[b] + j, 0, 5] = bad
+    def change_k(q, k, v, first):
+        for b, js in at.items():
+            for j in js:
+                k[first[b] + j, 0, 9] = NAN if bad != bad else bad
+    out, lse, *_, first, _ = run(lens, 1, G, D, seed=4, change=change_v)
+    assert torch.equal(lse, clean[1])
+    for b, js in at.items():
+        for i in range(lens[b]):
+            r = first[b] + i
+            hit = min(js) <= i
+            same = out[r] == clean[0][r]
+            assert same[:, [c for c in range(D) if c != 5]].all()
+            assert (~torch.isfinite(out[r][:, 5])).all() if hit else same[:, 5].all()
+            if hit and bad == bad and all(j <= i for j in js if j <= i):
+                assert (out[r][:, 5] == bad).all()
+    out, lse, *_, first, _ = run(lens, 1, G, D, seed=4, change=change_k)
+    for b, js in at.items():
+        s = slice(first[b], first[b] + min(js))
+        assert torch.equal(out[s], clean[0][s]) and torch.equal(lse[s], clean[1][s])
+        if bad != bad:
+            late = slice(first[b] + min(js), first[b] + lens[b])
+            assert torch.isnan(out[late]).all() and torch.isnan(lse[late]).all()
+
+
+def test_rows_that_do_not_fit_are_skipped():
+    """A sequence that is too long, or lies outside the rows, is left out and flagged; the others are computed."""
+    Hkv, G, D, rows = 1, 2, 64, 100
+    q, k, v = inputs(rows, 2, 1, D, BF, 1)
+    for first, lens, good in (([0, 40], [41, 30], [False, True]), ([0, 90], [30, 11], [True, False]), ([-1, 50], [10, 40], [False, True]),
+                              ([2 ** 31 - 1, 0], [5, 40], [False, True]), ([60, 0], [40, 40], [True, True])):
+        cache = handle(2, Hkv, D)
+        out = torch.full((rows, 2, D), 7.0, dtype=BF, device="cuda")
+        kvq.kvq_prompt_attention(cache, q, k, v, 0.125, t_per_seq=torch.tensor(lens, dtype=torch.int32).cuda(),
+                                 first_row=torch.tensor(first, dtype=torch.int32).cuda(), t_new=40, out=out)
+        assert cache.status_word() == (0 if all(good) else kvq.KVQ_STATUS_BAD_ROWS)
+        used = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        for f, n, g in zip(first, lens, good):
+            if g:
+                used[f:f + n] = True
+                s = slice(f, f + n)
+                check(out[s], None, q[s], k[s], v[s], 0.125, True)
+        assert (out[~used] == 7).all()
+
+
+def test_many_short_sequences():
+    """More sequences than a warp has lanes, their lengths from none up."""
+    lens = [(7 * b) % 23 for b in range(151)]
+    run_and_check(lens, 1, 2, 64)
+    run_and_check([5] * 70 + [300] + [0] * 40 + [129] * 3, 2, 1, 128)
+
+
+def test_graph_streams_and_repeats():
+    gen_lens = [700, 33]
+    out, lse, q, k, v, first, scale = run(gen_lens, 2, 4, 128)
+    cache = handle(2, 2, 128)
+    n, f = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (gen_lens, first)]
+    again, relse = torch.full_like(out, 7), torch.full_like(lse, 7)
+    args = dict(t_per_seq=n, first_row=f, t_new=700, out=again, lse=relse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    kvq.kvq_prompt_attention(cache, q, k, v, scale, stream=side, **args)
+    side.synchronize()
+    assert torch.equal(again, out) and torch.equal(relse, lse)   # the same bits
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.kvq_prompt_attention(cache, q, k, v, scale, **args)
+    n.copy_(torch.tensor([129, 31]))
+    q.neg_()
+    again.fill_(7)
+    graph.replay()
+    for b, m in enumerate((129, 31)):
+        s = slice(first[b], first[b] + m)
+        check(again[s], relse[s], q[s], k[s], v[s], scale, True)
+        assert (again[first[b] + m:first[b] + gen_lens[b]] == 7).all()
+    assert cache.status_word() == 0
+
+
+def test_prompt_then_decode():
+    """The calls together: norms and rotation, the prompt's attention, the append, and a decoded token."""
+    B, T, Hq, Hkv, D, P = 2, 45, 8, 2, 64, 4
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    lens = torch.tensor([45, 18], dtype=torch.int32, device="cuda")
+    cache = kvq.QuantizedKVCache(kvq.KVQ_FMT_FP4_E2M1_S16, B, Hkv, D, P, B * P)
+    wide = torch.randn((B, T, (Hq + 2 * Hkv) * D), generator=gen, device="cuda").to(BF)
+    q, k, v = [p.unflatten(-1, (-1, D)) for p in wide.split([Hq * D, Hkv * D, Hkv * D], -1)]
+    f = (1e4 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().cuda()
+    w = 1 + 0.1 * torch.randn(D, generator=gen, device="cuda")
+    pos = torch.arange(T, device="cuda", dtype=torch.int32).repeat(B, 1)
+    qr, kr = kvq.kvq_norm_rope(cache, q, k, pos, f, w, w)
+    lse = torch.zeros((B, T, Hq), device="cuda")
+    out = kvq.kvq_prompt_attention(cache, qr, kr, v, D ** -0.5, t_per_seq=lens, lse=lse)
+    for b, n in enumerate(lens.tolist()):
+        check(out[b, :n], lse[b, :n], qr[b, :n], kr[b, :n], v[b, :n], D ** -0.5, True)
+    kvq.kvq_quantize_append(cache, kr, v.contiguous(), t_per_seq=lens)
+    assert cache.seq_lens.tolist() == [45, 18]
+    one = torch.randn((B, 1, (Hq + 2 * Hkv) * D), generator=gen, device="cuda").to(BF)
+    q1, k1, v1 = [p.unflatten(-1, (-1, D)) for p in one.split([Hq * D, Hkv * D, Hkv * D], -1)]
+    q1, k1 = kvq.kvq_norm_rope(cache, q1, k1, cache.seq_lens, f, w, w)     # positions 45 and 18
+    kvq.kvq_quantize_append(cache, k1, v1.contiguous())
+    got = kvq.kvq_decode_attention(cache, q1[:, 0].contiguous(), D ** -0.5, 64, out_dtype=F32)
+    for b, n in enumerate((46, 19)):
+        kd, vd = [torch.stack([kvq.kvq_dequantize(cache, b, h, r, 0, n) for h in range(Hkv)], 1).double() for r in (0, 1)]
+        # the rotation at the cache's own length is that of position n - 1
+        pq, _ = ref.norm_rope(one[b, :, :Hq * D].unflatten(-1, (Hq, D)), w, 1e-6, torch.tensor([[n - 1]]), f, None, False)
+        assert (q1[b].double().cpu() - pq).abs().max() <= 2.0 ** -8 * pq.abs().max() + 1e-5
+        a = torch.einsum("hgd,nhd->hgn", q1[b, 0].double().unflatten(0, (Hkv, Hq // Hkv)), kd) * D ** -0.5
+        want = torch.einsum("hgn,nhd->hgd", a.softmax(-1), vd).flatten(0, 1)
+        assert (got[b].double() - want).abs().max() <= 2e-3
+    assert cache.status_word() == 0 and math.isfinite(float(got.sum()))
