@@ -471,7 +471,7 @@ kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride,
  *   of the sequence (causal = 0),   out_i = sum_j e^a_ij v_j / sum_j e^a_ij
  * with grouped heads as kvq_decode_attention (at most 16 query heads a kv head).
  *   q, k, v     device, dtype (bf16 or f16), num_rows rows each of num_q_heads, Hkv
- *               and Hkv heads.
+ *               and Hkv heads (a row may not overlap the next).
  *   first_row   device int32 [num_seqs] or NULL: sequence b's tokens are rows
  *               first_row[b], first_row[b] + 1, ...; NULL = b * t_new (a padded
  *               batch, as append's).  Sequences may not share rows.

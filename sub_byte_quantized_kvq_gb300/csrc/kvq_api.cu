@@ -577,9 +577,9 @@ kvq_status kvq_evict_pages(const kvq_config* cfg, const kvq_cache* cache, const 
 
 // ----------------------------------------------------------------------------- before the cache
 static int dtype_bytes(int t) { return t == KVQ_BF16 || t == KVQ_F16 ? 2 : t == KVQ_F32 ? 4 : 0; }
-// Rows of `width` elements of `es` bytes, `stride` elements apart: 16-byte aligned, and (written ones) apart from one another.
-static bool rows_ok(const void* p, int64_t stride, int es, int64_t width, bool written) {
-  if (!p || !aligned16(p) || stride < (written ? width : 0) || stride > (1ll << 37)) return false;
+// Rows of `width` elements of `es` bytes, `stride` elements apart: 16-byte aligned, and (apart) not one over another.
+static bool rows_ok(const void* p, int64_t stride, int es, int64_t width, bool apart) {
+  if (!p || !aligned16(p) || stride < (apart ? width : 0) || stride > (1ll << 37)) return false;
   return stride * es % 16 == 0;
 }
 
@@ -641,7 +641,7 @@ kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_
   const int G = num_q_heads / cfg->num_kv_heads;
   if (!dim_supported(cfg) || G > 16) return KVQ_ERR_UNSUPPORTED;
   const int64_t wq = (int64_t)num_q_heads * cfg->head_dim, wk = (int64_t)cfg->num_kv_heads * cfg->head_dim;
-  if (!rows_ok(q, q_stride, 2, wq, false) || !rows_ok(k, k_stride, 2, wk, false) || !rows_ok(v, v_stride, 2, wk, false) ||
+  if (!rows_ok(q, q_stride, 2, wq, true) || !rows_ok(k, k_stride, 2, wk, true) || !rows_ok(v, v_stride, 2, wk, true) ||
       !rows_ok(out, out_stride, dtype_bytes(out_dtype), wq, true))
     return KVQ_ERR_INVALID_ARG;
   if (t_new == 0 || num_rows == 0) return KVQ_OK;
@@ -665,8 +665,9 @@ kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_
   a.rows = num_rows;
   a.t_new = t_new;
   a.causal = causal;
+  a.out32 = out_dtype == KVQ_F32;
   a.scale = softmax_scale;
-  return cuda_status(prompt_launch(a, cfg->head_dim, dtype, out_dtype, static_cast<cudaStream_t>(stream)));
+  return cuda_status(prompt_launch(a, cfg->head_dim, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t kvq_last_cuda_error(void) { return g_last_cuda_error; }

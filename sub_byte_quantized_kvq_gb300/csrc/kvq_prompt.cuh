@@ -30,10 +30,11 @@ struct PromptArgs {
   uint32_t* status;
   long long q_stride, k_stride, v_stride, out_stride;   // elements from a row to the next
   int B, Hkv, Hq, G, rows, t_new, causal;
+  int out32;                // out is fp32, else of the inputs' type
   float scale;
 };
-// dtype: KVQ_BF16 or KVQ_F16; out_dtype: the same or KVQ_F32.
-cudaError_t prompt_launch(const PromptArgs& a, int D, int dtype, int out_dtype, cudaStream_t st);
+// dtype: KVQ_BF16 or KVQ_F16.
+cudaError_t prompt_launch(const PromptArgs& a, int D, int dtype, cudaStream_t st);
 
 // The rows of sequence b: false where it has none, or where they do not fit the
 // call's bounds (bad).

@@ -2332,26 +2332,9 @@ cudaError_t launch(ProjArgs& p, int cs, bool one_wave, cudaStream_t st, bool& en
 }
 }  // namespace small
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once through the runtime.
-static EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
 // Row-major bf16 [rows][cols] matrix, boxes of 64 columns x box_rows rows, 128-byte swizzle.
 static bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  const EncodeTiledFn enc = encode_tiled();
+  const tc::EncodeTiledFn enc = tc::encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
   const cuuint32_t box[2] = {(cuuint32_t)kPK, box_rows}, es[2] = {1, 1};

@@ -415,29 +415,6 @@ __device__ __forceinline__ void fill_page_lse(const TreeArgs& a, int b, int h, i
   }
 }
 
-// Pairs of fp32 in a 64-bit register.
-__device__ __forceinline__ uint64_t pack2u(uint32_t x, uint32_t y) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t pack2(float x, float y) { return pack2u(__float_as_uint(x), __float_as_uint(y)); }
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  uint32_t x, y;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
-  return make_float2(__uint_as_float(x), __uint_as_float(y));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // A softmax thread's row: m in log2 units, p = 2^(s f - m + kPBias), l the fp32 sum of p.  A page with a V shift b:
 // P = p 2^b, and m is raised by what P needs.
 template <int FMT, int D>

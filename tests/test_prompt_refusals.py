@@ -59,7 +59,7 @@ def test_prompt_refusals(kvq):
     assert prompt() == kvq.KVQ_OK and prompt(rows=5, t_new=0) == kvq.KVQ_OK     # no rows, no tokens
     assert prompt(t=1, tout=1) == kvq.KVQ_OK and prompt(t=1, tout=2) == kvq.KVQ_OK and prompt(tout=2) == kvq.KVQ_OK
     for bad in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(status=None), dict(q=FAKE + 8), dict(k=FAKE + 8),
-                dict(v=FAKE + 2), dict(out=FAKE + 4), dict(qs=4100), dict(ks=1020), dict(vs=-1024), dict(os=4088), dict(t=2), dict(t=2, tout=2),
+                dict(v=FAKE + 2), dict(out=FAKE + 4), dict(qs=4100), dict(ks=1020), dict(vs=-1024), dict(qs=4088), dict(ks=0), dict(os=4088), dict(t=2), dict(t=2, tout=2),
                 dict(tout=1), dict(tout=3), dict(Hq=0), dict(Hq=31), dict(rows=-1), dict(t_new=-1), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(causal=2)):
         assert prompt(**bad) == kvq.KVQ_ERR_INVALID_ARG, bad
