@@ -466,6 +466,10 @@ kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride,
                          void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, kvq_dtype out_dtype,
                          void* stream);
 
+/* Longest prompt of kvq_prompt_attention (a device wait gives up after 100 ms, and one lasts as long as the keys of a
+ * tile of tokens: about 2 us for 128). */
+#define KVQ_PROMPT_MAX_TOKENS (1 << 21)
+
 /* Attention of whole prompts, each sequence over its own tokens:
  *   a_ij = softmax_scale * q_i . k_j for j <= i (causal = 1) or for every token j
  *   of the sequence (causal = 0),   out_i = sum_j e^a_ij v_j / sum_j e^a_ij
@@ -477,7 +481,7 @@ kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride,
  *               batch, as append's).  Sequences may not share rows.
  *   t_per_seq   device int32 [num_seqs] or NULL: sequence b has t_per_seq[b] tokens
  *               (none if <= 0); NULL = t_new each.
- *   t_new       host bound on the lengths (sizes the grid).  A sequence that is
+ *   t_new       host bound on the lengths, at most KVQ_PROMPT_MAX_TOKENS.  A sequence that is
  *               longer, or whose rows are not all in 0..num_rows - 1, is skipped and
  *               sets KVQ_STATUS_BAD_ROWS.
  *   out         device, rows of num_q_heads heads, in out_dtype (dtype or f32).
@@ -487,7 +491,9 @@ kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride,
  * v that a token does not attend to (later tokens, other sequences, rows of none)
  * never reach it, whatever they hold.  Weights are rounded to the inputs' type
  * (2^-9 relative for bf16, 2^-11 for f16), the sums are fp32.  A token whose
- * scores are all -inf gets 0 and lse -inf.  One launch. */
+ * scores are all -inf gets 0 and lse -inf.  |v| below 2^100 (the sums before the
+ * division are of values up to 2^8 n |v|).  A call that sets KVQ_STATUS_TIMEOUT
+ * leaves NaN in the rows of every CTA that gave up.  One launch. */
 kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                 const void* v, int64_t v_stride, kvq_dtype dtype, int32_t num_q_heads, int32_t num_rows,
                                 const int32_t* first_row, const int32_t* t_per_seq, int32_t t_new, float softmax_scale,

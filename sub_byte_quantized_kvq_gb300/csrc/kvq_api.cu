@@ -639,7 +639,7 @@ kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_
     return KVQ_ERR_INVALID_ARG;
   if ((dtype != KVQ_BF16 && dtype != KVQ_F16) || (out_dtype != dtype && out_dtype != KVQ_F32)) return KVQ_ERR_INVALID_ARG;
   const int G = num_q_heads / cfg->num_kv_heads;
-  if (!dim_supported(cfg) || G > 16) return KVQ_ERR_UNSUPPORTED;
+  if (!dim_supported(cfg) || G > 16 || t_new > KVQ_PROMPT_MAX_TOKENS) return KVQ_ERR_UNSUPPORTED;
   const int64_t wq = (int64_t)num_q_heads * cfg->head_dim, wk = (int64_t)cfg->num_kv_heads * cfg->head_dim;
   if (!rows_ok(q, q_stride, 2, wq, true) || !rows_ok(k, k_stride, 2, wk, true) || !rows_ok(v, v_stride, 2, wk, true) ||
       !rows_ok(out, out_stride, dtype_bytes(out_dtype), wq, true))

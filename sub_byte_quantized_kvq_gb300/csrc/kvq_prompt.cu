@@ -27,6 +27,7 @@
 // is rounded to the inputs' type (fp16 biased by 2^6, so that small p keep their
 // bits: p <= 2^14).
 #include <algorithm>
+#include <mutex>
 
 #include "kvq_prompt.cuh"
 #include "kvq_tc.cuh"
@@ -59,6 +60,7 @@ struct Launch {
   PromptArgs a;
   int P, tokens, tiles;   // heads and tokens of a tile, tiles of a CTA
   int units;              // Hq / P
+  long long pairs;        // tile pairs of all units, at most
 };
 
 struct Wait {
@@ -90,50 +92,82 @@ __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
   return h2_as_u32(__floats2half2_rn(lo, hi));
 }
 
-// The CTA's sequence and the first of its tokens, by its rank among all CTAs of a head: those with the most keys first
-// (later CTAs then fill the gaps that they leave), none for what a sequence does not have.  With T_b tiles of `span`
-// tokens in sequence b, count(L) = sum_b max(0, T_b - L) tiles lie at L or later in their sequences; the rank-th is
-// the largest L with count(L) > rank.  By one warp, the first 128 sequences in registers.
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int span, long long rank, int lane, int& b, int& t0) {
-  constexpr int R = 4;
-  auto tiles_of = [&](int s) {
+// A tile pair's sequence and the first of its tokens, by its rank among all pairs of a head: those with the most keys
+// first (later pairs then fill the gaps that they leave), none for what a sequence does not have.  With T_b pairs of
+// `span` tokens in sequence b, count(L) = sum_b max(0, T_b - L) pairs lie at L or later in their sequences; the rank-th
+// is at the largest L with count(L) > rank.  By one warp, the first 512 sequences' T_b in registers.
+struct Finder {
+  static constexpr int R = 16;
+  const PromptArgs& a;
+  int span, lane, T[R];
+  bool even;   // every sequence has t_new tokens
+  __device__ __forceinline__ int tiles_of(int s) const {
     long long f;
     int n;
     bool bad;
     return s < a.B && prompt_rows(a, s, f, n, bad) ? (n + span - 1) / span : 0;
-  };
-  int T[R];
+  }
+  __device__ __forceinline__ Finder(const PromptArgs& args, int sp, int ln) : a(args), span(sp), lane(ln) {
+    even = !a.lens && !a.first && (long long)a.B * a.t_new <= a.rows;
 #pragma unroll
-  for (int k = 0; k < R; ++k) T[k] = tiles_of(lane + 32 * k);
-  auto count = [&](int L) {
+    for (int k = 0; k < R; ++k) T[k] = !even && 32 * k < a.B ? tiles_of(lane + 32 * k) : 0;
+  }
+  __device__ __forceinline__ long long count(int L) const {
     long long c = 0;
 #pragma unroll
     for (int k = 0; k < R; ++k) c += max(0, T[k] - L);
     for (int s = lane + 32 * R; s < a.B; s += 32) c += max(0, tiles_of(s) - L);
-    // (a sequence has at most 2^31 tiles; their sum over a warp in two halves)
+    // (the sum over a warp in two halves)
     const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)c & 0xFFFFFFu), hi = __reduce_add_sync(0xffffffffu, (unsigned)(c >> 24));
     return (long long)lo + ((long long)hi << 24);
-  };
-  if (count(0) <= rank) return false;
-  int lo = 0, hi = (a.t_new - 1) / span + 1;   // count(lo) > rank >= count(hi) = 0
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (count(mid) > rank) lo = mid;
-    else hi = mid;
   }
-  int left = (int)(rank - count(lo + 1));      // which of the sequences with more than lo tiles
-  for (int s0 = 0; s0 < a.B; s0 += 32) {
-    const unsigned has = __ballot_sync(0xffffffffu, tiles_of(s0 + lane) > lo);
-    const int n = __popc(has);
-    if (left < n) {
-      const unsigned at = __fns(has, 0, left + 1);
-      b = s0 + (int)at;
-      t0 = lo * span;
-      return true;
+  __device__ __forceinline__ bool find(long long rank, int& b, int& t0) const {
+    const int most = (a.t_new - 1) / span + 1;
+    if (even) {
+      b = (int)(rank % a.B);
+      t0 = (int)(most - 1 - rank / a.B) * span;
+      return rank < (long long)most * a.B;
     }
-    left -= n;
+    if (count(0) <= rank) return false;
+    int lo = 0, hi = most;   // count(lo) > rank >= count(hi) = 0
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (count(mid) > rank) lo = mid;
+      else hi = mid;
+    }
+    int left = (int)(rank - count(lo + 1));   // which of the sequences with more than lo pairs
+    for (int s0 = 0; s0 < a.B; s0 += 32) {
+      const unsigned has = __ballot_sync(0xffffffffu, tiles_of(s0 + lane) > lo);
+      const int n = __popc(has);
+      if (left < n) {
+        b = s0 + (int)__fns(has, 0, left + 1);
+        t0 = lo * span;
+        return true;
+      }
+      left -= n;
+    }
+    return false;
   }
-  return false;
+};
+
+// What the roles know of a tile pair: the sequence's first row and length (0: no more tiles), the first token, and the
+// heads (unit u: query heads u P .. u P + P - 1).
+struct Pair {
+  int first, n, t0, unit;
+};
+// The k-th pair of this CTA: every round of the grid's CTAs takes the next ones in the finder's order, odd rounds
+// backwards, so that no CTA has the longer one each time.
+__device__ __forceinline__ Pair next_pair(const Launch& p, const Finder& finder, long long k) {
+  const long long i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  Pair r = {0, 0, 0, (int)(i % p.units)};
+  int b;
+  if (i < p.pairs && finder.find(i / p.units, b, r.t0)) {
+    long long first;
+    bool bad;
+    prompt_rows(p.a, b, first, r.n, bad);
+    r.first = (int)first;
+  }
+  return r;
 }
 
 template <int D, bool BF>
@@ -142,28 +176,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   constexpr int NS = Pl::kStages, KC = D / 64;
   extern __shared__ uint8_t raw_smem[];
   const PromptArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
   uint8_t* ring = smem + 2 * Pl::kTile;
-  uint64_t *q_full = reinterpret_cast<uint64_t*>(ring + NS * Pl::kTile), *full = q_full + 2, *empty = full + NS, *s_full = empty + NS,
-           *p_full = s_full + 2, *o_done = p_full + 2, *v_raw = o_done + 2, *v_clean = v_raw + 4, *drained = v_clean + 4;
-  volatile int* found = reinterpret_cast<volatile int*>(drained + 1);   // [0] b or -1, [1] t0, [2] stop, [3] bad V
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1) + 4;
-  static_assert((2 + 2 * NS + 2 + 2 + 2 + 4 + 4 + 1) * 8 + 20 <= 512 && NS <= 8, "barriers");
+  uint64_t *q_full = reinterpret_cast<uint64_t*>(ring + NS * Pl::kTile), *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + NS,
+           *s_full = empty + NS, *p_full = s_full + 2, *o_done = p_full + 4, *v_raw = o_done + 2, *v_clean = v_raw + 4,
+           *info_full = v_clean + 4, *info_empty = info_full + 2, *drained = info_empty + 2;
+  volatile int* info = reinterpret_cast<volatile int*>(drained + 1);   // [2] Pair
+  volatile int* stop = info + 8;                                       // a wait gave up
+  volatile int* bad_v = stop + 1;                                      // [2] pair's V has infinities or NaN that were cleaned
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1) + 11;
+  static_assert((4 + 2 * NS + 2 + 4 + 2 + 4 + 4 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
 
-  if (warp == 0) {
-    int b = -1, t0 = 0;
-    if (!find_tile(a, p.tiles * p.tokens, blockIdx.x / p.units, lane, b, t0)) b = -1;
-    if (lane == 0) {
-      found[0] = b;
-      found[1] = t0;
-    }
-  } else if (warp == 8 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_done[i], 1);
+      mbar_init(&info_full[i], 1);
+      mbar_init(&info_empty[i], 11);   // softmax, MMA and cleaning warps
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(&full[i], 1);
@@ -175,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
     mbar_init(drained, 1);
     fence_mbar_init();
-    found[2] = found[3] = 0;
+    stop[0] = bad_v[0] = bad_v[1] = 0;
   } else if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -192,39 +226,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *tslot;
-  const int b = found[0], t0 = found[1];
+  const Wait wait{stop};
   bool ok = true;
-  if (b >= 0) {
-    const Wait wait{found + 2};
-    long long first;
-    int n;
-    bool bad;
-    prompt_rows(a, b, first, n, bad);
-    const int u = blockIdx.x % p.units, head0 = u * p.P, kvh = head0 / a.G;
-    // keys that tile x's tokens see, in tiles; the first of them that not every token sees whole
-    auto n_keys = [&](int x) {
-      const int t = t0 + x * p.tokens;
-      return x < p.tiles && t < n ? ((a.causal ? min(n, t + p.tokens) : n) + kKeys - 1) / kKeys : 0;
-    };
-    const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1);
-    auto masked_from = [&](int t) { return a.causal ? min(t + 1, n) / kKeys : n / kKeys; };
-    const int clean0 = masked_from(t0);   // V tiles from here on are cleaned
+  Pair pair = {0, 0, 0, 0};
+  // keys that the tokens of the pair's tile x see, in tiles; the first tile that not every token from t on sees whole
+  auto n_keys = [&](int x) {
+    const int t = pair.t0 + x * p.tokens;
+    return x < p.tiles && t < pair.n ? ((a.causal ? min(pair.n, t + p.tokens) : pair.n) + kKeys - 1) / kKeys : 0;
+  };
+  auto masked_from = [&](int t) { return (a.causal ? min(t + 1, pair.n) : pair.n) / kKeys; };
+  // the k-th pair, published by the load warp (whole warps; false at the end)
+  auto get_pair = [&](int k) {
+    ok = __all_sync(0xffffffffu, wait(&info_full[k & 1], (k >> 1) & 1));
+    if (!ok) return false;
+    const volatile int* i = info + 4 * (k & 1);
+    pair = {i[0], i[1], i[2], i[3]};
+    return pair.n > 0;
+  };
+  auto give_pair_back = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&info_empty[k & 1]);
+  };
 
-    if (warp < 8) {
-      // ---------------------------------------------------------------- softmax, one tile a warpgroup
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-      const int x = warp >> 2, row = tid & 127, nx = x ? n1 : n0, tx = t0 + x * p.tokens;
-      const int token = tx + row / p.P, head = head0 + row % p.P;
-      const int lim = a.causal ? min(n, token + 1) : n, mask0 = masked_from(tx);
-      const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-      const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + D * x, tp = tmem + lanes + Pl::p_at(x);
-      const bool neg = a.scale < 0.f;
-      const float f = fmaxf(fabsf(a.scale) * kLog2e, 1e-36f);   // (not 0: what is masked is -inf times it)
-      constexpr float bias = BF ? 0.f : 6.f;
+  struct Place {   // of the ring, and the phase of its barriers' use
+    int i, phase;
+    __device__ __forceinline__ Place next() const { return i + 1 == NS ? Place{0, phase ^ 1} : Place{i + 1, phase}; }
+  };
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------ softmax, one tile a warpgroup
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + D * x, tp = tmem + lanes + Pl::p_at(x);
+    const bool neg = a.scale < 0.f;
+    const float f = fmaxf(fabsf(a.scale) * kLog2e, 1e-36f);   // (not 0: what is masked is -inf times it)
+    constexpr float bias = BF ? 0.f : 6.f;
+    int done = 0;   // key tiles of earlier pairs
+    for (int pk = 0; get_pair(pk); ++pk) {
+      const int nx = n_keys(x), tx = pair.t0 + x * p.tokens;
+      const int token = tx + row / p.P, mask0 = masked_from(tx);
+      const int lim = a.causal ? min(pair.n, token + 1) : pair.n;
       float m = -INFINITY;
       uint64_t l2 = 0ull;
       for (int it = 0; it < nx; ++it) {
-        ok = __all_sync(0xffffffffu, wait(&s_full[x], it & 1));
+        ok = __all_sync(0xffffffffu, wait(&s_full[x], (done + it) & 1));
         if (!ok) break;
         tc::fence_after();
         uint32_t s[4][32];
@@ -258,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           m = mx;
         } else {
           if (!Pl::kOverS) {   // PV(it - 1) reads P (over S, S(it) was issued after it)
-            ok = __all_sync(0xffffffffu, wait(&o_done[x], (it - 1) & 1));
+            ok = __all_sync(0xffffffffu, wait(&o_done[x], (done + it - 1) & 1));
             if (!ok) break;
             tc::fence_after();
           }
@@ -291,35 +337,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             w[j / 2] = pack_p<BF>(e0, e1);
           }
           tc::st16(tp + 16 * c, w);
+          if (c & 1) {   // half of the keys: their PV may start
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * x + (c >> 1)]);
+          }
         }
-        tc::wait_st();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
       }
-      // ---- O / l, and the tile's log-sum-exp
+      if (!ok) break;
       if (nx > 0) {
-        ok = ok && __all_sync(0xffffffffu, wait(&o_done[x], (nx - 1) & 1));
+        // ---- O / l, and the tile's log-sum-exp
+        done += nx;
+        ok = __all_sync(0xffffffffu, wait(&o_done[x], (done - 1) & 1));
+        if (!ok) break;
         tc::fence_after();
         const float2 lp = unpack2(l2);
-        const float l = lp.x + lp.y;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const bool live = token < n, patch = found[3] != 0;
-        const long long r = first + token;
+        const float l = lp.x + lp.y, inv = l == 0.f ? 0.f : 1.f / l;
+        const bool live = token < pair.n, patch = bad_v[pk & 1] != 0;
+        const long long r = (long long)pair.first + token;
+        const int head = pair.unit * p.P + row % p.P;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          if (ok) {
-            tc::ld32(to + c, o);
+          tc::ld32(to + c, o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = NAN;
-          }
+          for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
           if (__builtin_expect(patch && live, 0)) {   // infinities and NaN that the cleaning took out of the tiles
-            for (int j = t0 + 1; j < lim; ++j) {
-              const uint16_t* v = static_cast<const uint16_t*>(a.v) + (first + j) * a.v_stride + (long long)kvh * D + c;
+            for (int j = pair.t0 + 1; j < lim; ++j) {
+              const uint16_t* v = static_cast<const uint16_t*>(a.v) + ((long long)pair.first + j) * a.v_stride + (long long)(head / a.G) * D + c;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float y = BF ? __uint_as_float((uint32_t)v[i] << 16) : __half2float(__ushort_as_half(v[i]));
@@ -341,119 +387,176 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           __syncwarp();
         }
-        if (a.lse && live)
-          a.lse[r * a.Hq + head] = !ok ? NAN : l == 0.f ? -INFINITY : (m * f - bias + __log2f(l)) * kLn2f;
+        if (a.lse && live) a.lse[r * a.Hq + head] = l == 0.f ? -INFINITY : (m * f - bias + __log2f(l)) * kLn2f;
         tc::fence_before();
       }
-    } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-      if (warp == 8 && lane == 0) {
-        // -------------------------------------------------------------- loads: K(0), V(0), K(1), ... through the ring
-        for (int x = 0; x < 2; ++x)
-          if (x ? n1 : n0) {
-            mbar_arrive_expect_tx(&q_full[x], Pl::kTile);
+      give_pair_back(pk);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    int pos = 0, cleaned = 0;   // places of the ring and cleaned V tiles of earlier pairs
+    if (warp == 8) {
+      // ---------------------------------------------------------------- pairs and loads: K(0), V(0), K(1), ... through the ring
+      int q_used[2] = {0, 0};
+      const Finder finder(a, p.tiles * p.tokens, lane);
+      for (int pk = 0; ok; ++pk) {
+        pair = next_pair(p, finder, pk);
+        if (lane == 0) {
+          if (pk >= 2) ok = wait(&info_empty[pk & 1], ((pk >> 1) - 1) & 1);
+          if (ok) {
+            volatile int* i = info + 4 * (pk & 1);
+            i[0] = pair.first;
+            i[1] = pair.n;
+            i[2] = pair.t0;
+            i[3] = pair.unit;
+            bad_v[pk & 1] = 0;
+            mbar_arrive(&info_full[pk & 1]);
+          }
+          const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1), clean0 = masked_from(pair.t0), head0 = pair.unit * p.P;
+          for (int i = 0; ok && pair.n > 0 && i < 2 * most; ++i) {
+            if (i == 0 || i == 1) {   // the tiles' queries: tile 0's before the first keys, tile 1's behind them
+              if (i ? n1 : n0) {
+                if (q_used[i]) ok = wait(&q_empty[i], (q_used[i] - 1) & 1);
+                if (!ok) break;
+                ++q_used[i];
+                mbar_arrive_expect_tx(&q_full[i], Pl::kTile);
+                for (int c = 0; c < KC; ++c)
+                  tc::tma3d(smem + i * Pl::kTile + c * Pl::kBlock, &p.q, 64 * c, head0, pair.first + pair.t0 + i * p.tokens, &q_full[i]);
+              }
+            }
+            const int st = pos % NS;
+            if (pos >= NS) ok = wait(&empty[st], (pos / NS - 1) & 1);
+            if (!ok) break;
+            // a V tile that is cleaned lands on a barrier of its own (the ring holds at most four), so that the cleaning warps
+            // see each of its phases
+            const bool raw = (i & 1) && (i >> 1) >= clean0;
+            uint64_t* bar = raw ? &v_raw[cleaned & 3] : &full[st];
+            if (raw) {
+              mbar_arrive(&full[st]);
+              ++cleaned;
+            }
+            mbar_arrive_expect_tx(bar, Pl::kTile);
             for (int c = 0; c < KC; ++c)
-              tc::tma3d(smem + x * Pl::kTile + c * Pl::kBlock, &p.q, 64 * c, head0, (int)first + t0 + x * p.tokens, &q_full[x]);
+              tc::tma3d(ring + st * Pl::kTile + c * Pl::kBlock, i & 1 ? &p.v : &p.k, 64 * c, head0 / a.G, pair.first + (i >> 1) * kKeys, bar);
+            ++pos;
           }
-        int i = 0;
-        for (; i < 2 * most; ++i) {
-          const int st = i % NS;
-          if (i >= NS && !wait(&empty[st], (i / NS - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          // a V tile that is cleaned lands on a barrier of its own (the ring holds at most four), so that the cleaning warps
-          // see each of its phases
-          const int w = (i >> 1) - clean0;
-          uint64_t* bar = (i & 1) && w >= 0 ? &v_raw[w & 3] : &full[st];
-          if (bar != &full[st]) mbar_arrive(&full[st]);
-          mbar_arrive_expect_tx(bar, Pl::kTile);
-          for (int c = 0; c < KC; ++c)
-            tc::tma3d(ring + st * Pl::kTile + c * Pl::kBlock, i & 1 ? &p.v : &p.k, 64 * c, kvh, (int)first + (i >> 1) * kKeys, bar);
-        }
-        if (!ok) {   // what is in flight has to land before the CTA ends
-          for (int x = 0; x < 2; ++x)
-            if (x ? n1 : n0) mbar_wait_bounded(&q_full[x], 0, kWaitLimitNs);
-          for (int j = max(0, i - NS); j < i; ++j) {
-            const int w = (j >> 1) - clean0;
-            if ((j & 1) && w >= 0) mbar_wait_bounded(&v_raw[w & 3], (w >> 2) & 1, kWaitLimitNs);
-            else mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kWaitLimitNs);
+          if (!ok) {   // what is in flight has to land before the CTA ends
+            for (int i = 0; i < 2; ++i)
+              if (q_used[i]) mbar_wait_bounded(&q_full[i], (q_used[i] - 1) & 1, kWaitLimitNs);
+            for (int j = max(0, pos - NS); j < pos; ++j) mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kWaitLimitNs);
+            for (int j = max(0, cleaned - 4); j < cleaned; ++j) mbar_wait_bounded(&v_raw[j & 3], (j >> 2) & 1, kWaitLimitNs);
           }
         }
-      } else if (warp == 9 && lane == 0) {
-        // -------------------------------------------------------------- MMA
-        constexpr uint32_t id_s = BF ? tc::idesc_bf16(kM, kKeys) : tc::idesc_f16(kM, kKeys);
-        constexpr uint32_t id_o = (BF ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorN;
-        const uint64_t qd = tc::desc_sw128(smem_u32(smem)), kd = tc::desc_sw128(smem_u32(ring)),
-                       vd = tc::desc_sw128_mn(smem_u32(ring), Pl::kBlock);
-        const int total = 2 * most;
-        auto full_wait = [&](int i) { return wait(&full[i % NS], (i / NS) & 1); };
-        auto release = [&](int i) {   // (only where a later tile takes the place)
-          if (i + NS < total) tc::commit(&empty[i % NS]);
-        };
-        auto scores = [&](int x, int it) {
-          const uint64_t kt = kd + ((2 * it) % NS * Pl::kTile >> 4), qt = qd + (x * Pl::kTile >> 4);
+        ok = __all_sync(0xffffffffu, ok);
+        if (pair.n == 0) break;
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMA
+      constexpr uint32_t id_s = BF ? tc::idesc_bf16(kM, kKeys) : tc::idesc_f16(kM, kKeys);
+      constexpr uint32_t id_o = (BF ? tc::idesc_bf16(kM, D) : tc::idesc_f16(kM, D)) | tc::kBMajorN;
+      const uint64_t qd = tc::desc_sw128(smem_u32(smem)), kd = tc::desc_sw128(smem_u32(ring)),
+                     vd = tc::desc_sw128_mn(smem_u32(ring), Pl::kBlock);
+      // The whole warp goes along, and one lane of it (elect.sync) issues: the operands are then known to be the same in
+      // all lanes.  Issued by one thread in a branch of its own, each MMA took 130 cycles instead of the 64 of its math.
+      int done[2] = {0, 0}, q_used[2] = {0, 0};   // key tiles of earlier pairs, pairs with a tile x
+      Place ks{0, 0};                             // where the next K tile lies
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      auto all_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+      for (int pk = 0; get_pair(pk); ++pk) {
+        give_pair_back(pk);
+        pair.n = __shfl_sync(0xffffffffu, pair.n, 0);
+        pair.t0 = __shfl_sync(0xffffffffu, pair.t0, 0);
+        const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1), clean0 = masked_from(pair.t0);
+        auto scores = [&](int x, int it) {   // (K(it) at place `ks` of the ring)
+          const uint64_t kt = kd + (ks.i * Pl::kTile >> 4), qt = qd + (x * Pl::kTile >> 4);
+          const bool last = it + 1 == (x ? n1 : n0), frees = x == (it < n1 ? 1 : 0);   // of the queries' uses; of K(it)'s
+          if (tc::elect()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = ((k >> 2) * Pl::kBlock + (k & 3) * 32) >> 4;
-            tc::mma(tmem + 128 * x, qt + at, kt + at, id_s, k != 0);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = ((k >> 2) * Pl::kBlock + (k & 3) * 32) >> 4;
+              tc::mma(tm + 128 * x, qt + at, kt + at, id_s, k != 0);
+            }
+            tc::commit(&s_full[x]);
+            if (last) tc::commit(&q_empty[x]);
+            if (frees) tc::commit(&empty[ks.i]);
           }
-          tc::commit(&s_full[x]);
+          __syncwarp();
         };
-        ok = full_wait(0);
-        for (int x = 0; x < 2 && ok; ++x)
-          if (x ? n1 : n0) {
-            ok = wait(&q_full[x], 0);
+        // S goes over the P before it, which PV reads: MMAs with different accumulators have no order of their own
+        auto p_read = [&](int x, int it) { return !Pl::kOverS || done[x] + it == 0 || all_wait(&o_done[x], (done[x] + it - 1) & 1); };
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (ok && (x ? n1 : n0)) {
+            ok = all_wait(&q_full[x], q_used[x] & 1) && all_wait(&full[ks.i], ks.phase) && p_read(x, 0);
+            ++q_used[x];
             tc::fence_after();
             if (ok) scores(x, 0);
           }
-        if (ok) release(0);
         for (int it = 0; it < most && ok; ++it) {
-          const int w = it - clean0;
-          ok = full_wait(2 * it + 1) && (w < 0 || (wait(&v_raw[w & 3], (w >> 2) & 1) && wait(&v_clean[w & 3], (w >> 2) & 1)));
-          const int last = it < n1 ? 1 : 0;   // the last tile that uses K(it), V(it)
-          for (int x = 0; x < 2 && ok; ++x) {
-            const int nx = x ? n1 : n0;
-            if (it >= nx) continue;
-            ok = wait(&p_full[x], it & 1);
-            if (!ok) break;
-            tc::fence_after();
-            const uint64_t vt = vd + ((2 * it + 1) % NS * Pl::kTile >> 4);
+          const int w = cleaned + it - clean0;
+          const Place vs = ks.next();   // V(it)'s
+          const uint64_t vt = vd + (vs.i * Pl::kTile >> 4);
+          ks = vs.next();               // K(it + 1)'s
+          ok = all_wait(&full[vs.i], vs.phase) && (it < clean0 || (all_wait(&v_raw[w & 3], (w >> 2) & 1) && all_wait(&v_clean[w & 3], (w >> 2) & 1)));
+          const int last = it < n1 ? 1 : 0;   // the last tile that uses V(it)
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              tc::mma_ta(tmem + 256 + D * x, tmem + Pl::p_at(x) + 8 * k, vt + (k * 2048 >> 4), id_o, (it | k) != 0);
-            tc::commit(&o_done[x]);
-            if (x == last) release(2 * it + 1);
-            if (it + 1 < nx) {
-              ok = full_wait(2 * it + 2);
-              // S(it + 1) goes over P(it), which PV(it) reads: MMAs with different accumulators have no order of their own
-              if (Pl::kOverS) ok = ok && wait(&o_done[x], it & 1);
-              if (!ok) break;
+          for (int x = 0; x < 2; ++x) {
+            const int nx = x ? n1 : n0;
+            if (!ok || it >= nx) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              ok = ok && all_wait(&p_full[2 * x + h], (done[x] + it) & 1);
               tc::fence_after();
-              scores(x, it + 1);
-              if (x == (it + 1 < n1 ? 1 : 0)) release(2 * it + 2);
+              if (ok && tc::elect()) {
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                  tc::mma_ta(tm + 256 + D * x, tm + Pl::p_at(x) + 8 * k, vt + (k * 2048 >> 4), id_o, (it | k) != 0);
+                if (h) {
+                  tc::commit(&o_done[x]);
+                  if (x == last) tc::commit(&empty[vs.i]);
+                }
+              }
+              __syncwarp();
+            }
+            if (ok && it + 1 < nx) {
+              ok = all_wait(&full[ks.i], ks.phase) && p_read(x, it + 1);
+              tc::fence_after();
+              if (ok) scores(x, it + 1);
             }
           }
         }
-        if (!ok) {   // tensor memory may be freed, and shared memory given up, once what was issued is done
-          tc::commit(drained);
-          mbar_wait_bounded(drained, 0, kWaitLimitNs);
-        }
-      } else if (warp >= 10) {
-        // -------------------------------------------------------------- V tiles that not every token sees whole
-        int bad_v = 0;
-        for (int it = clean0; it < most; ++it) {
-          const int w = it - clean0;
-          ok = __all_sync(0xffffffffu, wait(&v_raw[w & 3], (w >> 2) & 1));
+        if (!ok) break;
+        pos += 2 * most;
+        cleaned += max(0, most - clean0);
+        done[0] += n0;
+        done[1] += n1;
+      }
+      if (ok) {   // tensor memory may be freed, and shared memory given up, once what was issued is done
+        for (int j = max(0, pos - NS); j < pos; ++j) ok = ok && all_wait(&empty[j % NS], (j / NS) & 1);
+        for (int x = 0; x < 2; ++x)
+          if (q_used[x]) ok = ok && all_wait(&q_empty[x], (q_used[x] - 1) & 1);
+      }
+      if (!ok) {
+        if (tc::elect()) tc::commit(drained);
+        __syncwarp();
+        mbar_wait_bounded(drained, 0, kWaitLimitNs);
+      }
+    } else {
+      // ---------------------------------------------------------------- V tiles that not every token sees whole
+      for (int pk = 0; get_pair(pk); ++pk) {
+        const int most = max(n_keys(0), n_keys(1)), clean0 = masked_from(pair.t0);
+        int any_bad = 0;
+        for (int it = clean0; it < most; ++it, ++cleaned) {
+          ok = __all_sync(0xffffffffu, wait(&v_raw[cleaned & 3], (cleaned >> 2) & 1));
           if (!ok) break;
-          uint8_t* vt = ring + (2 * it + 1) % NS * Pl::kTile;
+          uint8_t* vt = ring + (pos + 2 * it + 1) % NS * Pl::kTile;
 #pragma unroll 4
           for (int e = tid - 320; e < Pl::kTile / 16; e += 64) {
             const int j = it * kKeys + (e >> 3) % kKeys;   // (the swizzle keeps a row's 128 bytes together)
             uint4* at = reinterpret_cast<uint4*>(vt) + e;
-            if (j >= n) {
+            if (j >= pair.n) {
               *at = make_uint4(0u, 0u, 0u, 0u);
-            } else if (j > t0 && a.causal) {
+            } else if (j > pair.t0 && a.causal) {
               // an exponent of all ones carries into its sign's place
               constexpr uint32_t ones = BF ? 0x7F807F80u : 0x7C007C00u, unit = BF ? 0x00800080u : 0x04000400u;
               uint4 y = *at;
@@ -468,23 +571,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                   yw[k] &= ~((c >> 15) * 0xFFFFu);
                 }
                 *at = y;
-                bad_v = 1;
+                any_bad = 1;
               }
             }
           }
-          if (bad_v) found[3] = 1;
+          if (any_bad) bad_v[pk & 1] = 1;
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&v_clean[w & 3]);
+          if (lane == 0) mbar_arrive(&v_clean[cleaned & 3]);
         }
+        if (!ok) break;
+        pos += 2 * most;
+        give_pair_back(pk);
       }
     }
-    if (!ok && lane == 0) atomicOr(a.status, KVQ_STATUS_TIMEOUT);
+  }
+  if (!ok && lane == 0) {
+    *stop = 1;
+    atomicOr(a.status, KVQ_STATUS_TIMEOUT);
   }
   __syncthreads();
   if (warp == 9) {
     tc::fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+  if (*stop) {   // nothing that a wait gave up on is taken for a result
+    const Finder finder(a, p.tiles * p.tokens, lane);
+    for (int pk = 0;; ++pk) {
+      pair = next_pair(p, finder, pk);   // (every warp by itself)
+      if (pair.n == 0) break;
+      for (int i = warp; i < p.tiles * kM; i += kThreads / 32) {
+        const int token = pair.t0 + i / p.P, head = pair.unit * p.P + i % p.P;
+        if (token >= pair.n) continue;
+        const long long r = (long long)pair.first + token, at = r * a.out_stride + (long long)head * D;
+        for (int c = lane; c < D; c += 32)
+          if (a.out32) static_cast<float*>(a.out)[at + c] = NAN;
+          else static_cast<uint16_t*>(a.out)[at + c] = 0x7FFF;   // NaN in bf16 and fp16
+        if (a.lse && lane == 0) a.lse[r * a.Hq + head] = NAN;
+      }
+    }
   }
 }
 
@@ -499,12 +624,29 @@ static bool encode(CUtensorMap* map, const void* base, bool bf, int D, int heads
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The SMs of the current device; the kernel's shared memory is allowed once for each.
+template <int D, bool BF>
+static cudaError_t sms_of_device(int& sms) {
+  static std::mutex mutex;
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (dev < 64 && known[dev]) {
+    sms = known[dev];
+    return cudaSuccess;
+  }
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(prompt_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<D>::kSmem);
+  if (e == cudaSuccess && dev < 64) known[dev] = sms;
+  return e;
+}
+
 template <int D, bool BF>
 static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(prompt_kernel<D, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<D>::kSmem);
+  int sms = 0;
+  const cudaError_t e = sms_of_device<D, BF>(sms);
   if (e != cudaSuccess) return e;
   Launch p;
   p.a = a;
@@ -517,12 +659,12 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
     return std::min((long long)a.B * ((a.t_new + span - 1) / span), a.rows / span + a.B);
   };
   p.tiles = ctas(2) * p.units >= sms ? 2 : 1;   // one tile a CTA where two would leave SMs idle
-  const long long grid = ctas(p.tiles) * p.units;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  p.pairs = ctas(p.tiles) * p.units;
+  const unsigned grid = (unsigned)std::min<long long>(p.pairs, sms);
   if (!encode(&p.q, a.q, BF, D, a.Hq, a.rows, a.q_stride, p.P, p.tokens) || !encode(&p.k, a.k, BF, D, a.Hkv, a.rows, a.k_stride, 1, kKeys) ||
       !encode(&p.v, a.v, BF, D, a.Hkv, a.rows, a.v_stride, 1, kKeys))
     return cudaErrorInvalidValue;
-  prompt_kernel<D, BF><<<(unsigned)grid, kThreads, Plan<D>::kSmem, st>>>(p);
+  prompt_kernel<D, BF><<<grid, kThreads, Plan<D>::kSmem, st>>>(p);
   return cudaGetLastError();
 }
 

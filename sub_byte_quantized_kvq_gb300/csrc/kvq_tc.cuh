@@ -59,6 +59,13 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       "h"((unsigned short)3)
       : "memory");
 }
+// One lane of a converged warp.  Code that it alone runs may take uniform registers for what the warp knows to be the same
+// in all lanes (an MMA's descriptors).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff; selp.u32 %0, 1, 0, e; }" : "=r"(p));
+  return p != 0;
+}
 // Shared-memory address of the same location in cluster CTA `rank`.
 __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   uint32_t r;

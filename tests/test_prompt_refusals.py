@@ -65,6 +65,7 @@ def test_prompt_refusals(kvq):
         assert prompt(**bad) == kvq.KVQ_ERR_INVALID_ARG, bad
     assert prompt(cfg_of(kvq, 96)) == kvq.KVQ_ERR_UNSUPPORTED
     assert prompt(Hq=8 * 17) == kvq.KVQ_ERR_UNSUPPORTED
+    assert prompt(t_new=(1 << 21) + 1) == kvq.KVQ_ERR_UNSUPPORTED and prompt(t_new=1 << 21) == kvq.KVQ_OK
 
 
 def test_rows_of_a_tensor(kvq):
