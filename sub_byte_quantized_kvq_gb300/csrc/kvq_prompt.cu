@@ -11,12 +11,12 @@
 //   load warp     Q, K and V tiles by tiled TMA with 128-byte swizzle, straight
 //                 from the caller's rows (any row stride); K and V in one ring
 //   MMA warp      S = Q K^T (both from shared memory), O += P V with P from tensor
-//                 memory and V as it lies, [token][channel].  Tile 0's and tile
-//                 1's MMAs alternate: one's run while the other's softmax does
+//                 memory and V as it lies, [token][channel]; one tile's MMAs run
+//                 while the other's softmax does
 //   2 x 4 softmax warps, one row a thread: the row of S in registers, its maximum,
-//                 p = 2^(a - m), P into tensor memory.  m is raised only when a row
-//                 passes it by more than 2^8 (rare after the first keys); the
-//                 warp then scales O.  At the end O / l goes to global memory
+//                 p = 2^(a - m), P into tensor memory.  m is raised only when the
+//                 sums ask for it (rare after the first keys); the warp then scales
+//                 O.  At the end O / l goes to global memory
 //   2 cleaning warps  V tiles with rows that not all of the CTA's tokens see: a
 //                 weight of 0 times what may lie there (infinities, NaN, stale
 //                 memory) has to stay 0.  Rows past the sequence become zeros;
@@ -40,7 +40,6 @@ constexpr int kThreads = 384;
 // Registers a thread: the launch has 168 each; the softmax warps take what the others give up.
 constexpr int kRegsSoftmax = 208, kRegsRest = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsRest <= kThreads * 168, "setmaxnreg shares exceed what the launch has");
-constexpr float kLag = 8.f;               // log2 of how far a row's scores may pass its reference m
 constexpr float kLn2f = 0.69314718055994531f, kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -49,9 +48,10 @@ struct Plan {
   static constexpr int kBlock = kM * 128;             // of its 64 channels
   static constexpr int kStages = D == 128 ? 5 : 8;    // the ring of K and V tiles
   static constexpr int kSmem = 1024 + (2 + kStages) * kTile + 512;   // 1024: alignment slack
-  // tensor memory: S of tile x at 128 x, O at 256 + D x, P over S (D = 128) or behind O
-  static constexpr bool kOverS = D == 128;
-  static __device__ __forceinline__ uint32_t p_at(int x) { return kOverS ? 128 * x : 384 + 64 * x; }
+  // Tensor memory: S at 0 (D = 64: tile 1's at 128), P at 128 (256) + 64 x, O behind.  With D = 128 both tiles' S go
+  // through one place, in turn: that leaves P one of its own, so that S(it + 1) need not wait for the PV that reads P(it).
+  static constexpr int kS = D == 128 ? 1 : 2, kP = 128 * kS, kO = kP + 128;
+  static_assert(kO + 2 * D == 512, "tensor memory");
 };
 static_assert(Plan<128>::kSmem <= 227 * 1024, "shared memory");
 
@@ -180,21 +180,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
   uint8_t* ring = smem + 2 * Pl::kTile;
   uint64_t *q_full = reinterpret_cast<uint64_t*>(ring + NS * Pl::kTile), *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + NS,
-           *s_full = empty + NS, *p_full = s_full + 2, *o_done = p_full + 4, *v_raw = o_done + 2, *v_clean = v_raw + 4,
+           *s_full = empty + NS, *s_read = s_full + 2, *p_full = s_read + 2, *h_done = p_full + 4, *o_done = h_done + 2, *v_raw = o_done + 2, *v_clean = v_raw + 4,
            *info_full = v_clean + 4, *info_empty = info_full + 2, *drained = info_empty + 2;
   volatile int* info = reinterpret_cast<volatile int*>(drained + 1);   // [2] Pair
   volatile int* stop = info + 8;                                       // a wait gave up
   volatile int* bad_v = stop + 1;                                      // [2] pair's V has infinities or NaN that were cleaned
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1) + 11;
-  static_assert((4 + 2 * NS + 2 + 4 + 2 + 4 + 4 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
+  static_assert((4 + 2 * NS + 2 + 2 + 4 + 2 + 2 + 4 + 4 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
 
   if (warp == 8 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_read[i], 4);
       mbar_init(&p_full[2 * i], 4);
       mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&h_done[i], 1);
       mbar_init(&o_done[i], 1);
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], 11);   // softmax, MMA and cleaning warps
@@ -203,11 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
+    mbar_init(drained, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&v_raw[i], 1);
       mbar_init(&v_clean[i], 2);
     }
-    mbar_init(drained, 1);
     fence_mbar_init();
     stop[0] = bad_v[0] = bad_v[1] = 0;
   } else if (warp == 9) {
@@ -258,17 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lanes + 128 * x, to = tmem + lanes + 256 + D * x, tp = tmem + lanes + Pl::p_at(x);
+    const uint32_t ts = tmem + lanes + 128 * (x % Pl::kS), to = tmem + lanes + Pl::kO + D * x, tp = tmem + lanes + Pl::kP + 64 * x;
     const bool neg = a.scale < 0.f;
     const float f = fmaxf(fabsf(a.scale) * kLog2e, 1e-36f);   // (not 0: what is masked is -inf times it)
-    constexpr float bias = BF ? 0.f : 6.f;
+    constexpr float bias = BF ? 0.f : 6.f, kMost = BF ? 0x1p16f : 0x1p15f;   // m and the weights in log2 units: p = 2^(s f - m + bias)
     int done = 0;   // key tiles of earlier pairs
     for (int pk = 0; get_pair(pk); ++pk) {
       const int nx = n_keys(x), tx = pair.t0 + x * p.tokens;
       const int token = tx + row / p.P, mask0 = masked_from(tx);
       const int lim = a.causal ? min(pair.n, token + 1) : pair.n;
-      float m = -INFINITY;
-      uint64_t l2 = 0ull;
+      float m = token < pair.n ? -INFINITY : 0.f, l = 0.f;   // (a row past the sequence asks for nothing)
       for (int it = 0; it < nx; ++it) {
         ok = __all_sync(0xffffffffu, wait(&s_full[x], (done + it) & 1));
         if (!ok) break;
@@ -278,72 +279,82 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int c = 0; c < 4; ++c) tc::ld32_issue(ts + 32 * c, s[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::wait_ld(s[c]);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[x % Pl::kS]);   // the next S may come
+        if (it > 0) {   // PV(it - 1) reads P, and adds to O
+          ok = __all_sync(0xffffffffu, wait(&o_done[x], (done + it - 1) & 1));
+          if (!ok) break;
+          tc::fence_after();
+        }
         if (neg)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[c][j] ^= 0x80000000u;
+          for (int j = 0; j < 128; ++j) s[j / 32][j % 32] ^= 0x80000000u;
         if (it >= mask0) {
-          const int k = lim - it * kKeys;
+          const int k = lim - it * kKeys;   // keys from here on that the row sees
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * c + j >= k) s[c][j] = 0xFF800000u;
+          for (int j = 0; j < 128; ++j)
+            if (j >= k) s[j / 32][j % 32] = 0xFF800000u;
         }
-        float top[4];
+        // Half of the keys at a time, so that their PV may start.  No maximum is taken in the common path: a half whose sum
+        // passes kMost (rare after the first; whatever P could not hold is among them) raises m to its maximum, scales
+        // l and O, and is computed again.
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          top[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int j = 1; j < 31; j += 2) top[c] = fmaxf(fmaxf(top[c], __uint_as_float(s[c][j])), __uint_as_float(s[c][j + 1]));
-          top[c] = fmaxf(top[c], __uint_as_float(s[c][31]));
-        }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (it == 0) {
-          m = mx;
-        } else {
-          if (!Pl::kOverS) {   // PV(it - 1) reads P (over S, S(it) was issued after it)
-            ok = __all_sync(0xffffffffu, wait(&o_done[x], (done + it - 1) & 1));
-            if (!ok) break;
-            tc::fence_after();
-          }
-          const bool raise = (mx - m) * f > kLag;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float alpha = raise ? ex2f((m - mx) * f) : 1.f;
-            if (raise) m = mx;
-            const float2 l = unpack2(l2);
-            l2 = pack2(l.x * alpha, l.y * alpha);
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t f2 = pack2(f, f);
+          float sum;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tc::ld16(to + c, o);
+          for (bool again = false;; again = true) {
+            const float mb = m == -INFINITY ? bias : bias - m;
+            const uint64_t mb2 = pack2(mb, mb);
+            uint64_t sums = 0ull;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tc::st16(to + c, o);
+            for (int c = 2 * h; c < 2 * h + 2; ++c) {
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 2) {
+                const float2 y = unpack2(fma2(pack2u(s[c][j], s[c][j + 1]), f2, mb2));
+                const float e0 = ex2f(y.x), e1 = ex2f(y.y);
+                sums = add2(sums, pack2(e0, e1));
+                w[j / 2] = pack_p<BF>(e0, e1);
+              }
+              tc::st16(tp + 16 * c, w);
+            }
+            const float2 y = unpack2(sums);
+            sum = y.x + y.y;
+            const bool raise = sum > kMost || m == -INFINITY;
+            if (__builtin_expect(again || !__any_sync(0xffffffffu, raise), 1)) break;
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 64 * h; j < 64 * h + 64; ++j) top = fmaxf(top, __uint_as_float(s[j / 32][j % 32]));
+            const float to_m = raise ? fmaxf(m, top * f) : m;
+            const float alpha = to_m == m ? 1.f : ex2f(m - to_m);
+            m = to_m;
+            l *= alpha;
+            if (it > 0 || h > 0) {   // (before that O holds nothing; PV(it - 1) is done, of the first half's PV not yet known)
+              if (h) {
+                ok = __all_sync(0xffffffffu, wait(&h_done[x], (done + it) & 1));
+                if (!ok) break;
+                tc::fence_after();
+              }
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tc::ld16(to + c, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tc::st16(to + c, o);
+              }
             }
           }
+          if (!ok) break;
+          l += sum;
+          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
         }
-        const float mb = m == -INFINITY ? bias : bias - m * f;
-        const uint64_t f2 = pack2(f, f), mb2 = pack2(mb, mb);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 y = unpack2(fma2(pack2u(s[c][j], s[c][j + 1]), f2, mb2));
-            const float e0 = ex2f(y.x), e1 = ex2f(y.y);
-            l2 = add2(l2, pack2(e0, e1));
-            w[j / 2] = pack_p<BF>(e0, e1);
-          }
-          tc::st16(tp + 16 * c, w);
-          if (c & 1) {   // half of the keys: their PV may start
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * x + (c >> 1)]);
-          }
-        }
+        if (!ok) break;
       }
       if (!ok) break;
       if (nx > 0) {
@@ -352,8 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         ok = __all_sync(0xffffffffu, wait(&o_done[x], (done - 1) & 1));
         if (!ok) break;
         tc::fence_after();
-        const float2 lp = unpack2(l2);
-        const float l = lp.x + lp.y, inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool live = token < pair.n, patch = bad_v[pk & 1] != 0;
         const long long r = (long long)pair.first + token;
         const int head = pair.unit * p.P + row % p.P;
@@ -387,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           __syncwarp();
         }
-        if (a.lse && live) a.lse[r * a.Hq + head] = l == 0.f ? -INFINITY : (m * f - bias + __log2f(l)) * kLn2f;
+        if (a.lse && live) a.lse[r * a.Hq + head] = l == 0.f ? -INFINITY : (m - bias + __log2f(l)) * kLn2f;
         tc::fence_before();
       }
       give_pair_back(pk);
@@ -458,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                      vd = tc::desc_sw128_mn(smem_u32(ring), Pl::kBlock);
       // The whole warp goes along, and one lane of it (elect.sync) issues: the operands are then known to be the same in
       // all lanes.  Issued by one thread in a branch of its own, each MMA took 130 cycles instead of the 64 of its math.
-      int done[2] = {0, 0}, q_used[2] = {0, 0};   // key tiles of earlier pairs, pairs with a tile x
+      int done[2] = {0, 0}, q_used[2] = {0, 0}, issued[2] = {0, 0};   // key tiles of earlier pairs, pairs with a tile x, S of a place
       Place ks{0, 0};                             // where the next K tile lies
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto all_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
@@ -467,61 +477,102 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         pair.n = __shfl_sync(0xffffffffu, pair.n, 0);
         pair.t0 = __shfl_sync(0xffffffffu, pair.t0, 0);
         const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1), clean0 = masked_from(pair.t0);
-        auto scores = [&](int x, int it) {   // (K(it) at place `ks` of the ring)
-          const uint64_t kt = kd + (ks.i * Pl::kTile >> 4), qt = qd + (x * Pl::kTile >> 4);
+        // What a block waits for is looked at where the block before it still runs: behind the two halves of a PV (its MMAs are
+        // queued), and among the MMAs of an S (the issue of these goes with their execution).
+        bool p_known = false;   // the next PV's first half has its P
+        auto await = [&](bool at_all, uint64_t* bar, int parity) { ok = ok && (!at_all || all_wait(bar, parity)); };
+        // S(it) of tile x, K(it) at place `ks` of the ring, once the last S in its place of tensor memory is read; y: the tile whose
+        // PV comes next
+        auto scores = [&](int x, int it, int y, bool y_has, int y_parity) {
+          const int place = x % Pl::kS;
+          await(issued[place] > 0, &s_read[place], (issued[place] - 1) & 1);
+          ++issued[place];
+          tc::fence_after();
+          const uint64_t kt = kd + (__shfl_sync(0xffffffffu, ks.i, 0) * Pl::kTile >> 4), qt = qd + (x * Pl::kTile >> 4);
           const bool last = it + 1 == (x ? n1 : n0), frees = x == (it < n1 ? 1 : 0);   // of the queries' uses; of K(it)'s
-          if (tc::elect()) {
+          auto part = [&](int k) {
+            const uint32_t at = ((k >> 2) * Pl::kBlock + (k & 3) * 32) >> 4;
+            tc::mma(tm + 128 * place, qt + at, kt + at, id_s, k != 0);
+          };
+          if (ok && tc::elect()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t at = ((k >> 2) * Pl::kBlock + (k & 3) * 32) >> 4;
-              tc::mma(tm + 128 * x, qt + at, kt + at, id_s, k != 0);
-            }
+            for (int k = 0; k < D / 16 - 1; ++k) part(k);
+          }
+          __syncwarp();
+          p_known = y_has && __all_sync(0xffffffffu, mbar_test(&p_full[2 * y], y_parity));
+          if (ok && tc::elect()) {
+            part(D / 16 - 1);
             tc::commit(&s_full[x]);
             if (last) tc::commit(&q_empty[x]);
             if (frees) tc::commit(&empty[ks.i]);
           }
           __syncwarp();
         };
-        // S goes over the P before it, which PV reads: MMAs with different accumulators have no order of their own
-        auto p_read = [&](int x, int it) { return !Pl::kOverS || done[x] + it == 0 || all_wait(&o_done[x], (done[x] + it - 1) & 1); };
+        // PV(it) of tile x, half h of the keys
+        auto values = [&](int x, int h, int it, const Place& vs) {
+          await(h || !p_known, &p_full[2 * x + h], (done[x] + it) & 1);
+          tc::fence_after();
+          const uint64_t vt = vd + (__shfl_sync(0xffffffffu, vs.i, 0) * Pl::kTile >> 4);
+          const bool frees = x == (it < n1 ? 1 : 0);   // the last use of V(it)
+          if (ok && tc::elect()) {
+#pragma unroll
+            for (int k = 4 * h; k < 4 * h + 4; ++k)
+              tc::mma_ta(tm + Pl::kO + D * x, tm + Pl::kP + 64 * x + 8 * k, vt + (k * 2048 >> 4), id_o, (it | k) != 0);
+            tc::commit(h ? &o_done[x] : &h_done[x]);
+            if (h && frees) tc::commit(&empty[vs.i]);
+          }
+          __syncwarp();
+          p_known = false;
+        };
+        auto await_v = [&](int it, const Place& vs) {
+          const int w = cleaned + it - clean0;
+          await(true, &full[vs.i], vs.phase);
+          await(it >= clean0, &v_raw[w & 3], (w >> 2) & 1);
+          await(it >= clean0, &v_clean[w & 3], (w >> 2) & 1);
+        };
+        await(true, &full[ks.i], ks.phase);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (ok && (x ? n1 : n0)) {
-            ok = all_wait(&q_full[x], q_used[x] & 1) && all_wait(&full[ks.i], ks.phase) && p_read(x, 0);
+          if (x ? n1 : n0) {
+            await(true, &q_full[x], q_used[x] & 1);
             ++q_used[x];
-            tc::fence_after();
-            if (ok) scores(x, 0);
+            scores(x, 0, x, false, 0);
           }
-        for (int it = 0; it < most && ok; ++it) {
-          const int w = cleaned + it - clean0;
-          const Place vs = ks.next();   // V(it)'s
-          const uint64_t vt = vd + (vs.i * Pl::kTile >> 4);
-          ks = vs.next();               // K(it + 1)'s
-          ok = all_wait(&full[vs.i], vs.phase) && (it < clean0 || (all_wait(&v_raw[w & 3], (w >> 2) & 1) && all_wait(&v_clean[w & 3], (w >> 2) & 1)));
-          const int last = it < n1 ? 1 : 0;   // the last tile that uses V(it)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int nx = x ? n1 : n0;
-            if (!ok || it >= nx) continue;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              ok = ok && all_wait(&p_full[2 * x + h], (done[x] + it) & 1);
-              tc::fence_after();
-              if (ok && tc::elect()) {
-#pragma unroll
-                for (int k = 4 * h; k < 4 * h + 4; ++k)
-                  tc::mma_ta(tm + 256 + D * x, tm + Pl::p_at(x) + 8 * k, vt + (k * 2048 >> 4), id_o, (it | k) != 0);
-                if (h) {
-                  tc::commit(&o_done[x]);
-                  if (x == last) tc::commit(&empty[vs.i]);
-                }
-              }
-              __syncwarp();
+        Place vs = ks.next();   // V(it)'s
+        await_v(0, vs);
+        ks = vs.next();         // K(it + 1)'s
+        if (n1 > 0) {
+          for (int it = 0; it < n1 && ok; ++it) {
+            const bool more0 = it + 1 < n0, more1 = it + 1 < n1;
+            if (it < n0) {
+              values(0, 0, it, vs);
+              await(more0, &full[ks.i], ks.phase);
+              values(0, 1, it, vs);
             }
-            if (ok && it + 1 < nx) {
-              ok = all_wait(&full[ks.i], ks.phase) && p_read(x, it + 1);
-              tc::fence_after();
-              if (ok) scores(x, it + 1);
+            if (more0) scores(0, it + 1, 1, true, (done[1] + it) & 1);
+            values(1, 0, it, vs);
+            const Place next = ks.next();
+            await(more1 && !more0, &full[ks.i], ks.phase);
+            values(1, 1, it, vs);
+            if (more1) {
+              await_v(it + 1, next);
+              scores(1, it + 1, 0, more0, (done[0] + it + 1) & 1);
+              vs = next;
+              ks = vs.next();
+            }
+          }
+        } else {   // a tile alone: its S beside its softmax
+          for (int it = 0; it < n0 && ok; ++it) {
+            const bool more = it + 1 < n0;
+            await(more, &full[ks.i], ks.phase);
+            if (more) scores(0, it + 1, 0, false, 0);
+            values(0, 0, it, vs);
+            const Place next = ks.next();
+            if (more) await_v(it + 1, next);
+            values(0, 1, it, vs);
+            if (more) {
+              vs = next;
+              ks = vs.next();
             }
           }
         }
@@ -550,31 +601,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           ok = __all_sync(0xffffffffu, wait(&v_raw[cleaned & 3], (cleaned >> 2) & 1));
           if (!ok) break;
           uint8_t* vt = ring + (pos + 2 * it + 1) % NS * Pl::kTile;
+          const int whole = max(0, (a.causal ? min(pair.t0 + 1, pair.n) : pair.n) - it * kKeys);   // rows before it: every token sees them
+          for (int c = 0; c < KC; ++c)
 #pragma unroll 4
-          for (int e = tid - 320; e < Pl::kTile / 16; e += 64) {
-            const int j = it * kKeys + (e >> 3) % kKeys;   // (the swizzle keeps a row's 128 bytes together)
-            uint4* at = reinterpret_cast<uint4*>(vt) + e;
-            if (j >= pair.n) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-            } else if (j > pair.t0 && a.causal) {
-              // an exponent of all ones carries into its sign's place
-              constexpr uint32_t ones = BF ? 0x7F807F80u : 0x7C007C00u, unit = BF ? 0x00800080u : 0x04000400u;
-              uint4 y = *at;
-              uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-              uint32_t any = 0u;
+            for (int e = 8 * whole + (tid - 320); e < 8 * kKeys; e += 64) {   // (the swizzle keeps a row's 128 bytes together)
+              uint4* at = reinterpret_cast<uint4*>(vt + c * Pl::kBlock) + e;
+              if (it * kKeys + (e >> 3) >= pair.n) {
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                // an exponent of all ones carries into its sign's place
+                constexpr uint32_t ones = BF ? 0x7F807F80u : 0x7C007C00u, unit = BF ? 0x00800080u : 0x04000400u;
+                uint4 y = *at;
+                uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+                uint32_t any = 0u;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) any |= (yw[k] & ones) + unit;
-              if (__builtin_expect(any & 0x80008000u, 0)) {
+                for (int k = 0; k < 4; ++k) any |= (yw[k] & ones) + unit;
+                if (__builtin_expect(any & 0x80008000u, 0)) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t c = ((yw[k] & ones) + unit) & 0x80008000u;   // 0x8000 in the halves to clear
-                  yw[k] &= ~((c >> 15) * 0xFFFFu);
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t z = ((yw[k] & ones) + unit) & 0x80008000u;   // 0x8000 in the halves to clear
+                    yw[k] &= ~((z >> 15) * 0xFFFFu);
+                  }
+                  *at = y;
+                  any_bad = 1;
                 }
-                *at = y;
-                any_bad = 1;
               }
             }
-          }
           if (any_bad) bad_v[pk & 1] = 1;
           fence_proxy_async();
           __syncwarp();
