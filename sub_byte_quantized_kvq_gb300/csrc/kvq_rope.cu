@@ -18,6 +18,7 @@
 // 32 / (D / 16) heads a step and shares the sines and cosines of its row, each
 // computed by one lane.
 #include <algorithm>
+#include <atomic>
 
 #include "kvq_prompt.cuh"
 
@@ -216,11 +217,24 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
   }
 }
 
+// The SMs of the current device (looked up once for each).
+static cudaError_t sms_of_device(int& sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (sms == 0) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  }
+  return e;
+}
+
 template <int D, int IN, int OUT>
 static cudaError_t launch(const NormRopeArgs& a, cudaStream_t st) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t e = sms_of_device(sms);
   if (e != cudaSuccess) return e;
   constexpr int HPW = 32 / (D / 16);
   const int groups = (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW;

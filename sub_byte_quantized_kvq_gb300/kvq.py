@@ -515,19 +515,23 @@ def kvq_evict_pages(cache: QuantizedKVCache, mass: torch.Tensor, keep_pages: int
 def _token_rows(t: torch.Tensor, heads: int, D: int):
     """(rows, elements from a row to the next) of a tensor [..., heads, D] whose last two dimensions are
     dense and whose others step evenly: a contiguous tensor, or a part of one projection's rows."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) < 3 or shape[-2:] != (heads, D):
+    shape = t.shape
+    if len(shape) < 3 or shape[-1] != D or shape[-2] != heads:
         raise ValueError(f"a tensor of shape {tuple(shape)} where [..., {heads}, {D}] is wanted")
+    if t.is_contiguous():
+        return t.numel() // (heads * D), heads * D
+    strides = t.stride()
     rows, step = 1, None
-    for n, s in zip(reversed(shape[:-2]), reversed(strides[:-2])):
+    for i in range(len(shape) - 3, -1, -1):
+        n = shape[i]
         if n != 1:
             if step is None:
-                step = s
-            elif s != step * rows:
-                raise ValueError(f"rows of a tensor with strides {tuple(strides)} are not evenly spaced")
-        rows *= n
-    if rows and (strides[-1] != 1 or (heads > 1 and strides[-2] != D)):
-        raise ValueError(f"a tensor with strides {tuple(strides)}: the heads of a row have to be contiguous")
+                step = strides[i]
+            elif strides[i] != step * rows:
+                raise ValueError(f"rows of a tensor with strides {strides} are not evenly spaced")
+            rows *= n
+    if strides[-1] != 1 or (heads > 1 and strides[-2] != D):
+        raise ValueError(f"a tensor with strides {strides}: the heads of a row have to be contiguous")
     return rows, heads * D if step is None else step
 
 
@@ -541,57 +545,65 @@ def kvq_norm_rope(cache: QuantizedKVCache, q: torch.Tensor | None, k: torch.Tens
     inv_freq: fp32 [rot_dim / 2] (None: norms alone).  q_weight, k_weight: fp32 [D] gains (None: ones).  The outputs
     may be the inputs."""
     cfg, (pcfg, _, index) = cache.cfg, _refs(cache)
-    D, f32 = cfg.head_dim, torch.float32
-    x = q if q is not None else k
-    if x is None or (q is not None and k is not None and q.dtype is not k.dtype):
-        raise ValueError("q or k, of one type, is wanted")
-    Hq = q.shape[-2] if q is not None else 0
-    given = [out for src, out in ((q, q_out), (k, k_out)) if src is not None and out is not None]
+    D, Hkv = cfg.head_dim, cfg.num_kv_heads
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("q or k is wanted")
+    dtype = x.dtype
     if out_dtype is None:
-        out_dtype = given[0].dtype if given else x.dtype
-    if any(t.dtype is not out_dtype for t in given):
-        raise ValueError("q_out and k_out have to be of one type, out_dtype")
-    args, rows = [], None
-    for src, out, heads in ((q, q_out, Hq), (k, k_out, cfg.num_kv_heads)):
-        if src is None:
-            args.append((None, 0, None, None, 0))
-            continue
-        n, step = _token_rows(src, heads, D)
-        if rows not in (None, n):
-            raise ValueError(f"{rows} rows of q and {n} of k")
+        out_dtype = q_out.dtype if q_out is not None else k_out.dtype if k_out is not None else dtype
+    Hq = rows = qp = qs = qop = qos = kp = ks = kop = kos = 0
+    if q is None:
+        q_out = None
+    else:
+        Hq = q.shape[-2]
+        rows, qs = _token_rows(q, Hq, D)
+        if q_out is None:
+            q_out = _made_on(stream, lambda: torch.empty(q.shape, dtype=out_dtype, device=q.device), returned=True)
+        n, qos = _token_rows(q_out, Hq, D)
+        if n != rows or q_out.dtype is not out_dtype:
+            raise ValueError(f"q_out: {n} rows of {q_out.dtype} for {rows} of {out_dtype}")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    if k is None:
+        k_out = None
+    else:
+        n, ks = _token_rows(k, Hkv, D)
+        if k.dtype is not dtype or (q is not None and n != rows):
+            raise ValueError(f"k: {n} rows of {k.dtype} beside {rows} of {dtype}")
         rows = n
-        if out is None:
-            shape = src.shape
-            out = _made_on(stream, lambda: torch.empty(shape, dtype=out_dtype, device=src.device), returned=True)
-        m, out_step = _token_rows(out, heads, D)
-        if m != n:
-            raise ValueError(f"{n} rows in, {m} out")
-        args.append((src.data_ptr(), step, out, out.data_ptr(), out_step))
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    axes = 1
-    if rot:
-        assert inv_freq.dtype is f32 and inv_freq.is_contiguous() and inv_freq.dim() == 1
+        if k_out is None:
+            k_out = _made_on(stream, lambda: torch.empty(k.shape, dtype=out_dtype, device=k.device), returned=True)
+        n, kos = _token_rows(k_out, Hkv, D)
+        if n != rows or k_out.dtype is not out_dtype:
+            raise ValueError(f"k_out: {n} rows of {k_out.dtype} for {rows} of {out_dtype}")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    rot, axes, pp, fp, pairs = 0, 1, None, None, None
+    if inv_freq is not None:
+        assert inv_freq.dtype is torch.float32 and inv_freq.dim() == 1 and inv_freq.is_contiguous()
         assert positions is not None and positions.dtype is torch.int32 and positions.is_contiguous()
-        axes = positions.shape[0] if pair_axis is not None else 1
+        rot, pp, fp = 2 * inv_freq.numel(), positions.data_ptr(), inv_freq.data_ptr()
+        if pair_axis is not None:
+            axes = positions.shape[0]
         if positions.numel() != axes * rows:
             raise ValueError(f"{positions.numel()} positions for {rows} rows of {axes} axes")
-    for w in (q_weight, k_weight):
-        assert w is None or (w.dtype is f32 and w.is_contiguous() and w.shape == (D,))
-    pairs = None
     if pair_axis is not None:
-        pair_axis = [int(p) for p in pair_axis]
-        if len(pair_axis) != rot // 2 or any(not 0 <= p < axes for p in pair_axis):
+        if len(pair_axis) != rot // 2 or (rot and not 0 <= min(pair_axis) <= max(pair_axis) < axes):
             raise ValueError(f"pair_axis: an axis below {axes} for each of the {rot // 2} pairs")
         pairs = bytes(pair_axis)
-    if eps is not None and not eps >= 0:
+    if q_weight is not None:
+        assert q_weight.dtype is torch.float32 and q_weight.is_contiguous() and q_weight.shape == (D,)
+    if k_weight is not None:
+        assert k_weight.dtype is torch.float32 and k_weight.is_contiguous() and k_weight.shape == (D,)
+    if eps is None:
+        eps = -1.0
+    elif not eps >= 0:
         raise ValueError("eps has to be at least 0 (None: no norm)")
-    (qp, qs, qo, qop, qos), (kp, ks, ko, kop, kos) = args
-    _check_on(index, q, k, qo, ko, positions if rot else None, inv_freq, q_weight, k_weight)
+    _check_on(index, q, k, q_out, k_out, None if rot == 0 else positions, inv_freq, q_weight, k_weight)
     if rows:
-        _call("kvq_norm_rope", index, stream, pcfg, qp, qs, Hq, kp, ks, _DTYPE[x.dtype], rows, _addr(q_weight), _addr(k_weight),
-              -1.0 if eps is None else float(eps), _addr(positions) if rot else None, axes, _addr(inv_freq) if rot else None, rot,
-              pairs, int(interleaved), qop, qos, kop, kos, _DTYPE[out_dtype])
-    return qo, ko
+        _call("kvq_norm_rope", index, stream, pcfg, qp or None, qs, Hq, kp or None, ks, _DTYPE[dtype], rows, _addr(q_weight),
+              _addr(k_weight), eps, pp, axes, fp, rot, pairs, 1 if interleaved else 0, qop or None, qos, kop or None, kos,
+              _DTYPE[out_dtype])
+    return q_out, k_out
 
 
 def kvq_prompt_attention(cache: QuantizedKVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, softmax_scale: float,
@@ -604,33 +616,38 @@ def kvq_prompt_attention(cache: QuantizedKVCache, q: torch.Tensor, k: torch.Tens
     device, t_new a bound on the lengths.  lse: fp32 of q's leading shape x Hq, filled when given.  Rows of no
     sequence are left as they were (an `out` made here: uninitialised)."""
     cfg, (pcfg, _, index) = cache.cfg, _refs(cache)
-    B, Hkv, D = cfg.num_seqs, cfg.num_kv_heads, cfg.head_dim
-    Hq, packed = q.shape[-2], first_row is not None
-    if q.dtype not in (torch.bfloat16, torch.float16) or k.dtype is not q.dtype or v.dtype is not q.dtype:
+    B, D = cfg.num_seqs, cfg.head_dim
+    shape, dtype = q.shape, q.dtype
+    Hq = shape[-2]
+    code = _DTYPE[dtype]
+    if code == KVQ_F32 or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("q, k and v have to be of one type, bf16 or f16")
-    if packed:
+    if first_row is not None:
         if t_per_seq is None or t_new is None:
             raise ValueError("packed sequences: t_per_seq and t_new are wanted")
-        assert q.dim() == 3 and first_row.dtype is torch.int32 and first_row.is_contiguous() and first_row.shape == (B,)
+        assert len(shape) == 3 and first_row.dtype is torch.int32 and first_row.is_contiguous() and first_row.shape == (B,)
     else:
-        assert q.dim() == 4 and q.shape[0] == B and t_new in (None, q.shape[1])
-        t_new = q.shape[1]
-    assert k.shape == q.shape[:-2] + (Hkv, D) and v.shape == k.shape
+        assert len(shape) == 4 and shape[0] == B and t_new in (None, shape[1])
+        t_new = shape[1]
     if t_per_seq is not None:
         assert t_per_seq.dtype is torch.int32 and t_per_seq.is_contiguous() and t_per_seq.shape == (B,)
-    (rows, qs), (_, ks), (_, vs) = _token_rows(q, Hq, D), _token_rows(k, Hkv, D), _token_rows(v, Hkv, D)
+    rows, qs = _token_rows(q, Hq, D)
+    _, ks = _token_rows(k, cfg.num_kv_heads, D)
+    _, vs = _token_rows(v, cfg.num_kv_heads, D)
     if out is None:
-        shape, made = q.shape, out_dtype or q.dtype
+        made = out_dtype or dtype
         out = _made_on(stream, lambda: torch.empty(shape, dtype=made, device=q.device), returned=True)
-    assert out.shape == q.shape and out.dtype in (q.dtype, torch.float32) and out_dtype in (None, out.dtype)
+    od = out.dtype
+    assert k.shape[:-2] == shape[:-2] and v.shape[:-2] == shape[:-2] and out.shape == shape
+    assert (od is dtype or od is torch.float32) and out_dtype in (None, od)
     _, outs = _token_rows(out, Hq, D)
     if lse is not None:
-        assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.shape == q.shape[:-1]
+        assert lse.dtype is torch.float32 and lse.is_contiguous() and lse.shape == shape[:-1]
     _check_on(index, q, k, v, t_per_seq, first_row, out, lse)
     if rows:
-        _call("kvq_prompt_attention", index, stream, pcfg, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPE[q.dtype], Hq,
-              rows, _addr(first_row), _addr(t_per_seq), t_new, float(softmax_scale), int(causal), out.data_ptr(), outs,
-              _DTYPE[out.dtype], _addr(lse), cache.status.data_ptr())
+        _call("kvq_prompt_attention", index, stream, pcfg, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, Hq, rows,
+              _addr(first_row), _addr(t_per_seq), t_new, softmax_scale, 1 if causal else 0, out.data_ptr(), outs, _DTYPE[od],
+              _addr(lse), cache.status.data_ptr())
     return out
 
 
