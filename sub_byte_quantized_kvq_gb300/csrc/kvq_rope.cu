@@ -68,7 +68,7 @@ __device__ __forceinline__ void pack8(const float* x, uint32_t (&u)[Elem<DT>::kW
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&u)[N], const uint8_t* p) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(u + i) = *reinterpret_cast<const uint4*>(p + 4 * i);
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(u + i) = __ldcs(reinterpret_cast<const uint4*>(p + 4 * i));   // (read once)
 }
 template <int N>
 __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&u)[N]) {
@@ -95,10 +95,16 @@ __device__ __forceinline__ void turn_sincos(int pos, uint64_t per, float& s, flo
   if ((quad + 1) & 2) c = -c;
 }
 
-// Item (row, g) is 32 / (D / 16) heads of one row: q's groups first, then k's.  A warp takes every S-th group of
-// its rows; the next item's loads are in flight while one is computed.
+// CTAs an SM: by the registers that keep the common types from spilling.
+template <int IN>
+constexpr int rope_ctas() { return IN == KVQ_F32 ? 3 : 4; }
+
+// Item (row, g) is 32 / (D / 16) heads of one row: q's groups first, then k's.  A warp takes whole rows, as many as every
+// warp can have, then a run of the items of the rows that are left; the next item's loads are in flight while one is
+// computed.  (7777 rows of 10 items, 4864 warps: 33 us, or 38 with whole rows alone; 131072 rows: 410 us, or 429 where a
+// warp's rows lie behind one another.)
 template <int D, int IN, int OUT>
-__global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int S) {
+__global__ void __launch_bounds__(32 * kRopeWarps, rope_ctas<IN>()) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, PER = 8 / HPW;   // lanes a head, heads a step, pairs whose phase a lane computes
   constexpr int EI = IN == KVQ_F32 ? 4 : 2, EO = OUT == KVQ_F32 ? 4 : 2;
   __shared__ __align__(16) float gain[2][D];
@@ -121,8 +127,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
   }
   __syncthreads();
   const int gq = (a.heads[0] + HPW - 1) / HPW, groups = gq + (a.heads[1] + HPW - 1) / HPW;
-  const long long warps = (long long)gridDim.x * kRopeWarps, w = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-  const int g0 = (int)(w % S);
+  const int warps = gridDim.x * kRopeWarps, w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const int rounds = a.rows / warps;                                   // rows of each warp
+  const int over = a.rows - rounds * warps;                            // rows that are left, and their items
+  const long long rest = (long long)over * groups, run = (rest + warps - 1) / warps, run0 = min(w * run, rest);
+  long long left = (long long)rounds * groups + min(run, rest - run0);   // items of this warp
   uint32_t u0[Elem<IN>::kWords], u1[Elem<IN>::kWords];
   int h = 0, role = 0;
   auto place = [&](int g, int& r, int& head) {
@@ -130,18 +139,19 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
     head = (g - (r ? gq : 0)) * HPW + hg;
     return head < a.heads[r];
   };
-  auto fetch = [&](long long row, int g) {
+  auto fetch = [&](int row, int g) {
     if (place(g, role, h)) {
       const uint8_t* p = static_cast<const uint8_t*>(a.in[role]) + (row * a.in_stride[role] + (long long)h * D) * EI;
       load_words(u0, p + 8 * EI * c0);
       load_words(u1, p + 8 * EI * c1);
     }
   };
-  long long row = w / S;
-  const long long step = warps / S;
-  if (g0 >= groups || row >= a.rows || w >= step * S) return;
-  fetch(row, g0);
-  for (; row < a.rows; row += step) {
+  if (left == 0) return;
+  const int run_row = rounds * warps + (int)(run0 / groups), run_g = (int)(run0 % groups);
+  int row = rounds > 0 ? w : run_row, g = rounds > 0 ? 0 : run_g;
+  auto next_row = [&]() { return row >= (rounds - 1) * warps ? (row >= rounds * warps ? row + 1 : run_row) : row + warps; };
+  fetch(row, g);
+  while (true) {
     float cs[8], sn[8];
     {
       float s[PER], c[PER];
@@ -157,14 +167,17 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
         cs[j] = __shfl_sync(0xffffffffu, c[j % PER], j / PER * LPH + l);
       }
     }
-    for (int g = g0; g < groups; g += S) {
+    for (; g < groups; ++g) {
       float x[8], y[8];
       unpack8<IN>(u0, x);
       unpack8<IN>(u1, y);
       int r, head;
       const bool live = place(g, r, head);
-      if (g + S < groups) fetch(row, g + S);
-      else if (row + step < a.rows) fetch(row + step, g0);
+      const bool more = --left > 0;
+      if (more) {
+        if (g + 1 < groups) fetch(row, g + 1);
+        else fetch(next_row(), row >= (rounds - 1) * warps && row < rounds * warps ? run_g : 0);
+      }
       if (norm) {
         float ss = 0.f;
 #pragma unroll
@@ -213,7 +226,10 @@ __global__ void __launch_bounds__(32 * kRopeWarps) norm_rope_kernel(const __grid
         pack8<OUT>(y, o);
         store_words(p + 8 * EO * c1, o);
       }
+      if (!more) return;
     }
+    g = row >= (rounds - 1) * warps && row < rounds * warps ? run_g : 0;
+    row = next_row();
   }
 }
 
@@ -238,11 +254,8 @@ static cudaError_t launch(const NormRopeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   constexpr int HPW = 32 / (D / 16);
   const int groups = (a.heads[0] + HPW - 1) / HPW + (a.heads[1] + HPW - 1) / HPW;
-  // a row to a warp where there are rows enough for every SM's resident warps, else a row's heads over several
-  const long long slots = (long long)sms * 4 * kRopeWarps;
-  const int S = (int)std::min<long long>(groups, std::max<long long>(1, slots / a.rows));
-  const long long ctas = std::min<long long>(((long long)a.rows * S + kRopeWarps - 1) / kRopeWarps, slots / kRopeWarps);
-  norm_rope_kernel<D, IN, OUT><<<(unsigned)ctas, 32 * kRopeWarps, 0, st>>>(a, S);
+  const long long items = (long long)a.rows * groups, ctas = std::min<long long>((items + kRopeWarps - 1) / kRopeWarps, sms * rope_ctas<IN>());
+  norm_rope_kernel<D, IN, OUT><<<(unsigned)ctas, 32 * kRopeWarps, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <int D, int IN>
