@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     int done = 0;   // key tiles of earlier pairs
     for (int pk = 0; get_pair(pk); ++pk) {
       const int nx = n_keys(x), tx = pair.t0 + x * p.tokens;
+      const bool alone = n_keys(1) == 0;
       const int token = tx + row / p.P, mask0 = masked_from(tx);
       const int lim = a.causal ? min(pair.n, token + 1) : pair.n;
       float m = token < pair.n ? -INFINITY : 0.f, l = 0.f;   // (a row past the sequence asks for nothing)
@@ -282,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_read[x % Pl::kS]);   // the next S may come
-        if (it > 0) {   // PV(it - 1) reads P, and adds to O
+        // PV(it - 1) reads P, and adds to O: where it was issued before S(it), S's commit says that it is done
+        if (alone && it > 0) {
           ok = __all_sync(0xffffffffu, wait(&o_done[x], (done + it - 1) & 1));
           if (!ok) break;
           tc::fence_after();
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_arrive(&info_full[pk & 1]);
           }
           const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1), clean0 = masked_from(pair.t0), head0 = pair.unit * p.P;
+          uint64_t* v_bar = nullptr;
           for (int i = 0; ok && pair.n > 0 && i < 2 * most; ++i) {
             if (i == 0 || i == 1) {   // the tiles' queries: tile 0's before the first keys, tile 1's behind them
               if (i ? n1 : n0) {
@@ -437,15 +440,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const int st = pos % NS;
             if (pos >= NS) ok = wait(&empty[st], (pos / NS - 1) & 1);
             if (!ok) break;
-            // a V tile that is cleaned lands on a barrier of its own (the ring holds at most four), so that the cleaning warps
-            // see each of its phases
+            // K(0) has its place's barrier; V(it) and K(it + 1) land on V's together.  A V tile that is cleaned lands on a
+            // barrier of its own (the ring holds at most four), so that the cleaning warps see each of its phases
             const bool raw = (i & 1) && (i >> 1) >= clean0;
-            uint64_t* bar = raw ? &v_raw[cleaned & 3] : &full[st];
-            if (raw) {
-              mbar_arrive(&full[st]);
-              ++cleaned;
+            if (i & 1) {
+              v_bar = &full[st];
+              const int with = (raw ? 0 : Pl::kTile) + (i + 1 < 2 * most ? Pl::kTile : 0);
+              if (with) mbar_arrive_expect_tx(v_bar, with);
+              else mbar_arrive(v_bar);
+            } else {
+              if (i == 0) mbar_arrive_expect_tx(&full[st], Pl::kTile);
+              else mbar_arrive(&full[st]);
             }
-            mbar_arrive_expect_tx(bar, Pl::kTile);
+            uint64_t* bar = raw ? &v_raw[cleaned & 3] : i == 0 ? &full[st] : v_bar;
+            if (raw) {
+              ++cleaned;
+              mbar_arrive_expect_tx(bar, Pl::kTile);
+            }
             for (int c = 0; c < KC; ++c)
               tc::tma3d(ring + st * Pl::kTile + c * Pl::kBlock, i & 1 ? &p.v : &p.k, 64 * c, head0 / a.G, pair.first + (i >> 1) * kKeys, bar);
             ++pos;
@@ -477,15 +488,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         pair.n = __shfl_sync(0xffffffffu, pair.n, 0);
         pair.t0 = __shfl_sync(0xffffffffu, pair.t0, 0);
         const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1), clean0 = masked_from(pair.t0);
-        // What a block waits for is looked at where the block before it still runs: behind the two halves of a PV (its MMAs are
-        // queued), and among the MMAs of an S (the issue of these goes with their execution).
-        bool p_known = false;   // the next PV's first half has its P
+        // The tensor cores run dry where the warp looks at a barrier before each block (about 100 cycles, ready or not), so it
+        // looks at two at a time, behind MMAs that are queued or among those of an S: `ahead` says that they are ready.
         auto await = [&](bool at_all, uint64_t* bar, int parity) { ok = ok && (!at_all || all_wait(bar, parity)); };
-        // S(it) of tile x, K(it) at place `ks` of the ring, once the last S in its place of tensor memory is read; y: the tile whose
-        // PV comes next
+        auto test = [&](uint64_t* bar, int parity) { return mbar_test(bar, parity); };
+        auto place_read = [&](int x) { return &s_read[x % Pl::kS]; };
+        auto place_parity = [&](int x) { return (issued[x % Pl::kS] - 1) & 1; };
+        // S(it) of tile x, K(it) at place `ks` of the ring (the last S in its place of tensor memory is read); y: the tile whose PV
+        // comes next.  Returns whether that PV has the first half of its P.
         auto scores = [&](int x, int it, int y, bool y_has, int y_parity) {
           const int place = x % Pl::kS;
-          await(issued[place] > 0, &s_read[place], (issued[place] - 1) & 1);
           ++issued[place];
           tc::fence_after();
           const uint64_t kt = kd + (__shfl_sync(0xffffffffu, ks.i, 0) * Pl::kTile >> 4), qt = qd + (x * Pl::kTile >> 4);
@@ -499,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int k = 0; k < D / 16 - 1; ++k) part(k);
           }
           __syncwarp();
-          p_known = y_has && __all_sync(0xffffffffu, mbar_test(&p_full[2 * y], y_parity));
+          const bool ahead = y_has && __all_sync(0xffffffffu, test(&p_full[2 * y], y_parity));
           if (ok && tc::elect()) {
             part(D / 16 - 1);
             tc::commit(&s_full[x]);
@@ -507,10 +519,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (frees) tc::commit(&empty[ks.i]);
           }
           __syncwarp();
+          return ahead;
         };
-        // PV(it) of tile x, half h of the keys
-        auto values = [&](int x, int h, int it, const Place& vs) {
-          await(h || !p_known, &p_full[2 * x + h], (done[x] + it) & 1);
+        auto half = [&](int x, int h, int it, const Place& vs) {   // PV(it) of tile x, half h of the keys (its P is there)
           tc::fence_after();
           const uint64_t vt = vd + (__shfl_sync(0xffffffffu, vs.i, 0) * Pl::kTile >> 4);
           const bool frees = x == (it < n1 ? 1 : 0);   // the last use of V(it)
@@ -522,19 +533,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (h && frees) tc::commit(&empty[vs.i]);
           }
           __syncwarp();
-          p_known = false;
         };
-        auto await_v = [&](int it, const Place& vs) {
-          const int w = cleaned + it - clean0;
+        // PV(it) of tile x; then (more) its place of S is known to be read
+        auto values = [&](int x, int it, const Place& vs, bool ahead, bool more) {
+          const int parity = (done[x] + it) & 1;
+          await(!ahead, &p_full[2 * x], parity);
+          half(x, 0, it, vs);
+          const bool h1 = test(&p_full[2 * x + 1], parity);
+          ahead = __all_sync(0xffffffffu, h1 && (!more || test(place_read(x), place_parity(x))));
+          await(!ahead, &p_full[2 * x + 1], parity);
+          half(x, 1, it, vs);
+          await(!ahead && more, place_read(x), place_parity(x));
+        };
+        auto await_v = [&](int it, const Place& vs) {   // V(it) and K(it + 1)
           await(true, &full[vs.i], vs.phase);
-          await(it >= clean0, &v_raw[w & 3], (w >> 2) & 1);
-          await(it >= clean0, &v_clean[w & 3], (w >> 2) & 1);
+          if (it >= clean0) {
+            const int w = cleaned + it - clean0;
+            await(true, &v_raw[w & 3], (w >> 2) & 1);
+            await(true, &v_clean[w & 3], (w >> 2) & 1);
+          }
         };
         await(true, &full[ks.i], ks.phase);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (x ? n1 : n0) {
             await(true, &q_full[x], q_used[x] & 1);
+            await(issued[x % Pl::kS] > 0, place_read(x), place_parity(x));
             ++q_used[x];
             scores(x, 0, x, false, 0);
           }
@@ -542,21 +566,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         await_v(0, vs);
         ks = vs.next();         // K(it + 1)'s
         if (n1 > 0) {
+          bool ahead = false;
           for (int it = 0; it < n1 && ok; ++it) {
             const bool more0 = it + 1 < n0, more1 = it + 1 < n1;
-            if (it < n0) {
-              values(0, 0, it, vs);
-              await(more0, &full[ks.i], ks.phase);
-              values(0, 1, it, vs);
-            }
-            if (more0) scores(0, it + 1, 1, true, (done[1] + it) & 1);
-            values(1, 0, it, vs);
-            const Place next = ks.next();
-            await(more1 && !more0, &full[ks.i], ks.phase);
-            values(1, 1, it, vs);
+            if (it < n0) values(0, it, vs, ahead, more0);
+            ahead = more0 && scores(0, it + 1, 1, true, (done[1] + it) & 1);
+            values(1, it, vs, ahead, more1);
+            ahead = false;
             if (more1) {
+              const Place next = ks.next();
               await_v(it + 1, next);
-              scores(1, it + 1, 0, more0, (done[0] + it + 1) & 1);
+              ahead = scores(1, it + 1, 0, more0, (done[0] + it + 1) & 1);
               vs = next;
               ks = vs.next();
             }
@@ -564,13 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         } else {   // a tile alone: its S beside its softmax
           for (int it = 0; it < n0 && ok; ++it) {
             const bool more = it + 1 < n0;
-            await(more, &full[ks.i], ks.phase);
-            if (more) scores(0, it + 1, 0, false, 0);
-            values(0, 0, it, vs);
-            const Place next = ks.next();
-            if (more) await_v(it + 1, next);
-            values(0, 1, it, vs);
             if (more) {
+              await(true, place_read(0), place_parity(0));
+              scores(0, it + 1, 0, false, 0);
+            }
+            values(0, it, vs, false, false);
+            if (more) {
+              const Place next = ks.next();
+              await_v(it + 1, next);
               vs = next;
               ks = vs.next();
             }
