@@ -60,6 +60,7 @@ struct Launch {
   PromptArgs a;
   int P, tokens, tiles;   // heads and tokens of a tile, tiles of a CTA
   int units;              // Hq / P
+  int wide;               // rows of out are 32-byte aligned
   long long pairs;        // tile pairs of all units, at most
 };
 
@@ -298,8 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int j = 0; j < 128; ++j)
             if (j >= k) s[j / 32][j % 32] = 0xFF800000u;
         }
+        if (it == 0) {   // m: the maximum of the first half (where that is -inf, the code below goes on looking)
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 64; ++j) top = fmaxf(top, __uint_as_float(s[j / 32][j % 32]));
+          m = fmaxf(m, top * f);
+        }
         // Half of the keys at a time, so that their PV may start.  No maximum is taken in the common path: a half whose sum
-        // passes kMost (rare after the first; whatever P could not hold is among them) raises m to its maximum, scales
+        // passes kMost (rare; whatever P could not hold is among them) raises m to its maximum, scales
         // l and O, and is computed again.
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -393,9 +400,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           } else {
             uint16_t* dst = static_cast<uint16_t*>(a.out) + r * a.out_stride + (long long)head * D + c;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              *reinterpret_cast<uint4*>(dst + j) = make_uint4(pack_p<BF>(o[j], o[j + 1]), pack_p<BF>(o[j + 2], o[j + 3]),
-                                                              pack_p<BF>(o[j + 4], o[j + 5]), pack_p<BF>(o[j + 6], o[j + 7]));
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = pack_p<BF>(o[j + 2 * i], o[j + 2 * i + 1]);
+              if (p.wide) {   // 32 bytes a store: whole sectors
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + j), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                             "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                             : "memory");
+              } else {
+                *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(dst + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
           }
           __syncwarp();
         }
@@ -726,6 +743,7 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
   p.P = a.G & -a.G;
   p.tokens = kM / p.P;
   p.units = a.Hq / p.P;
+  p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
   // CTAs of a head: every sequence may have a last tile that is not full, and no more rows than there are
   auto ctas = [&](int tiles) {
     const long long span = (long long)tiles * p.tokens;
