@@ -399,19 +399,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           } else {
             uint16_t* dst = static_cast<uint16_t*>(a.out) + r * a.out_stride + (long long)head * D + c;
+            uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              uint32_t w[8];
+            for (int i = 0; i < 16; ++i) w[i] = pack_p<BF>(o[2 * i], o[2 * i + 1]);
+            if (p.wide) {   // 32 bytes a store: whole sectors
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = pack_p<BF>(o[j + 2 * i], o[j + 2 * i + 1]);
-              if (p.wide) {   // 32 bytes a store: whole sectors
-                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + j), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                             "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+              for (int i = 0; i < 16; i += 8)
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 2 * i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]),
+                             "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
                              : "memory");
-              } else {
-                *reinterpret_cast<uint4*>(dst + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4*>(dst + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
             }
           }
           __syncwarp();
