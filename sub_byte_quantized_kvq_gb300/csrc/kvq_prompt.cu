@@ -48,20 +48,20 @@ struct Plan {
   static constexpr int kBlock = kM * 128;             // of its 64 channels
   static constexpr int kStages = D == 128 ? 5 : 8;    // the ring of K and V tiles
   static constexpr int kSmem = 1024 + (2 + kStages) * kTile + 512;   // 1024: alignment slack
-  // Tensor memory: S at 0 (D = 64: tile 1's at 128), P at 128 (256) + 64 x, O behind.  With D = 128 both tiles' S go
-  // through one place, in turn: that leaves P one of its own, so that S(it + 1) need not wait for the PV that reads P(it).
-  static constexpr int kS = D == 128 ? 1 : 2, kP = 128 * kS, kO = kP + 128;
-  static_assert(kO + 2 * D == 512, "tensor memory");
+  // Tensor memory: S at 0, P at 128 + 64 x, O at 256 + D x.  Both tiles' S go through one place, in turn: P then has one of
+  // its own, and S(it + 1) need not wait for the PV that reads P(it).
+  static constexpr int kP = 128, kO = 256;
 };
 static_assert(Plan<128>::kSmem <= 227 * 1024, "shared memory");
 
 struct Launch {
   CUtensorMap q, k, v;
   PromptArgs a;
-  int P, tokens, tiles;   // heads and tokens of a tile, tiles of a CTA
+  int P, log_p, tokens, tiles;   // heads (a power of two) and tokens of a tile, tiles of a CTA
+  int log_span;           // log2 of a pair's tokens
   int units;              // Hq / P
   int wide;               // rows of out are 32-byte aligned
-  long long pairs;        // tile pairs of all units, at most
+  int pairs;              // tile pairs of all units, at most
 };
 
 struct Wait {
@@ -93,56 +93,73 @@ __device__ __forceinline__ uint32_t pack_p(float lo, float hi) {
   return h2_as_u32(__floats2half2_rn(lo, hi));
 }
 
+template <bool BF>
+__device__ __forceinline__ float2 unpack_p(uint32_t u) {
+  if (BF) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  return __half22float2(u32_as_h2(u));
+}
+
 // A tile pair's sequence and the first of its tokens, by its rank among all pairs of a head: those with the most keys
 // first (later pairs then fill the gaps that they leave), none for what a sequence does not have.  With T_b pairs of
 // `span` tokens in sequence b, count(L) = sum_b max(0, T_b - L) pairs lie at L or later in their sequences; the rank-th
 // is at the largest L with count(L) > rank.  By one warp, the first 512 sequences' T_b in registers.
 struct Finder {
-  static constexpr int R = 16;
+  static constexpr int R = 8;
   const PromptArgs& a;
-  int span, lane, T[R];
+  int log_span, lane, T[R];
   bool even;   // every sequence has t_new tokens
   __device__ __forceinline__ int tiles_of(int s) const {
     long long f;
     int n;
     bool bad;
-    return s < a.B && prompt_rows(a, s, f, n, bad) ? (n + span - 1) / span : 0;
+    return s < a.B && prompt_rows(a, s, f, n, bad) ? ((n - 1) >> log_span) + 1 : 0;
   }
-  __device__ __forceinline__ Finder(const PromptArgs& args, int sp, int ln) : a(args), span(sp), lane(ln) {
+  __device__ __forceinline__ Finder(const PromptArgs& args, int log_sp, int ln) : a(args), log_span(log_sp), lane(ln) {
     even = !a.lens && !a.first && (long long)a.B * a.t_new <= a.rows;
 #pragma unroll
-    for (int k = 0; k < R; ++k) T[k] = !even && 32 * k < a.B ? tiles_of(lane + 32 * k) : 0;
-  }
-  __device__ __forceinline__ long long count(int L) const {
-    long long c = 0;
+    for (int k = 0; k < R; ++k) T[k] = 0;
+    if (!even)
 #pragma unroll
-    for (int k = 0; k < R; ++k) c += max(0, T[k] - L);
-    for (int s = lane + 32 * R; s < a.B; s += 32) c += max(0, tiles_of(s) - L);
-    // (the sum over a warp in two halves)
-    const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)c & 0xFFFFFFu), hi = __reduce_add_sync(0xffffffffu, (unsigned)(c >> 24));
-    return (long long)lo + ((long long)hi << 24);
+      for (int k = 0; k < R; ++k)
+        if (32 * k < a.B) T[k] = tiles_of(lane + 32 * k);
   }
-  __device__ __forceinline__ bool find(long long rank, int& b, int& t0) const {
-    const int most = (a.t_new - 1) / span + 1;
+  // The pairs of a head are below 2^31 (checked by the launch), so 32 bits count them.
+  __device__ __forceinline__ bool find(unsigned rank, int& b, int& t0) const {
+    const int most = ((a.t_new - 1) >> log_span) + 1;
     if (even) {
-      b = (int)(rank % a.B);
-      t0 = (int)(most - 1 - rank / a.B) * span;
-      return rank < (long long)most * a.B;
+      b = (int)(rank % (unsigned)a.B);
+      t0 = (most - 1 - (int)(rank / (unsigned)a.B)) << log_span;
+      return t0 >= 0;
     }
-    if (count(0) <= rank) return false;
-    int lo = 0, hi = most;   // count(lo) > rank >= count(hi) = 0
+    int lo = -1, hi = most;    // count(lo) > rank >= count(hi)
+    unsigned above = 0;        // count(hi)
+#pragma unroll 1
     while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;
-      if (count(mid) > rank) lo = mid;
-      else hi = mid;
+      const int mid = (lo + hi) >> 1;
+      unsigned c = 0;
+#pragma unroll
+      for (int k = 0; k < R; ++k) c += max(0, T[k] - mid);
+#pragma unroll 1
+      for (int s = lane + 32 * R; s < a.B; s += 32) c += max(0, tiles_of(s) - mid);
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (c > rank) {
+        lo = mid;
+      } else {
+        hi = mid;
+        above = c;
+      }
     }
-    int left = (int)(rank - count(lo + 1));   // which of the sequences with more than lo pairs
+    if (lo < 0) return false;
+    int left = (int)(rank - above);   // which of the sequences with more than lo pairs
+#pragma unroll 1
     for (int s0 = 0; s0 < a.B; s0 += 32) {
-      const unsigned has = __ballot_sync(0xffffffffu, tiles_of(s0 + lane) > lo);
+      unsigned has = __ballot_sync(0xffffffffu, tiles_of(s0 + lane) > lo);
       const int n = __popc(has);
       if (left < n) {
-        b = s0 + (int)__fns(has, 0, left + 1);
-        t0 = lo * span;
+#pragma unroll 1
+        for (; left > 0; --left) has &= has - 1;
+        b = s0 + __ffs((int)has) - 1;
+        t0 = lo << log_span;
         return true;
       }
       left -= n;
@@ -158,11 +175,11 @@ struct Pair {
 };
 // The k-th pair of this CTA: every round of the grid's CTAs takes the next ones in the finder's order, odd rounds
 // backwards, so that no CTA has the longer one each time.
-__device__ __forceinline__ Pair next_pair(const Launch& p, const Finder& finder, long long k) {
-  const long long i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-  Pair r = {0, 0, 0, (int)(i % p.units)};
+__device__ __forceinline__ Pair next_pair(const Launch& p, const Finder& finder, unsigned k) {
+  const unsigned i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);   // below 2^31 + 2 grids
+  Pair r = {0, 0, 0, (int)(i % (unsigned)p.units)};
   int b;
-  if (i < p.pairs && finder.find(i / p.units, b, r.t0)) {
+  if (i < (unsigned)p.pairs && finder.find(i / (unsigned)p.units, b, r.t0)) {
     long long first;
     bool bad;
     prompt_rows(p.a, b, first, r.n, bad);
@@ -181,22 +198,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
   uint8_t* ring = smem + 2 * Pl::kTile;
   uint64_t *q_full = reinterpret_cast<uint64_t*>(ring + NS * Pl::kTile), *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + NS,
-           *s_full = empty + NS, *s_read = s_full + 2, *p_full = s_read + 2, *h_done = p_full + 4, *o_done = h_done + 2, *v_raw = o_done + 2, *v_clean = v_raw + 4,
-           *info_full = v_clean + 4, *info_empty = info_full + 2, *drained = info_empty + 2;
+           *s_full = empty + NS, *s_read = s_full + 2, *p_full = s_read + 1, *h_done = p_full + 2, *o_done = h_done + 2, *v_raw = o_done + 2, *v_clean = v_raw + 8,
+           *info_full = v_clean + 8, *info_empty = info_full + 2, *drained = info_empty + 2;
   volatile int* info = reinterpret_cast<volatile int*>(drained + 1);   // [2] Pair
   volatile int* stop = info + 8;                                       // a wait gave up
   volatile int* bad_v = stop + 1;                                      // [2] pair's V has infinities or NaN that were cleaned
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1) + 11;
-  static_assert((4 + 2 * NS + 2 + 2 + 4 + 2 + 2 + 4 + 4 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
+  static_assert((4 + 2 * NS + 2 + 1 + 2 + 2 + 2 + 8 + 8 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
 
   if (warp == 8 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_read[i], 4);
-      mbar_init(&p_full[2 * i], 4);
-      mbar_init(&p_full[2 * i + 1], 4);
+      mbar_init(&p_full[i], 4);
       mbar_init(&h_done[i], 1);
       mbar_init(&o_done[i], 1);
       mbar_init(&info_full[i], 1);
@@ -207,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&empty[i], 1);
     }
     mbar_init(drained, 1);
-    for (int i = 0; i < 4; ++i) {
+    mbar_init(s_read, 4);
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&v_raw[i], 1);
       mbar_init(&v_clean[i], 2);
     }
@@ -261,15 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lanes + 128 * (x % Pl::kS), to = tmem + lanes + Pl::kO + D * x, tp = tmem + lanes + Pl::kP + 64 * x;
+    const uint32_t ts = tmem + lanes, to = tmem + lanes + Pl::kO + D * x, tp = tmem + lanes + Pl::kP + 64 * x;
     const bool neg = a.scale < 0.f;
     const float f = fmaxf(fabsf(a.scale) * kLog2e, 1e-36f);   // (not 0: what is masked is -inf times it)
     constexpr float bias = BF ? 0.f : 6.f, kMost = BF ? 0x1p16f : 0x1p15f;   // m and the weights in log2 units: p = 2^(s f - m + bias)
     int done = 0;   // key tiles of earlier pairs
     for (int pk = 0; get_pair(pk); ++pk) {
       const int nx = n_keys(x), tx = pair.t0 + x * p.tokens;
-      const bool alone = n_keys(1) == 0;
-      const int token = tx + row / p.P, mask0 = masked_from(tx);
+      const int token = tx + (row >> p.log_p), mask0 = masked_from(tx);
       const int lim = a.causal ? min(pair.n, token + 1) : pair.n;
       float m = token < pair.n ? -INFINITY : 0.f, l = 0.f;   // (a row past the sequence asks for nothing)
       for (int it = 0; it < nx; ++it) {
@@ -283,13 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int c = 0; c < 4; ++c) tc::wait_ld(s[c]);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_read[x % Pl::kS]);   // the next S may come
-        // PV(it - 1) reads P, and adds to O: where it was issued before S(it), S's commit says that it is done
-        if (alone && it > 0) {
-          ok = __all_sync(0xffffffffu, wait(&o_done[x], (done + it - 1) & 1));
-          if (!ok) break;
-          tc::fence_after();
-        }
+        if (lane == 0) mbar_arrive(s_read);   // the next S may come
         if (neg)
 #pragma unroll
           for (int j = 0; j < 128; ++j) s[j / 32][j % 32] ^= 0x80000000u;
@@ -305,29 +314,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int j = 0; j < 64; ++j) top = fmaxf(top, __uint_as_float(s[j / 32][j % 32]));
           m = fmaxf(m, top * f);
         }
-        // Half of the keys at a time, so that their PV may start.  No maximum is taken in the common path: a half whose sum
-        // passes kMost (rare; whatever P could not hold is among them) raises m to its maximum, scales
-        // l and O, and is computed again.
+        // Half of the keys at a time.  No maximum is taken in the common path: a half whose sum passes kMost (rare; whatever P
+        // could not hold is among them) raises m to its maximum, scales l, O and the first half's P, and is computed again.
+        // PV(it - 1) reads P and adds to O: its halves are waited for when the weights are ready to go over it.
+        const int before = (done + it - 1) & 1;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint64_t f2 = pack2(f, f);
           float sum;
+          uint32_t w[2][16];
 #pragma unroll 1
           for (bool again = false;; again = true) {
             const float mb = m == -INFINITY ? bias : bias - m;
             const uint64_t mb2 = pack2(mb, mb);
             uint64_t sums = 0ull;
 #pragma unroll
-            for (int c = 2 * h; c < 2 * h + 2; ++c) {
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float2 y = unpack2(fma2(pack2u(s[c][j], s[c][j + 1]), f2, mb2));
-                const float e0 = ex2f(y.x), e1 = ex2f(y.y);
-                sums = add2(sums, pack2(e0, e1));
-                w[j / 2] = pack_p<BF>(e0, e1);
-              }
-              tc::st16(tp + 16 * c, w);
+            for (int j = 0; j < 64; j += 2) {
+              const float2 y = unpack2(fma2(pack2u(s[2 * h + j / 32][j % 32], s[2 * h + j / 32][j % 32 + 1]), f2, mb2));
+              const float e0 = ex2f(y.x), e1 = ex2f(y.y);
+              sums = add2(sums, pack2(e0, e1));
+              w[j / 32][j % 32 / 2] = pack_p<BF>(e0, e1);
             }
             const float2 y = unpack2(sums);
             sum = y.x + y.y;
@@ -340,12 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const float alpha = to_m == m ? 1.f : ex2f(m - to_m);
             m = to_m;
             l *= alpha;
-            if (it > 0 || h > 0) {   // (before that O holds nothing; PV(it - 1) is done, of the first half's PV not yet known)
-              if (h) {
-                ok = __all_sync(0xffffffffu, wait(&h_done[x], (done + it) & 1));
-                if (!ok) break;
-                tc::fence_after();
-              }
+            if (it > 0) {   // (before that O holds nothing)
+              ok = __all_sync(0xffffffffu, wait(&o_done[x], before));
+              if (!ok) break;
+              tc::fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
@@ -355,15 +359,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 tc::st16(to + c, o);
               }
             }
+            if (h)
+#pragma unroll 1
+              for (int c = 0; c < 32; c += 16) {
+                uint32_t o[16];
+                tc::ld16(tp + c, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float2 v = unpack_p<BF>(o[j]);
+                  o[j] = pack_p<BF>(v.x * alpha, v.y * alpha);
+                }
+                tc::st16(tp + c, o);
+              }
           }
+          if (ok && it > 0) ok = __all_sync(0xffffffffu, wait(h ? &o_done[x] : &h_done[x], before));
           if (!ok) break;
+          tc::fence_after();
+          tc::st16(tp + 32 * h, w[0]);
+          tc::st16(tp + 32 * h + 16, w[1]);
           l += sum;
-          tc::wait_st();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * x + h]);
         }
         if (!ok) break;
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
       if (nx > 0) {
@@ -375,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const bool live = token < pair.n, patch = bad_v[pk & 1] != 0;
         const long long r = (long long)pair.first + token;
-        const int head = pair.unit * p.P + row % p.P;
+        const int head = pair.unit * p.P + (row & (p.P - 1));
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -424,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     int pos = 0, cleaned = 0;   // places of the ring and cleaned V tiles of earlier pairs
     if (warp == 8) {
-      // ---------------------------------------------------------------- pairs and loads: K(0), V(0), K(1), ... through the ring
+      // ---------------------------------------------------------------- pairs, and loads through the ring
       int q_used[2] = {0, 0};
-      const Finder finder(a, p.tiles * p.tokens, lane);
+      const Finder finder(a, p.log_span, lane);
       for (int pk = 0; ok; ++pk) {
         pair = next_pair(p, finder, pk);
         if (lane == 0) {
@@ -456,32 +476,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const int st = pos % NS;
             if (pos >= NS) ok = wait(&empty[st], (pos / NS - 1) & 1);
             if (!ok) break;
-            // K(0) has its place's barrier; V(it) and K(it + 1) land on V's together.  A V tile that is cleaned lands on a
-            // barrier of its own (the ring holds at most four), so that the cleaning warps see each of its phases
-            const bool raw = (i & 1) && (i >> 1) >= clean0;
-            if (i & 1) {
+            // the i-th tile: K(0), K(1), V(0), K(2), V(1), ..., V(most - 1)
+            const bool is_v = i == 2 * most - 1 || (i > 0 && i % 2 == 0);
+            const int j = is_v ? (i == 2 * most - 1 ? most - 1 : i / 2 - 1) : (i + 1) / 2;
+            // K(0) and K(1) have their places' barriers; V(j) and K(j + 2) land on V's together.  A V tile that is cleaned lands
+            // on a barrier of its own (the ring holds at most eight), so that the cleaning warps see each of its phases
+            const bool raw = is_v && j >= clean0;
+            if (is_v) {
               v_bar = &full[st];
-              const int with = (raw ? 0 : Pl::kTile) + (i + 1 < 2 * most ? Pl::kTile : 0);
+              const int with = (raw ? 0 : Pl::kTile) + (j + 2 < most ? Pl::kTile : 0);
               if (with) mbar_arrive_expect_tx(v_bar, with);
               else mbar_arrive(v_bar);
             } else {
-              if (i == 0) mbar_arrive_expect_tx(&full[st], Pl::kTile);
+              if (j < 2) mbar_arrive_expect_tx(&full[st], Pl::kTile);
               else mbar_arrive(&full[st]);
             }
-            uint64_t* bar = raw ? &v_raw[cleaned & 3] : i == 0 ? &full[st] : v_bar;
+            uint64_t* bar = raw ? &v_raw[cleaned & 7] : !is_v && j < 2 ? &full[st] : v_bar;
             if (raw) {
               ++cleaned;
               mbar_arrive_expect_tx(bar, Pl::kTile);
             }
             for (int c = 0; c < KC; ++c)
-              tc::tma3d(ring + st * Pl::kTile + c * Pl::kBlock, i & 1 ? &p.v : &p.k, 64 * c, head0 / a.G, pair.first + (i >> 1) * kKeys, bar);
+              tc::tma3d(ring + st * Pl::kTile + c * Pl::kBlock, is_v ? &p.v : &p.k, 64 * c, head0 / a.G, pair.first + j * kKeys, bar);
             ++pos;
           }
           if (!ok) {   // what is in flight has to land before the CTA ends
             for (int i = 0; i < 2; ++i)
               if (q_used[i]) mbar_wait_bounded(&q_full[i], (q_used[i] - 1) & 1, kWaitLimitNs);
             for (int j = max(0, pos - NS); j < pos; ++j) mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kWaitLimitNs);
-            for (int j = max(0, cleaned - 4); j < cleaned; ++j) mbar_wait_bounded(&v_raw[j & 3], (j >> 2) & 1, kWaitLimitNs);
+            for (int j = max(0, cleaned - 8); j < cleaned; ++j) mbar_wait_bounded(&v_raw[j & 7], (j >> 3) & 1, kWaitLimitNs);
           }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -495,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                      vd = tc::desc_sw128_mn(smem_u32(ring), Pl::kBlock);
       // The whole warp goes along, and one lane of it (elect.sync) issues: the operands are then known to be the same in
       // all lanes.  Issued by one thread in a branch of its own, each MMA took 130 cycles instead of the 64 of its math.
-      int done[2] = {0, 0}, q_used[2] = {0, 0}, issued[2] = {0, 0};   // key tiles of earlier pairs, pairs with a tile x, S of a place
-      Place ks{0, 0};                             // where the next K tile lies
+      int done[2] = {0, 0}, q_used[2] = {0, 0}, issued = 0;   // key tiles of earlier pairs, pairs with a tile x; S so far
+      Place base{0, 0};                           // of the pair's K(0)
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       auto all_wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
       for (int pk = 0; get_pair(pk); ++pk) {
@@ -504,115 +527,81 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         pair.n = __shfl_sync(0xffffffffu, pair.n, 0);
         pair.t0 = __shfl_sync(0xffffffffu, pair.t0, 0);
         const int n0 = n_keys(0), n1 = n_keys(1), most = max(n0, n1), clean0 = masked_from(pair.t0);
-        // The tensor cores run dry where the warp looks at a barrier before each block (about 100 cycles, ready or not), so it
-        // looks at two at a time, behind MMAs that are queued or among those of an S: `ahead` says that they are ready.
         auto await = [&](bool at_all, uint64_t* bar, int parity) { ok = ok && (!at_all || all_wait(bar, parity)); };
-        auto test = [&](uint64_t* bar, int parity) { return mbar_test(bar, parity); };
-        auto place_read = [&](int x) { return &s_read[x % Pl::kS]; };
-        auto place_parity = [&](int x) { return (issued[x % Pl::kS] - 1) & 1; };
-        // S(it) of tile x, K(it) at place `ks` of the ring (the last S in its place of tensor memory is read); y: the tile whose PV
-        // comes next.  Returns whether that PV has the first half of its P.
-        auto scores = [&](int x, int it, int y, bool y_has, int y_parity) {
-          const int place = x % Pl::kS;
-          ++issued[place];
+        // S(it) of tile x, K(it) at place ks, once the S before it is read
+        auto scores = [&](int x, int it, const Place& ks) {
+          await(issued > 0, s_read, (issued - 1) & 1);
+          ++issued;
           tc::fence_after();
           const uint64_t kt = kd + (__shfl_sync(0xffffffffu, ks.i, 0) * Pl::kTile >> 4), qt = qd + (x * Pl::kTile >> 4);
           const bool last = it + 1 == (x ? n1 : n0), frees = x == (it < n1 ? 1 : 0);   // of the queries' uses; of K(it)'s
-          auto part = [&](int k) {
-            const uint32_t at = ((k >> 2) * Pl::kBlock + (k & 3) * 32) >> 4;
-            tc::mma(tm + 128 * place, qt + at, kt + at, id_s, k != 0);
-          };
           if (ok && tc::elect()) {
 #pragma unroll
-            for (int k = 0; k < D / 16 - 1; ++k) part(k);
-          }
-          __syncwarp();
-          const bool ahead = y_has && __all_sync(0xffffffffu, test(&p_full[2 * y], y_parity));
-          if (ok && tc::elect()) {
-            part(D / 16 - 1);
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t at = ((k >> 2) * Pl::kBlock + (k & 3) * 32) >> 4;
+              tc::mma(tm, qt + at, kt + at, id_s, k != 0);
+            }
             tc::commit(&s_full[x]);
             if (last) tc::commit(&q_empty[x]);
             if (frees) tc::commit(&empty[ks.i]);
           }
           __syncwarp();
-          return ahead;
         };
-        auto half = [&](int x, int h, int it, const Place& vs) {   // PV(it) of tile x, half h of the keys (its P is there)
+        // PV(it) of tile x, V(it) at place vs; known: its P is (an S read after it was written has been waited for)
+        auto values = [&](int x, int it, const Place& vs, bool known) {
+          await(!known, &p_full[x], (done[x] + it) & 1);
           tc::fence_after();
           const uint64_t vt = vd + (__shfl_sync(0xffffffffu, vs.i, 0) * Pl::kTile >> 4);
           const bool frees = x == (it < n1 ? 1 : 0);   // the last use of V(it)
           if (ok && tc::elect()) {
 #pragma unroll
-            for (int k = 4 * h; k < 4 * h + 4; ++k)
+            for (int k = 0; k < kKeys / 16; ++k) {
               tc::mma_ta(tm + Pl::kO + D * x, tm + Pl::kP + 64 * x + 8 * k, vt + (k * 2048 >> 4), id_o, (it | k) != 0);
-            tc::commit(h ? &o_done[x] : &h_done[x]);
-            if (h && frees) tc::commit(&empty[vs.i]);
+              if (k == 3) tc::commit(&h_done[x]);
+            }
+            tc::commit(&o_done[x]);
+            if (frees) tc::commit(&empty[vs.i]);
           }
           __syncwarp();
         };
-        // PV(it) of tile x; then (more) its place of S is known to be read
-        auto values = [&](int x, int it, const Place& vs, bool ahead, bool more) {
-          const int parity = (done[x] + it) & 1;
-          await(!ahead, &p_full[2 * x], parity);
-          half(x, 0, it, vs);
-          const bool h1 = test(&p_full[2 * x + 1], parity);
-          ahead = __all_sync(0xffffffffu, h1 && (!more || test(place_read(x), place_parity(x))));
-          await(!ahead, &p_full[2 * x + 1], parity);
-          half(x, 1, it, vs);
-          await(!ahead && more, place_read(x), place_parity(x));
-        };
-        auto await_v = [&](int it, const Place& vs) {   // V(it) and K(it + 1)
-          await(true, &full[vs.i], vs.phase);
-          if (it >= clean0) {
-            const int w = cleaned + it - clean0;
-            await(true, &v_raw[w & 3], (w >> 2) & 1);
-            await(true, &v_clean[w & 3], (w >> 2) & 1);
-          }
-        };
-        await(true, &full[ks.i], ks.phase);
+        const Place first = base;
+        Place k1 = base.next();                         // K(it + 1)'s place
+        Place vs = most > 1 ? k1.next() : k1;           // V(it)'s
+        await(true, &full[first.i], first.phase);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (x ? n1 : n0) {
             await(true, &q_full[x], q_used[x] & 1);
-            await(issued[x % Pl::kS] > 0, place_read(x), place_parity(x));
             ++q_used[x];
-            scores(x, 0, x, false, 0);
+            scores(x, 0, first);
           }
-        Place vs = ks.next();   // V(it)'s
-        await_v(0, vs);
-        ks = vs.next();         // K(it + 1)'s
-        if (n1 > 0) {
-          bool ahead = false;
-          for (int it = 0; it < n1 && ok; ++it) {
-            const bool more0 = it + 1 < n0, more1 = it + 1 < n1;
-            if (it < n0) values(0, it, vs, ahead, more0);
-            ahead = more0 && scores(0, it + 1, 1, true, (done[1] + it) & 1);
-            values(1, it, vs, ahead, more1);
-            ahead = false;
-            if (more1) {
-              const Place next = ks.next();
-              await_v(it + 1, next);
-              ahead = scores(1, it + 1, 0, more0, (done[0] + it + 1) & 1);
-              vs = next;
-              ks = vs.next();
-            }
+        await(most > 1, &full[k1.i], k1.phase);
+        if (n1 > 0 && n0 > 1) scores(0, 1, k1);
+        // Two tiles: S(it + 1) of tile 1, PV(it) of tile 0, S(it + 2) of tile 0, PV(it) of tile 1.  A softmax reads its next S when
+        // it has written its P; the other tile's S then goes first, and the PV has the time that the softmax takes until it
+        // has the next weights.  One tile: S(it + 1), PV(it).
+        for (int it = 0; it < most && ok; ++it) {
+          const Place k2 = vs.next();                   // K(it + 2)'s place
+          if (n1 > 0) {
+            if (it + 1 < n1) scores(1, it + 1, k1);
+          } else if (it + 1 < n0) {
+            scores(0, it + 1, k1);
           }
-        } else {   // a tile alone: its S beside its softmax
-          for (int it = 0; it < n0 && ok; ++it) {
-            const bool more = it + 1 < n0;
-            if (more) {
-              await(true, place_read(0), place_parity(0));
-              scores(0, it + 1, 0, false, 0);
-            }
-            values(0, it, vs, false, false);
-            if (more) {
-              const Place next = ks.next();
-              await_v(it + 1, next);
-              vs = next;
-              ks = vs.next();
-            }
+          await(true, &full[vs.i], vs.phase);           // V(it), and with it K(it + 2)
+          if (it >= clean0) {
+            const int w = cleaned + it - clean0;
+            await(true, &v_raw[w & 7], (w >> 3) & 1);
+            await(true, &v_clean[w & 7], (w >> 3) & 1);
           }
+          if (it < n0) values(0, it, vs, n1 > 0 && it + 1 < n0);
+          if (n1 > 0) {
+            if (it + 2 < n0) scores(0, it + 2, k2);
+            values(1, it, vs, it + 2 < n0);
+          }
+          vs = it + 2 < most ? k2.next() : k2;
+          k1 = k2;
         }
+        base = vs;
         if (!ok) break;
         pos += 2 * most;
         cleaned += max(0, most - clean0);
@@ -635,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int most = max(n_keys(0), n_keys(1)), clean0 = masked_from(pair.t0);
         int any_bad = 0;
         for (int it = clean0; it < most; ++it, ++cleaned) {
-          ok = __all_sync(0xffffffffu, wait(&v_raw[cleaned & 3], (cleaned >> 2) & 1));
+          ok = __all_sync(0xffffffffu, wait(&v_raw[cleaned & 7], (cleaned >> 3) & 1));
           if (!ok) break;
-          uint8_t* vt = ring + (pos + 2 * it + 1) % NS * Pl::kTile;
+          uint8_t* vt = ring + (pos + (it == most - 1 ? 2 * most - 1 : 2 * it + 2)) % NS * Pl::kTile;
           const int whole = max(0, (a.causal ? min(pair.t0 + 1, pair.n) : pair.n) - it * kKeys);   // rows before it: every token sees them
           for (int c = 0; c < KC; ++c)
 #pragma unroll 4
@@ -667,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           if (any_bad) bad_v[pk & 1] = 1;
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&v_clean[cleaned & 3]);
+          if (lane == 0) mbar_arrive(&v_clean[cleaned & 7]);
         }
         if (!ok) break;
         pos += 2 * most;
@@ -685,12 +674,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
   if (*stop) {   // nothing that a wait gave up on is taken for a result
-    const Finder finder(a, p.tiles * p.tokens, lane);
+    const Finder finder(a, p.log_span, lane);
     for (int pk = 0;; ++pk) {
       pair = next_pair(p, finder, pk);   // (every warp by itself)
       if (pair.n == 0) break;
       for (int i = warp; i < p.tiles * kM; i += kThreads / 32) {
-        const int token = pair.t0 + i / p.P, head = pair.unit * p.P + i % p.P;
+        const int token = pair.t0 + (i >> p.log_p), head = pair.unit * p.P + (i & (p.P - 1));
         if (token >= pair.n) continue;
         const long long r = (long long)pair.first + token, at = r * a.out_stride + (long long)head * D;
         for (int c = lane; c < D; c += 32)
@@ -740,6 +729,7 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
   Launch p;
   p.a = a;
   p.P = a.G & -a.G;
+  for (p.log_p = 0; 1 << p.log_p < p.P; ++p.log_p) {}
   p.tokens = kM / p.P;
   p.units = a.Hq / p.P;
   p.wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;
@@ -749,8 +739,11 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
     return std::min((long long)a.B * ((a.t_new + span - 1) / span), a.rows / span + a.B);
   };
   p.tiles = ctas(2) * p.units >= sms ? 2 : 1;   // one tile a CTA where two would leave SMs idle
-  p.pairs = ctas(p.tiles) * p.units;
-  const unsigned grid = (unsigned)std::min<long long>(p.pairs, sms);
+  const long long pairs = ctas(p.tiles) * p.units;
+  if (pairs > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;   // (more rows or heads than memory holds)
+  p.pairs = (int)pairs;
+  p.log_span = 7 - p.log_p + (p.tiles == 2);
+  const unsigned grid = (unsigned)std::min(p.pairs, sms);
   if (!encode(&p.q, a.q, BF, D, a.Hq, a.rows, a.q_stride, p.P, p.tokens) || !encode(&p.k, a.k, BF, D, a.Hkv, a.rows, a.k_stride, 1, kKeys) ||
       !encode(&p.v, a.v, BF, D, a.Hkv, a.rows, a.v_stride, 1, kKeys))
     return cudaErrorInvalidValue;
