@@ -198,13 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   uint8_t* smem = raw_smem + (((smem_u32(raw_smem) + 1023u) & ~1023u) - smem_u32(raw_smem));
   uint8_t* ring = smem + 2 * Pl::kTile;
   uint64_t *q_full = reinterpret_cast<uint64_t*>(ring + NS * Pl::kTile), *q_empty = q_full + 2, *full = q_empty + 2, *empty = full + NS,
-           *s_full = empty + NS, *s_read = s_full + 2, *p_full = s_read + 1, *h_done = p_full + 2, *o_done = h_done + 2, *v_raw = o_done + 2, *v_clean = v_raw + 8,
+           *s_full = empty + NS, *s_read = s_full + 2, *p_full = s_read + 1, *o_done = p_full + 2, *v_raw = o_done + 2, *v_clean = v_raw + 8,
            *info_full = v_clean + 8, *info_empty = info_full + 2, *drained = info_empty + 2;
   volatile int* info = reinterpret_cast<volatile int*>(drained + 1);   // [2] Pair
   volatile int* stop = info + 8;                                       // a wait gave up
   volatile int* bad_v = stop + 1;                                      // [2] pair's V has infinities or NaN that were cleaned
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1) + 11;
-  static_assert((4 + 2 * NS + 2 + 1 + 2 + 2 + 2 + 8 + 8 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
+  static_assert((4 + 2 * NS + 2 + 1 + 2 + 2 + 8 + 8 + 2 + 2 + 1) * 8 + 48 <= 512 && NS <= 8, "barriers");
 
   if (warp == 8 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
-      mbar_init(&h_done[i], 1);
       mbar_init(&o_done[i], 1);
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], 11);   // softmax, MMA and cleaning warps
@@ -315,22 +314,22 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           m = fmaxf(m, top * f);
         }
         // Half of the keys at a time.  No maximum is taken in the common path: a half whose sum passes kMost (rare; whatever P
-        // could not hold is among them) raises m to its maximum, scales l, O and the first half's P, and is computed again.
-        // PV(it - 1) reads P and adds to O: its halves are waited for when the weights are ready to go over it.
+        // could not hold is among them) raises m to its maximum, scales l, O and the first half's weights, and is computed
+        // again.  PV(it - 1), which reads P and adds to O, is waited for when the weights are ready to go over P.
         const int before = (done + it - 1) & 1;
+        const uint64_t f2 = pack2(f, f);
+        uint32_t w[4][16];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint64_t f2 = pack2(f, f);
           float sum;
-          uint32_t w[2][16];
 #pragma unroll 1
           for (bool again = false;; again = true) {
             const float mb = m == -INFINITY ? bias : bias - m;
             const uint64_t mb2 = pack2(mb, mb);
             uint64_t sums = 0ull;
 #pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-              const float2 y = unpack2(fma2(pack2u(s[2 * h + j / 32][j % 32], s[2 * h + j / 32][j % 32 + 1]), f2, mb2));
+            for (int j = 64 * h; j < 64 * h + 64; j += 2) {
+              const float2 y = unpack2(fma2(pack2u(s[j / 32][j % 32], s[j / 32][j % 32 + 1]), f2, mb2));
               const float e0 = ex2f(y.x), e1 = ex2f(y.y);
               sums = add2(sums, pack2(e0, e1));
               w[j / 32][j % 32 / 2] = pack_p<BF>(e0, e1);
@@ -346,6 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const float alpha = to_m == m ? 1.f : ex2f(m - to_m);
             m = to_m;
             l *= alpha;
+            if (h)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float2 v = unpack_p<BF>(w[j / 16][j % 16]);
+                w[j / 16][j % 16] = pack_p<BF>(v.x * alpha, v.y * alpha);
+              }
             if (it > 0) {   // (before that O holds nothing)
               ok = __all_sync(0xffffffffu, wait(&o_done[x], before));
               if (!ok) break;
@@ -359,27 +364,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 tc::st16(to + c, o);
               }
             }
-            if (h)
-#pragma unroll 1
-              for (int c = 0; c < 32; c += 16) {
-                uint32_t o[16];
-                tc::ld16(tp + c, o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float2 v = unpack_p<BF>(o[j]);
-                  o[j] = pack_p<BF>(v.x * alpha, v.y * alpha);
-                }
-                tc::st16(tp + c, o);
-              }
           }
-          if (ok && it > 0) ok = __all_sync(0xffffffffu, wait(h ? &o_done[x] : &h_done[x], before));
-          if (!ok) break;
-          tc::fence_after();
-          tc::st16(tp + 32 * h, w[0]);
-          tc::st16(tp + 32 * h + 16, w[1]);
           l += sum;
         }
+        if (ok && it > 0) ok = __all_sync(0xffffffffu, wait(&o_done[x], before));
         if (!ok) break;
+        tc::fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::st16(tp + 16 * c, w[c]);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -555,10 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const bool frees = x == (it < n1 ? 1 : 0);   // the last use of V(it)
           if (ok && tc::elect()) {
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k) {
+            for (int k = 0; k < kKeys / 16; ++k)
               tc::mma_ta(tm + Pl::kO + D * x, tm + Pl::kP + 64 * x + 8 * k, vt + (k * 2048 >> 4), id_o, (it | k) != 0);
-              if (k == 3) tc::commit(&h_done[x]);
-            }
             tc::commit(&o_done[x]);
             if (frees) tc::commit(&empty[vs.i]);
           }
