@@ -187,6 +187,92 @@ def test_many_short_sequences():
     run_and_check([5] * 70 + [300] + [0] * 40 + [129] * 3, 2, 1, 128)
 
 
+def test_scores_that_jump_within_a_tile():
+    """Each run of 64 keys scores far above (or below) the one before: the maximum has to follow between the halves of a tile."""
+    steps = torch.tensor([0, 40, 3, 90, -50, 91, 150, 0, 151, 260, 20, 261], dtype=torch.float32, device="cuda")
+    for dtype, D in ((BF, 128), (HF, 64)):
+        def change(q, k, v, first):
+            q[..., 0] = 1.0
+            n = 12 * 64
+            k[first[0]:first[0] + n, ..., 0] = steps.repeat_interleave(64)[:, None].to(k.dtype)
+        for causal in (True, False):
+            run_and_check([12 * 64, 100], 1, 2, D, dtype=dtype, causal=causal, scale=1.0, change=change, seed=2)
+
+
+def test_scores_of_minus_infinity():
+    """Keys that score -inf have no weight; a token that sees no other gets 0 and lse -inf."""
+    n, m, G, D = 700, 333, 2, 128
+    def change(q, k, v, first):
+        q[..., 0] = q[..., 0].abs() + 0.5
+        k[first[0]:first[0] + m, ..., 0] = -math.inf
+    out, lse, q, k, v, first, scale = run([n], 1, G, D, change=change)
+    s = slice(first[0], first[0] + m)
+    assert (out[s] == 0).all() and (lse[s] == -math.inf).all()
+    s = slice(first[0] + m, first[0] + n)   # the rest attends to itself alone
+    check(out[s], lse[s], q[s], k[s], v[s], scale, True)
+
+
+@pytest.mark.parametrize("offset,pad", [(8, 0), (0, 8), (16, 24)])
+def test_out_rows_of_any_alignment(offset, pad):
+    """Output rows that are 16-byte, not 32-byte aligned, with a gap behind each."""
+    n, Hq, Hkv, D = 300, 4, 2, 64
+    q, k, v = inputs(n, Hq, Hkv, D, BF, 7)
+    cache = handle(1, Hkv, D)
+    want = kvq.kvq_prompt_attention(cache, q[None], k[None], v[None], 0.125)
+    flat = torch.full((offset + n * (Hq * D + pad),), 3.0, dtype=BF, device="cuda")
+    rows = flat[offset:].view(n, Hq * D + pad)
+    out = rows[:, :Hq * D].unflatten(1, (Hq, D))[None]
+    kvq.kvq_prompt_attention(cache, q[None], k[None], v[None], 0.125, out=out)
+    assert torch.equal(out, want) and (rows[:, Hq * D:] == 3).all() and (flat[:offset] == 3).all()
+
+
+def test_more_sequences_than_registers_hold():
+    gen = torch.Generator().manual_seed(5)
+    lens = torch.randint(-2, 200, (700,), generator=gen).tolist()
+    out, lse, q, k, v, first, scale = run(lens, 1, 2, 64, gap=0)
+    for b in [0, 1, 255, 256, 257, 511, 698, 699] + torch.randint(0, 700, (40,), generator=gen).tolist():
+        s = slice(first[b], first[b] + max(lens[b], 0))
+        check(out[s], lse[s], q[s], k[s], v[s], scale, True)
+    # every row was written (run() looked at the others)
+    for f, n in zip(first, lens):
+        assert n <= 0 or bool((lse[f:f + n] != 7).all())
+
+
+def test_two_calls_at_once():
+    """Calls on two streams share nothing but their inputs, and give the same bits as one after the other."""
+    a = inputs(4096, 8, 2, 128, BF, 1)
+    b = inputs(3000, 6, 2, 64, HF, 2)
+    ca, cb = handle(2, 2, 128), handle(3, 2, 64)
+    one = [x.view(2, 2048, *x.shape[1:]) for x in a], [x.view(3, 1000, *x.shape[1:]) for x in b]
+    want = kvq.kvq_prompt_attention(ca, *one[0], 0.1), kvq.kvq_prompt_attention(cb, *one[1], 0.1, causal=False)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        got.append((kvq.kvq_prompt_attention(ca, *one[0], 0.1, stream=s1), kvq.kvq_prompt_attention(cb, *one[1], 0.1, causal=False, stream=s2)))
+    s1.synchronize()
+    s2.synchronize()
+    for x, y in got:
+        assert torch.equal(x, want[0]) and torch.equal(y, want[1])
+    assert ca.status_word() == 0 and cb.status_word() == 0
+
+
+def test_long_prompt_sampled():
+    """20,011 tokens: some tokens against all the keys that they see."""
+    n, Hq, Hkv, D = 20011, 4, 1, 128
+    q, k, v = inputs(n, Hq, Hkv, D, BF, 9)
+    lse = torch.empty((1, n, Hq), device="cuda")
+    out = kvq.kvq_prompt_attention(handle(1, Hkv, D), q[None], k[None], v[None], 0.09, lse=lse, out_dtype=F32)[0]
+    for i in [0, 1, 127, 128, 129, 4095, 9999, 12345, n - 2, n - 1]:
+        a = q[i].double() @ k[:i + 1, 0].double().T * 0.09
+        z = a.logsumexp(-1)
+        p = (a - z[:, None]).exp()
+        y, size = p @ v[:i + 1, 0].double(), p @ v[:i + 1, 0].double().abs()
+        reach = (q[i].double().abs() @ k[:i + 1, 0].double().abs().T * 0.09).amax(-1)
+        bound, zbound = ref.prompt_bounds(y, z, size, reach, float(v.double().abs().max()), i + 1, D, BF, F32)
+        assert ((out[i].double() - y).abs() <= bound).all() and ((lse[0, i].double() - z).abs() <= zbound).all()
+
+
 def test_graph_streams_and_repeats():
     gen_lens = [700, 33]
     out, lse, q, k, v, first, scale = run(gen_lens, 2, 4, 128)

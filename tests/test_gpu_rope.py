@@ -108,6 +108,24 @@ def test_parts_of_one_projection_and_in_place():
     assert empty[0].shape == (0, T, Hq, D)
 
 
+def test_outputs_with_gaps():
+    """Output rows that are parts of a wider row; what lies between stays."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    rows, Hq, Hkv, D = 300, 5, 1, 128
+    q, k = [torch.randn((rows, h, D), generator=gen, device="cuda").to(HF) for h in (Hq, Hkv)]
+    pos, f, cache = torch.arange(rows, device="cuda", dtype=torch.int32), freqs(96), handle(Hkv, D)
+    want = kvq.kvq_norm_rope(cache, q, k, pos, f, out_dtype=BF)
+    wide = torch.full((rows, 8 + (Hq + Hkv) * D + 8), 5.0, dtype=BF, device="cuda")
+    qo, ko = wide[:, 8:8 + Hq * D].unflatten(1, (Hq, D)), wide[:, 8 + Hq * D:-8].unflatten(1, (Hkv, D))
+    kvq.kvq_norm_rope(cache, q, k, pos, f, q_out=qo, k_out=ko)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+    assert (wide[:, :8] == 5).all() and (wide[:, -8:] == 5).all()
+    one = q[:1].expand(rows, Hq, D)   # one row for every position
+    y, _ = kvq.kvq_norm_rope(cache, one, None, pos, f)
+    z, _ = kvq.kvq_norm_rope(cache, one.contiguous(), None, pos, f)
+    assert torch.equal(y, z)
+
+
 def test_special_values():
     """A NaN or an infinity stays in its head; rows of zeros stay zero; channels behind rot_dim do not meet the rotation."""
     D, R = 128, 32

@@ -86,3 +86,38 @@ def test_rows_of_a_tensor(kvq):
     for shape in ((3, 6, 8), (6, 16)):
         with pytest.raises(ValueError):
             rows(torch.zeros(shape), 6, 16)
+
+
+def test_binding_refusals(kvq):
+    """What the binding refuses before it looks for a device (tensors and cache on the host)."""
+    cache = kvq.QuantizedKVCache(1, 2, 2, 64, 1, 1, device="cpu")
+    bf = torch.bfloat16
+    q, k, pos, f = torch.zeros((6, 4, 64), dtype=bf), torch.zeros((6, 2, 64), dtype=bf), torch.zeros(6, dtype=torch.int32), torch.zeros(32)
+    rope = lambda *a, **kw: kvq.kvq_norm_rope(cache, *a, **kw)
+    for call in (lambda: rope(None, None, pos, f), lambda: rope(q, k[:5], pos, f), lambda: rope(q, k.float(), pos, f), lambda: rope(q, k, pos[:5], f),
+                 lambda: rope(q, k, pos, f, eps=-1.0), lambda: rope(q, k, pos, f, pair_axis=[0] * 31), lambda: rope(q, k, torch.zeros((2, 6), dtype=torch.int32), f),
+                 lambda: rope(q, k, pos[None], f, pair_axis=[1] * 32), lambda: rope(q, k, pos[None], f, pair_axis=[-1] * 32),
+                 lambda: rope(q, k, pos, f, q_out=q[:5]), lambda: rope(q, k, pos, f, q_out=q, k_out=k.float()),
+                 lambda: rope(q[..., :32], k, pos, f), lambda: rope(q, torch.zeros((6, 4, 64), dtype=bf), pos, f),
+                 lambda: rope(q, k, pos, f)):                                   # (all is right but the device)
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: rope(q, k, pos.long(), f), lambda: rope(q, k, None, f), lambda: rope(q, k, pos, f.double()),
+                 lambda: rope(q, k, pos, f, q_weight=torch.zeros(64, dtype=bf)), lambda: rope(q, k, pos, f, k_weight=torch.zeros(65))):
+        with pytest.raises(AssertionError):
+            call()
+    prompt = lambda *a, **kw: kvq.kvq_prompt_attention(cache, *a, **kw)
+    n = torch.zeros(2, dtype=torch.int32)
+    pq, pk = q.view(2, 3, 4, 64), k.view(2, 3, 2, 64)
+    for call in (lambda: prompt(pq.float(), pk.float(), pk.float(), 0.1), lambda: prompt(pq, pk.half(), pk, 0.1), lambda: prompt(q, k, k, 0.1, first_row=n),
+                 lambda: prompt(q, k, k, 0.1, first_row=n, t_per_seq=n), lambda: prompt(pq, pk[..., :1, :], pk, 0.1),
+                 lambda: prompt(pq, pk[:, :2], pk, 0.1),                        # (rows that are not evenly spaced)
+                 lambda: prompt(pq, pk, pk, 0.1)):                              # (all is right but the device)
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: prompt(q, k, k, 0.1), lambda: prompt(pq[:1], pk[:1], pk[:1], 0.1), lambda: prompt(pq, pk, pk, 0.1, t_new=2),
+                 lambda: prompt(pq, pk, pk, 0.1, t_per_seq=n.long()),
+                 lambda: prompt(pq, pk, pk, 0.1, out=torch.zeros((2, 3, 4, 64), dtype=torch.float16)), lambda: prompt(pq, pk, pk, 0.1, lse=torch.zeros((2, 3))),
+                 lambda: prompt(q, k, k, 0.1, first_row=n[:1], t_per_seq=n, t_new=3)):
+        with pytest.raises(AssertionError):
+            call()
