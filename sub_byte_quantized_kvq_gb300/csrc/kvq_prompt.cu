@@ -99,72 +99,82 @@ __device__ __forceinline__ float2 unpack_p(uint32_t u) {
   return __half22float2(u32_as_h2(u));
 }
 
-// A tile pair's sequence and the first of its tokens, by its rank among all pairs of a head: those with the most keys
-// first (later pairs then fill the gaps that they leave), none for what a sequence does not have.  With T_b pairs of
-// `span` tokens in sequence b, count(L) = sum_b max(0, T_b - L) pairs lie at L or later in their sequences; the rank-th
-// is at the largest L with count(L) > rank.  By one warp, the first 512 sequences' T_b in registers.
+// A tile pair's sequence and the first of its tokens, by its rank among all pairs of a head: 256 sequences after the other
+// 256, and of those the pairs with the most keys first (later ones then fill the gaps that they leave), none for what a
+// sequence does not have.  With T_b pairs of `span` tokens in sequence b, count(L) = sum_b max(0, T_b - L) pairs lie at L or
+// later in their sequences; the rank-th is at the largest L with count(L) > rank.  By one warp, the 256 sequences' T_b in
+// registers: asked for rising ranks, it reads each sequence's length once.
 struct Finder {
   static constexpr int R = 8;
   const PromptArgs& a;
   int log_span, lane, T[R];
-  bool even;   // every sequence has t_new tokens
+  int seq0 = -32 * R;      // the first of the 256 sequences
+  unsigned rank0 = 0, n = 0;   // rank of their first pair, and their pairs
+  bool even;               // every sequence has t_new tokens
   __device__ __forceinline__ int tiles_of(int s) const {
     long long f;
-    int n;
+    int len;
     bool bad;
-    return s < a.B && prompt_rows(a, s, f, n, bad) ? ((n - 1) >> log_span) + 1 : 0;
+    return s < a.B && prompt_rows(a, s, f, len, bad) ? ((len - 1) >> log_span) + 1 : 0;
+  }
+  __device__ __forceinline__ void read() {
+#pragma unroll
+    for (int k = 0; k < R; ++k) T[k] = tiles_of(seq0 + lane + 32 * k);
+    n = count(0);
+  }
+  __device__ __forceinline__ unsigned count(int L) const {
+    unsigned c = 0;
+#pragma unroll
+    for (int k = 0; k < R; ++k) c += max(0, T[k] - L);
+    return __reduce_add_sync(0xffffffffu, c);
   }
   __device__ __forceinline__ Finder(const PromptArgs& args, int log_sp, int ln) : a(args), log_span(log_sp), lane(ln) {
     even = !a.lens && !a.first && (long long)a.B * a.t_new <= a.rows;
-#pragma unroll
-    for (int k = 0; k < R; ++k) T[k] = 0;
-    if (!even)
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-        if (32 * k < a.B) T[k] = tiles_of(lane + 32 * k);
   }
   // The pairs of a head are below 2^31 (checked by the launch), so 32 bits count them.
-  __device__ __forceinline__ bool find(unsigned rank, int& b, int& t0) const {
+  __device__ __forceinline__ bool find(unsigned rank, int& b, int& t0) {
     const int most = ((a.t_new - 1) >> log_span) + 1;
     if (even) {
       b = (int)(rank % (unsigned)a.B);
       t0 = (most - 1 - (int)(rank / (unsigned)a.B)) << log_span;
       return t0 >= 0;
     }
-    int lo = -1, hi = most;    // count(lo) > rank >= count(hi)
+#pragma unroll 1
+    while (rank - rank0 >= n) {
+      if (a.B - 32 * R <= seq0) return false;
+      rank0 += n;
+      seq0 += 32 * R;
+      read();
+    }
+    int lo = 0, hi = most;     // count(lo) > rank - rank0 >= count(hi)
     unsigned above = 0;        // count(hi)
 #pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      unsigned c = 0;
-#pragma unroll
-      for (int k = 0; k < R; ++k) c += max(0, T[k] - mid);
-#pragma unroll 1
-      for (int s = lane + 32 * R; s < a.B; s += 32) c += max(0, tiles_of(s) - mid);
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c > rank) {
+      const unsigned c = count(mid);
+      if (c > rank - rank0) {
         lo = mid;
       } else {
         hi = mid;
         above = c;
       }
     }
-    if (lo < 0) return false;
-    int left = (int)(rank - above);   // which of the sequences with more than lo pairs
+    int left = (int)(rank - rank0 - above);   // which of the sequences with more than lo pairs
+    b = 0;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      unsigned has = __ballot_sync(0xffffffffu, T[k] > lo);
+      if (left >= 0 && left < __popc(has)) {
 #pragma unroll 1
-    for (int s0 = 0; s0 < a.B; s0 += 32) {
-      unsigned has = __ballot_sync(0xffffffffu, tiles_of(s0 + lane) > lo);
-      const int n = __popc(has);
-      if (left < n) {
-#pragma unroll 1
-        for (; left > 0; --left) has &= has - 1;
-        b = s0 + __ffs((int)has) - 1;
-        t0 = lo << log_span;
-        return true;
+        for (int i = left; i > 0; --i) has &= has - 1;
+        b = seq0 + 32 * k + __ffs((int)has) - 1;
+        left = -1;
+      } else if (left >= 0) {
+        left -= __popc(has);
       }
-      left -= n;
     }
-    return false;
+    t0 = lo << log_span;
+    return true;
   }
 };
 
@@ -175,7 +185,7 @@ struct Pair {
 };
 // The k-th pair of this CTA: every round of the grid's CTAs takes the next ones in the finder's order, odd rounds
 // backwards, so that no CTA has the longer one each time.
-__device__ __forceinline__ Pair next_pair(const Launch& p, const Finder& finder, unsigned k) {
+__device__ __forceinline__ Pair next_pair(const Launch& p, Finder& finder, unsigned k) {
   const unsigned i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);   // below 2^31 + 2 grids
   Pair r = {0, 0, 0, (int)(i % (unsigned)p.units)};
   int b;
@@ -231,12 +241,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp == 10 && blockIdx.x == 0) {
-    for (int s = lane; s < a.B; s += 32) {
+  } else if (warp == 10) {
+    for (long long i = blockIdx.x * 32 + lane; i < a.B; i += gridDim.x * 32) {   // the sequences' rows are checked once
       long long f;
       int n;
       bool bad;
-      prompt_rows(a, s, f, n, bad);
+      prompt_rows(a, (int)i, f, n, bad);
       if (bad) atomicOr(a.status, KVQ_STATUS_BAD_ROWS);
     }
   }
@@ -438,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (warp == 8) {
       // ---------------------------------------------------------------- pairs, and loads through the ring
       int q_used[2] = {0, 0};
-      const Finder finder(a, p.log_span, lane);
+      Finder finder(a, p.log_span, lane);
       for (int pk = 0; ok; ++pk) {
         pair = next_pair(p, finder, pk);
         if (lane == 0) {
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
   if (*stop) {   // nothing that a wait gave up on is taken for a result
-    const Finder finder(a, p.log_span, lane);
+    Finder finder(a, p.log_span, lane);
     for (int pk = 0;; ++pk) {
       pair = next_pair(p, finder, pk);   // (every warp by itself)
       if (pair.n == 0) break;

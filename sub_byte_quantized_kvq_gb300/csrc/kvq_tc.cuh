@@ -129,15 +129,6 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// One 32-bit column of the calling warp's 32 lanes.
-__device__ __forceinline__ void st1(uint32_t taddr, uint32_t r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
-}
-__device__ __forceinline__ uint32_t ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
-  return r;
-}
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
   st16(taddr, r);
   st16(taddr + 16, r + 16);

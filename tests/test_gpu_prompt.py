@@ -238,6 +238,32 @@ def test_more_sequences_than_registers_hold():
         assert n <= 0 or bool((lse[f:f + n] != 7).all())
 
 
+def test_runs_of_sequences_without_tokens():
+    """Hundreds of sequences in a row without tokens, and the longest ones far behind the first."""
+    lens = [3] + [0] * 599 + [700, 1] + [0] * 290 + [5, 1500] + [-1] * 300 + [130]
+    run_and_check(lens, 1, 2, 64, gap=0)
+    run_and_check([0] * 1000 + [17], 2, 4, 128)
+    run_and_check([0] * 300, 1, 1, 64)
+
+
+def test_a_sequence_that_does_not_fit_among_many():
+    n, at = 5, 801
+    B, Hkv, G, D = 1000, 1, 1, 64
+    q, k, v = inputs(B * n, Hkv * G, Hkv, D, BF, 3)
+    first = torch.arange(0, B * n, n, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    lens[at] = n + 1
+    cache = handle(B, Hkv, D)
+    out = torch.full_like(q, 7.0)
+    kvq.kvq_prompt_attention(cache, q, k, v, 0.125, t_per_seq=lens, first_row=first, t_new=n, out=out)
+    assert cache.status_word() == kvq.KVQ_STATUS_BAD_ROWS
+    skipped = slice(at * n, at * n + n)
+    assert (out[skipped] == 7).all()
+    for b in (0, at - 1, at + 1, B - 1):
+        s = slice(b * n, b * n + n)
+        check(out[s], None, q[s], k[s], v[s], 0.125, True)
+
+
 def test_two_calls_at_once():
     """Calls on two streams share nothing but their inputs, and give the same bits as one after the other."""
     a = inputs(4096, 8, 2, 128, BF, 1)
