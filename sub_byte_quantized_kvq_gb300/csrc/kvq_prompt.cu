@@ -502,16 +502,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               tc::tma3d(ring + st * Pl::kTile + c * Pl::kBlock, is_v ? &p.v : &p.k, 64 * c, head0 / a.G, pair.first + j * kKeys, bar);
             ++pos;
           }
-          if (!ok) {   // what is in flight has to land before the CTA ends
-            for (int i = 0; i < 2; ++i)
-              if (q_used[i]) mbar_wait_bounded(&q_full[i], (q_used[i] - 1) & 1, kWaitLimitNs);
-            for (int j = max(0, pos - NS); j < pos; ++j) mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kWaitLimitNs);
-            for (int j = max(0, cleaned - 8); j < cleaned; ++j) mbar_wait_bounded(&v_raw[j & 7], (j >> 3) & 1, kWaitLimitNs);
-          }
         }
         ok = __all_sync(0xffffffffu, ok);
         if (pair.n == 0) break;
       }
+      if (lane == 0) {   // what is in flight has to land before the CTA ends, whatever became of the other roles
+        for (int i = 0; i < 2; ++i)
+          if (q_used[i]) mbar_wait_bounded(&q_full[i], (q_used[i] - 1) & 1, kWaitLimitNs);
+        for (int j = max(0, pos - NS); j < pos; ++j) mbar_wait_bounded(&full[j % NS], (j / NS) & 1, kWaitLimitNs);
+        for (int j = max(0, cleaned - 8); j < cleaned; ++j) mbar_wait_bounded(&v_raw[j & 7], (j >> 3) & 1, kWaitLimitNs);
+      }
+      __syncwarp();
     } else if (warp == 9) {
       // ---------------------------------------------------------------- MMA
       constexpr uint32_t id_s = BF ? tc::idesc_bf16(kM, kKeys) : tc::idesc_f16(kM, kKeys);
