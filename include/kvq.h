@@ -484,15 +484,17 @@ kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride,
  *   t_new       host bound on the lengths, at most KVQ_PROMPT_MAX_TOKENS.  A sequence that is
  *               longer, or whose rows are not all in 0..num_rows - 1, is skipped and
  *               sets KVQ_STATUS_BAD_ROWS.
- *   out         device, rows of num_q_heads heads, in out_dtype (dtype or f32).
+ *   out         device, rows of num_q_heads heads, in out_dtype (dtype or f32); may
+ *               not overlap the inputs.
  *   lse         NULL, or device fp32 [num_rows][num_q_heads]: ln sum_j e^a_ij.
  *   status      device word, OR-ed with KVQ_STATUS_* bits (a cache's status).
  * Rows of out and lse that belong to no sequence are not written; rows of q, k and
  * v that a token does not attend to (later tokens, other sequences, rows of none)
  * never reach it, whatever they hold.  Weights are rounded to the inputs' type
- * (2^-9 relative for bf16, 2^-11 for f16), the sums are fp32.  A token whose
- * scores are all -inf gets 0 and lse -inf.  |v| below 2^100 (the sums before the
- * division are of values up to 2^8 n |v|).  A call that sets KVQ_STATUS_TIMEOUT
+ * (off by at most 2^-8 of each for bf16, 2^-11 for f16; twice that for keys whose
+ * weights a later one within 128 keys exceeds by far), the sums are fp32.  A token
+ * whose scores are all -inf gets 0 and lse -inf.  |v| below 2^90 (the sums before
+ * the division reach 2^10 n |v|).  A call that sets KVQ_STATUS_TIMEOUT
  * leaves NaN in the rows of every CTA that gave up.  One launch. */
 kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                 const void* v, int64_t v_stride, kvq_dtype dtype, int32_t num_q_heads, int32_t num_rows,

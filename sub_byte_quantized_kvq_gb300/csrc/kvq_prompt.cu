@@ -4,28 +4,47 @@
 //   out_i = sum_j e^a_ij v_j / sum_j e^a_ij,  lse_i = ln sum_j e^a_ij
 //
 // A tile is 128 rows: 128 / P consecutive tokens of P query heads of one kv head
-// (P: the power of two in the group size), so short prompts fill tiles too.  A
-// CTA takes two tiles, one behind the other, and goes once over the keys that
-// they see, 128 at a time:
+// (P: the power of two in the group size), so short prompts fill tiles too.  One
+// CTA an SM takes pairs of tiles, those with the most keys first; a pair's two
+// tiles lie behind one another and go once over the keys that they see, 128 at a
+// time:
 //
-//   load warp     Q, K and V tiles by tiled TMA with 128-byte swizzle, straight
-//                 from the caller's rows (any row stride); K and V in one ring
+//   load warp     finds the pairs; Q, K and V tiles by tiled TMA with 128-byte
+//                 swizzle, straight from the caller's rows (any row stride); K and
+//                 V in one ring of five 32 KB tiles (D = 64: eight of 16 KB)
 //   MMA warp      S = Q K^T (both from shared memory), O += P V with P from tensor
-//                 memory and V as it lies, [token][channel]; one tile's MMAs run
-//                 while the other's softmax does
-//   2 x 4 softmax warps, one row a thread: the row of S in registers, its maximum,
-//                 p = 2^(a - m), P into tensor memory.  m is raised only when the
-//                 sums ask for it (rare after the first keys); the warp then scales
-//                 O.  At the end O / l goes to global memory
-//   2 cleaning warps  V tiles with rows that not all of the CTA's tokens see: a
+//                 memory and V as it lies, [token][channel]
+//   2 x 4 softmax warps, a warpgroup a tile, one row a thread: 128 scores in
+//                 registers, p = 2^(a - m), P into tensor memory.  m is raised only
+//                 when the sums ask for it (rare after the first keys); the warp
+//                 then scales O.  At the end O / l goes to global memory
+//   2 cleaning warps  V tiles with rows that not all of the pair's tokens see: a
 //                 weight of 0 times what may lie there (infinities, NaN, stale
 //                 memory) has to stay 0.  Rows past the sequence become zeros;
 //                 infinities and NaN in rows of later tokens too, and the tokens
 //                 that do see them get them added at the end
 //
-// Precision: products of the inputs are exact in fp32, S, m, l and O are fp32; P
-// is rounded to the inputs' type (fp16 biased by 2^6, so that small p keep their
-// bits: p <= 2^14).
+// Precision: products of the inputs are exact in fp32, S, m, l and O are fp32.  P
+// is rounded to the inputs' type, as the MMA takes it: off by at most 2^-8 (bf16) or
+// 2^-11 (fp16) of each weight, as an output of that type is itself, and averaged
+// over the keys; l adds the weights before they are rounded.  fp16 weights are
+// biased by 2^6, so that small ones keep their bits (a half's sum stays below 2^15).
+//
+// What bounds it: MMA time and the power limit for long prompts, the ends of pairs
+// for shorter ones.  128 keys of a pair are 2048 cycles of MMAs (D = 128), measured
+// as 2100 to 2300 (S reads both operands from shared memory), and take 2600: the
+// softmax of a tile (16384 exponentials at 16 a cycle and SM are 1024 cycles, with
+// the fused multiply-adds, sums and conversions about 700 a half for all four warps
+// of a scheduler) runs beside the other tile's MMAs, and each hand-over between the
+// roles costs about 200.  A pair costs 5000 to 8000 cycles at its ends (first
+// softmax, output of 64 KB, cleaning of the last V tiles).
+//   32768 tokens, 64 heads of 128, causal: 10.4 to 10.7 ms, 1.65 to 1.70 PFLOP/s (a
+//   library product of 8192^3 holds 1.74 under the same power limit)
+//   8 x 4096, 32 heads: 740 us, 1.49 PFLOP/s;  17 tokens: 5.7 us
+// What carried it: the MMAs issued by one elected lane of a converged warp (130 ->
+// 64 cycles an MMA of N = 128; 12.2 -> 11.1 ms), one place for both tiles' S and no
+// maximum in the common path (10.7 ms), S a step ahead of PV (17 tokens: 6.9 -> 5.7
+// us), all weights computed before the wait for the last PV (10.4 ms).
 #include <algorithm>
 #include <mutex>
 
@@ -103,7 +122,8 @@ __device__ __forceinline__ float2 unpack_p(uint32_t u) {
 // 256, and of those the pairs with the most keys first (later ones then fill the gaps that they leave), none for what a
 // sequence does not have.  With T_b pairs of `span` tokens in sequence b, count(L) = sum_b max(0, T_b - L) pairs lie at L or
 // later in their sequences; the rank-th is at the largest L with count(L) > rank.  By one warp, the 256 sequences' T_b in
-// registers: asked for rising ranks, it reads each sequence's length once.
+// registers: asked for rising ranks, it reads each sequence's length once (2048 sequences of up to 200 tokens: 1.03 ms; with
+// the lengths behind the 256th read again for each pair 10.5 ms).
 struct Finder {
   static constexpr int R = 8;
   const PromptArgs& a;
@@ -325,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         // Half of the keys at a time.  No maximum is taken in the common path: a half whose sum passes kMost (rare; whatever P
         // could not hold is among them) raises m to its maximum, scales l, O and the first half's weights, and is computed
-        // again.  PV(it - 1), which reads P and adds to O, is waited for when the weights are ready to go over P.
+        // again.  (The first half's weights are then rounded a second time: half a step more, where m jumps within 128 keys.)
+        // PV(it - 1), which reads P and adds to O, is waited for when the weights are ready to go over P.
         const int before = (done + it - 1) & 1;
         const uint64_t f2 = pack2(f, f);
         uint32_t w[4][16];
@@ -739,7 +760,9 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
     const long long span = (long long)tiles * p.tokens;
     return std::min((long long)a.B * ((a.t_new + span - 1) / span), a.rows / span + a.B);
   };
-  p.tiles = ctas(2) * p.units >= sms ? 2 : 1;   // one tile a CTA where two would leave SMs idle
+  // One tile a CTA where pairs would leave SMs idle.  8 kv heads x 4, D 128, pairs and single tiles: 1024 tokens (128 pairs)
+  // 19.1 and 18.2 us, 1536 (192 pairs) 26.3 and 31.0, 2048 32.0 and 42.9; one kv head of 64 channels, 2048 tokens 21.3 and 18.2.
+  p.tiles = ctas(2) * p.units >= sms ? 2 : 1;
   const long long pairs = ctas(p.tiles) * p.units;
   if (pairs > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;   // (more rows or heads than memory holds)
   p.pairs = (int)pairs;

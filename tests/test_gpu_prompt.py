@@ -299,6 +299,25 @@ def test_long_prompt_sampled():
         assert ((out[i].double() - y).abs() <= bound).all() and ((lse[0, i].double() - z).abs() <= zbound).all()
 
 
+def test_rows_far_apart():
+    """Rows so far apart that their elements lie behind 2^31, of the inputs and of out."""
+    rows, step, Hq, Hkv, D, lens, first = 700, 1 << 22, 2, 1, 64, [130, 40], [560, 3]
+    q, k, v = inputs(rows, Hq, Hkv, D, BF, 13)
+    want = torch.full((rows, Hq, D), 7.0, dtype=BF, device="cuda")
+    n, f = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lens, first)]
+    cache = handle(2, Hkv, D)
+    kvq.kvq_prompt_attention(cache, q, k, v, 0.125, t_per_seq=n, first_row=f, t_new=130, out=want)
+    wide = torch.empty((rows, step), dtype=BF, device="cuda")
+    parts, at = [], 0
+    for x in (q, k, v, want):
+        parts.append(wide[:, at:at + x[0].numel()].unflatten(1, x.shape[1:]))
+        at += x[0].numel()
+        parts[-1].copy_(x)
+    parts[3].fill_(7)
+    kvq.kvq_prompt_attention(cache, *parts[:3], 0.125, t_per_seq=n, first_row=f, t_new=130, out=parts[3])
+    assert torch.equal(parts[3], want) and cache.status_word() == 0
+
+
 def test_graph_streams_and_repeats():
     gen_lens = [700, 33]
     out, lse, q, k, v, first, scale = run(gen_lens, 2, 4, 128)

@@ -126,6 +126,22 @@ def test_outputs_with_gaps():
     assert torch.equal(y, z)
 
 
+def test_rows_far_apart():
+    """Rows so far apart that their elements lie behind 2^31, of the inputs and of the outputs."""
+    rows, step, Hq, Hkv, D = 601, 1 << 22, 3, 1, 64
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    q, k = [torch.randn((rows, h, D), generator=gen, device="cuda").to(BF) for h in (Hq, Hkv)]
+    pos, f, cache = torch.arange(rows, device="cuda", dtype=torch.int32), freqs(D), handle(Hkv, D)
+    want = kvq.kvq_norm_rope(cache, q, k, pos, f)
+    wide = torch.empty((rows, step), dtype=BF, device="cuda")
+    qi, ki = wide[:, :Hq * D].unflatten(1, (Hq, D)), wide[:, Hq * D:(Hq + Hkv) * D].unflatten(1, (Hkv, D))
+    qo, ko = wide[:, 512:512 + Hq * D].unflatten(1, (Hq, D)), wide[:, 512 + Hq * D:512 + (Hq + Hkv) * D].unflatten(1, (Hkv, D))
+    qi.copy_(q)
+    ki.copy_(k)
+    kvq.kvq_norm_rope(cache, qi, ki, pos, f, q_out=qo, k_out=ko)
+    assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
+
+
 def test_special_values():
     """A NaN or an infinity stays in its head; rows of zeros stay zero; channels behind rot_dim do not meet the rotation."""
     D, R = 128, 32
