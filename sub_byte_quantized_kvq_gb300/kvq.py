@@ -521,6 +521,8 @@ def _token_rows(t: torch.Tensor, heads: int, D: int):
     if t.is_contiguous():
         return t.numel() // (heads * D), heads * D
     strides = t.stride()
+    if len(shape) == 3 and strides[2] == 1 and (heads == 1 or strides[1] == D):   # (what the loop below says, for one dimension)
+        return shape[0], strides[0] if shape[0] != 1 else heads * D
     rows, step = 1, None
     for i in range(len(shape) - 3, -1, -1):
         n = shape[i]
@@ -632,13 +634,14 @@ def kvq_prompt_attention(cache: QuantizedKVCache, q: torch.Tensor, k: torch.Tens
     if t_per_seq is not None:
         assert t_per_seq.dtype is torch.int32 and t_per_seq.is_contiguous() and t_per_seq.shape == (B,)
     rows, qs = _token_rows(q, Hq, D)
-    _, ks = _token_rows(k, cfg.num_kv_heads, D)
-    _, vs = _token_rows(v, cfg.num_kv_heads, D)
+    kshape, Hkv = k.shape, cfg.num_kv_heads
+    _, ks = _token_rows(k, Hkv, D)
+    _, vs = _token_rows(v, Hkv, D)
     if out is None:
         made = out_dtype or dtype
         out = _made_on(stream, lambda: torch.empty(shape, dtype=made, device=q.device), returned=True)
     od = out.dtype
-    assert k.shape[:-2] == shape[:-2] and v.shape[:-2] == shape[:-2] and out.shape == shape
+    assert kshape[:-2] == shape[:-2] and v.shape == kshape and out.shape == shape
     assert (od is dtype or od is torch.float32) and out_dtype in (None, od)
     _, outs = _token_rows(out, Hq, D)
     if lse is not None:
