@@ -81,6 +81,7 @@ struct Launch {
   int units;              // Hq / P
   int wide;               // rows of out are 32-byte aligned
   int pairs;              // tile pairs of all units, at most
+  int seqs, hu, parts;    // sequences and units that are taken together; such parts of the units
 };
 
 struct Wait {
@@ -118,29 +119,37 @@ __device__ __forceinline__ float2 unpack_p(uint32_t u) {
   return __half22float2(u32_as_h2(u));
 }
 
-// A tile pair's sequence and the first of its tokens, by its rank among all pairs of a head: 256 sequences after the other
-// 256, and of those the pairs with the most keys first (later ones then fill the gaps that they leave), none for what a
-// sequence does not have.  With T_b pairs of `span` tokens in sequence b, count(L) = sum_b max(0, T_b - L) pairs lie at L or
-// later in their sequences; the rank-th is at the largest L with count(L) > rank.  By one warp, the 256 sequences' T_b in
-// registers: asked for rising ranks, it reads each sequence's length once (2048 sequences of up to 200 tokens: 1.03 ms; with
-// the lengths behind the 256th read again for each pair 10.5 ms).
+// What the roles know of a tile pair: the sequence's first row and length (0: no more tiles), the first token, and the
+// heads (unit u: query heads u P .. u P + P - 1).
+struct Pair {
+  int first, n, t0, unit;
+};
+
+// The order of the pairs.  `seqs` sequences and `heads` kv heads are taken at a time: their K and V are about 32 MB (one
+// sequence and kv head at least), so that the CTAs, which go through them together, find them in L2.  Under the power limit
+// 8 x 4096 tokens of 8 kv heads take 778 us with 16 MB at a time and 863 with all 134 MB, 32768 tokens of 8 kv heads 11022,
+// 10875, 10852 and 10899 us with 134, 67, 34 and 17 MB.  Within such a part the pairs with the most keys come first (later
+// ones then fill the gaps that they leave); every other part goes backwards, so that the pairs of one round of CTAs are
+// alike at its borders too, the last one forwards.
+//
+// Sequence b has T_b pairs of `span` tokens (none for what it does not have); count(L) = sum_b max(0, T_b - L) pairs of a head
+// lie at L or later in their sequences, and the rank-th is at the largest L with count(L) > rank.  By one warp, the T_b of up
+// to 256 sequences in registers: asked for rising indices, it reads each length once (2048 sequences of up to 200 tokens:
+// 1.03 ms; with the lengths behind the 256th read again for each pair 10.5 ms).
 struct Finder {
   static constexpr int R = 8;
+  const Launch& p;
   const PromptArgs& a;
-  int log_span, lane, T[R];
-  int seq0 = -32 * R;      // the first of the 256 sequences
-  unsigned rank0 = 0, n = 0;   // rank of their first pair, and their pairs
-  bool even;               // every sequence has t_new tokens
-  __device__ __forceinline__ int tiles_of(int s) const {
-    long long f;
-    int len;
-    bool bad;
-    return s < a.B && prompt_rows(a, s, f, len, bad) ? ((len - 1) >> log_span) + 1 : 0;
-  }
-  __device__ __forceinline__ void read() {
+  int lane, most, T[R];
+  int seq0;                    // the first of the `seqs` sequences
+  unsigned item0 = 0, n = 0;   // their first item (pair x unit), and their pairs of a head
+  bool even;                   // every sequence has t_new tokens
+  __device__ __forceinline__ Finder(const Launch& launch, int ln) : p(launch), a(launch.a), lane(ln) {
+    most = ((a.t_new - 1) >> p.log_span) + 1;
+    seq0 = -p.seqs;
+    even = !a.lens && !a.first && (long long)a.B * a.t_new <= a.rows;
 #pragma unroll
-    for (int k = 0; k < R; ++k) T[k] = tiles_of(seq0 + lane + 32 * k);
-    n = count(0);
+    for (int k = 0; k < R; ++k) T[k] = 0;
   }
   __device__ __forceinline__ unsigned count(int L) const {
     unsigned c = 0;
@@ -148,73 +157,85 @@ struct Finder {
     for (int k = 0; k < R; ++k) c += max(0, T[k] - L);
     return __reduce_add_sync(0xffffffffu, c);
   }
-  __device__ __forceinline__ Finder(const PromptArgs& args, int log_sp, int ln) : a(args), log_span(log_sp), lane(ln) {
-    even = !a.lens && !a.first && (long long)a.B * a.t_new <= a.rows;
-  }
-  // The pairs of a head are below 2^31 (checked by the launch), so 32 bits count them.
-  __device__ __forceinline__ bool find(unsigned rank, int& b, int& t0) {
-    const int most = ((a.t_new - 1) >> log_span) + 1;
+  // The pair of item i (indices below 2^31, checked by the launch).
+  __device__ __forceinline__ bool find(unsigned i, Pair& r) {
+    long long first;
+    bool bad;
     if (even) {
-      b = (int)(rank % (unsigned)a.B);
-      t0 = (most - 1 - (int)(rank / (unsigned)a.B)) << log_span;
-      return t0 >= 0;
-    }
+      const unsigned per = (unsigned)most * p.seqs * p.units, g = i / per;
+      seq0 = (int)g * p.seqs;
+      item0 = g * per;
+      if (seq0 >= a.B) return false;
+      n = (unsigned)most * min(p.seqs, a.B - seq0);
+    } else {
 #pragma unroll 1
-    while (rank - rank0 >= n) {
-      if (a.B - 32 * R <= seq0) return false;
-      rank0 += n;
-      seq0 += 32 * R;
-      read();
-    }
-    int lo = 0, hi = most;     // count(lo) > rank - rank0 >= count(hi)
-    unsigned above = 0;        // count(hi)
-#pragma unroll 1
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      const unsigned c = count(mid);
-      if (c > rank - rank0) {
-        lo = mid;
-      } else {
-        hi = mid;
-        above = c;
-      }
-    }
-    int left = (int)(rank - rank0 - above);   // which of the sequences with more than lo pairs
-    b = 0;
+      while (i - item0 >= n * p.units) {
+        if (a.B - seq0 <= p.seqs) return false;
+        item0 += n * p.units;
+        seq0 += p.seqs;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      unsigned has = __ballot_sync(0xffffffffu, T[k] > lo);
-      if (left >= 0 && left < __popc(has)) {
-#pragma unroll 1
-        for (int i = left; i > 0; --i) has &= has - 1;
-        b = seq0 + 32 * k + __ffs((int)has) - 1;
-        left = -1;
-      } else if (left >= 0) {
-        left -= __popc(has);
+        for (int k = 0; k < R; ++k) {
+          const int j = lane + 32 * k, s = seq0 + j;
+          int len;
+          T[k] = j < p.seqs && s < a.B && prompt_rows(a, s, first, len, bad) ? ((len - 1) >> p.log_span) + 1 : 0;
+        }
+        n = count(0);
       }
     }
-    t0 = lo << log_span;
+    const unsigned q = i - item0, part = q / (n * p.hu), inside = q - part * n * p.hu;
+    const unsigned hw = min(p.hu, p.units - (int)part * p.hu);   // units of this part
+    unsigned rank = inside / hw;
+    r.unit = (int)(part * p.hu + inside - rank * hw);
+    if (((a.B - 1 - seq0) / p.seqs + 1) * p.parts - 1 - (int)part & 1) rank = n - 1 - rank;
+    int b;
+    if (even) {
+      const unsigned width = min(p.seqs, a.B - seq0), level = rank / width;
+      b = seq0 + (int)(rank - level * width);
+      r.t0 = (most - 1 - (int)level) << p.log_span;
+    } else {
+      int lo = 0, hi = most;     // count(lo) > rank >= count(hi)
+      unsigned above = 0;        // count(hi)
+#pragma unroll 1
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        const unsigned c = count(mid);
+        if (c > rank) {
+          lo = mid;
+        } else {
+          hi = mid;
+          above = c;
+        }
+      }
+      int left = (int)(rank - above);   // which of the sequences with more than lo pairs
+      b = 0;
+#pragma unroll 1
+      for (int j = 0; j < p.seqs; j += 32) {
+        const int s = seq0 + j + lane;
+        int len;
+        unsigned has = __ballot_sync(0xffffffffu, j + lane < p.seqs && s < a.B && prompt_rows(a, s, first, len, bad) && (len - 1) >> p.log_span >= lo);
+        const int c = __popc(has);
+        if (left < c) {
+#pragma unroll 1
+          for (; left > 0; --left) has &= has - 1;
+          b = seq0 + j + __ffs((int)has) - 1;
+          break;
+        }
+        left -= c;
+      }
+      r.t0 = lo << p.log_span;
+    }
+    prompt_rows(a, b, first, r.n, bad);
+    r.first = (int)first;
     return true;
   }
 };
 
-// What the roles know of a tile pair: the sequence's first row and length (0: no more tiles), the first token, and the
-// heads (unit u: query heads u P .. u P + P - 1).
-struct Pair {
-  int first, n, t0, unit;
-};
 // The k-th pair of this CTA: every round of the grid's CTAs takes the next ones in the finder's order, odd rounds
 // backwards, so that no CTA has the longer one each time.
 __device__ __forceinline__ Pair next_pair(const Launch& p, Finder& finder, unsigned k) {
   const unsigned i = k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);   // below 2^31 + 2 grids
-  Pair r = {0, 0, 0, (int)(i % (unsigned)p.units)};
-  int b;
-  if (i < (unsigned)p.pairs && finder.find(i / (unsigned)p.units, b, r.t0)) {
-    long long first;
-    bool bad;
-    prompt_rows(p.a, b, first, r.n, bad);
-    r.first = (int)first;
-  }
+  Pair r = {0, 0, 0, 0};
+  if (i < (unsigned)p.pairs) finder.find(i, r);
   return r;
 }
 
@@ -469,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (warp == 8) {
       // ---------------------------------------------------------------- pairs, and loads through the ring
       int q_used[2] = {0, 0};
-      Finder finder(a, p.log_span, lane);
+      Finder finder(p, lane);
       for (int pk = 0; ok; ++pk) {
         pair = next_pair(p, finder, pk);
         if (lane == 0) {
@@ -696,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
   if (*stop) {   // nothing that a wait gave up on is taken for a result
-    Finder finder(a, p.log_span, lane);
+    Finder finder(p, lane);
     for (int pk = 0;; ++pk) {
       pair = next_pair(p, finder, pk);   // (every warp by itself)
       if (pair.n == 0) break;
@@ -767,6 +788,12 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
   if (pairs > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;   // (more rows or heads than memory holds)
   p.pairs = (int)pairs;
   p.log_span = 7 - p.log_p + (p.tiles == 2);
+  const int tokens = std::max(1, (int)std::min((long long)a.t_new, (long long)a.rows / a.B));   // of a sequence, about
+  const int at_once = std::max(1, (32 << 20) / (4 * D * a.Hkv));                                // whose K and V are 32 MB
+  p.seqs = std::min({a.B, 256, std::max(1, at_once / tokens)});
+  const int heads = tokens <= at_once ? a.Hkv : std::max(1, (int)((long long)at_once * a.Hkv / tokens));
+  p.hu = heads * (p.units / a.Hkv);
+  p.parts = (a.Hkv + heads - 1) / heads;
   const unsigned grid = (unsigned)std::min(p.pairs, sms);
   if (!encode(&p.q, a.q, BF, D, a.Hq, a.rows, a.q_stride, p.P, p.tokens) || !encode(&p.k, a.k, BF, D, a.Hkv, a.rows, a.k_stride, 1, kKeys) ||
       !encode(&p.v, a.v, BF, D, a.Hkv, a.rows, a.v_stride, 1, kKeys))

@@ -299,6 +299,34 @@ def test_long_prompt_sampled():
         assert ((out[i].double() - y).abs() <= bound).all() and ((lse[0, i].double() - z).abs() <= zbound).all()
 
 
+@pytest.mark.parametrize("lens,padded", [([20011, 5, 0, 12000], False), ([9001, 9001], True), ([3001] * 7, True), ([2999, 3100] * 4, False),
+                                         ([70, 9100, 130], False)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_keys_than_are_taken_at_once(lens, padded, causal):
+    """K and V far beyond what the order of the pairs takes at a time: each head's rows are, bit for bit, those of a call of its
+    own, and every row is written."""
+    B, Hkv, G, D = len(lens), 8, 2 if padded else 1, 128
+    first = torch.tensor([sum(lens[:b]) for b in range(B)], dtype=torch.int32, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q, k, v = inputs(sum(lens), Hkv * G, Hkv, D, BF, 21)
+    def attend(Hkv, q, k, v):
+        lse = torch.full(q.shape[:2], 7.0, device="cuda")
+        if padded:
+            shape = (B, lens[0])
+            out = kvq.kvq_prompt_attention(handle(B, Hkv, D), *[x.unflatten(0, shape) for x in (q, k, v)], 0.09, causal=causal, lse=lse.unflatten(0, shape))
+            return out.flatten(0, 1), lse
+        return kvq.kvq_prompt_attention(handle(B, Hkv, D), q, k, v, 0.09, t_per_seq=n, first_row=first, t_new=max(lens), causal=causal, lse=lse), lse
+    out, lse = attend(Hkv, q, k, v)
+    assert (lse != 7).all()
+    for h in range(Hkv):
+        heads = slice(h * G, h * G + G)
+        o, z = attend(1, q[:, heads], k[:, h:h + 1], v[:, h:h + 1])
+        assert torch.equal(out[:, heads], o) and torch.equal(lse[:, heads], z)
+    s = slice(0, min(lens[0], 2000))
+    if causal:
+        check(out[s], lse[s], q[s], k[s], v[s], 0.09, True)
+
+
 def test_rows_far_apart():
     """Rows so far apart that their elements lie behind 2^31, of the inputs and of out."""
     rows, step, Hq, Hkv, D, lens, first = 700, 1 << 22, 2, 1, 64, [130, 40], [560, 3]
