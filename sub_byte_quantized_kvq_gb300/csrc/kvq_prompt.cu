@@ -5,7 +5,7 @@
 //
 // A tile is 128 rows: 128 / P consecutive tokens of P query heads of one kv head
 // (P: the power of two in the group size), so short prompts fill tiles too.  One
-// CTA an SM takes pairs of tiles, those with the most keys first; a pair's two
+// CTA an SM takes pairs of tiles, in parts whose keys stay in L2; a pair's two
 // tiles lie behind one another and go once over the keys that they see, 128 at a
 // time:
 //
@@ -38,13 +38,16 @@
 // of a scheduler) runs beside the other tile's MMAs, and each hand-over between the
 // roles costs about 200.  A pair costs 5000 to 8000 cycles at its ends (first
 // softmax, output of 64 KB, cleaning of the last V tiles).
-//   32768 tokens, 64 heads of 128, causal: 10.4 to 10.7 ms, 1.65 to 1.70 PFLOP/s (a
+//   32768 tokens, 64 heads of 128, causal: 10.2 to 10.4 ms, 1.69 to 1.73 PFLOP/s (a
 //   library product of 8192^3 holds 1.74 under the same power limit)
-//   8 x 4096, 32 heads: 740 us, 1.49 PFLOP/s;  17 tokens: 5.7 us
+//   8 x 4096, 32 heads: 700 us, 1.57 PFLOP/s (760 without a pause);  17 tokens: 5.7 us
 // What carried it: the MMAs issued by one elected lane of a converged warp (130 ->
 // 64 cycles an MMA of N = 128; 12.2 -> 11.1 ms), one place for both tiles' S and no
 // maximum in the common path (10.7 ms), S a step ahead of PV (17 tokens: 6.9 -> 5.7
-// us), all weights computed before the wait for the last PV (10.4 ms).
+// us), all weights computed before the wait for the last PV (10.4 ms), pairs in
+// parts that L2 holds (8 x 4096: 740 -> 700 us, without a pause 830 -> 760).  The
+// compiled softmax changes by up to 8% with code elsewhere in the kernel: time
+// every change.
 #include <algorithm>
 #include <mutex>
 
@@ -130,7 +133,7 @@ struct Pair {
 // 8 x 4096 tokens of 8 kv heads take 778 us with 16 MB at a time and 863 with all 134 MB, 32768 tokens of 8 kv heads 11022,
 // 10875, 10852 and 10899 us with 134, 67, 34 and 17 MB.  Within such a part the pairs with the most keys come first (later
 // ones then fill the gaps that they leave); every other part goes backwards, so that the pairs of one round of CTAs are
-// alike at its borders too, the last one forwards.
+// alike at its borders too, the last one forwards.  (Measured with closed forms of this order, on one GPU without a pause.)
 //
 // Sequence b has T_b pairs of `span` tokens (none for what it does not have); count(L) = sum_b max(0, T_b - L) pairs of a head
 // lie at L or later in their sequences, and the rank-th is at the largest L with count(L) > rank.  By one warp, the T_b of up
