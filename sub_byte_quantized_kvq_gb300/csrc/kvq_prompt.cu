@@ -128,12 +128,13 @@ struct Pair {
   int first, n, t0, unit;
 };
 
-// The order of the pairs.  `seqs` sequences and `heads` kv heads are taken at a time: their K and V are about 32 MB (one
-// sequence and kv head at least), so that the CTAs, which go through them together, find them in L2.  Under the power limit
-// 8 x 4096 tokens of 8 kv heads take 778 us with 16 MB at a time and 863 with all 134 MB, 32768 tokens of 8 kv heads 11022,
-// 10875, 10852 and 10899 us with 134, 67, 34 and 17 MB.  Within such a part the pairs with the most keys come first (later
+// The order of the pairs.  `seqs` sequences and `heads` kv heads are taken at a time: their K and V are about 24 MB (one
+// sequence and kv head at least), so that the CTAs, which go through them together, find them in L2.  Calls without a pause,
+// under the power limit, on one GPU: 8 x 4096 tokens of 8 kv heads 840 us with all 134 MB, 780 with 64 MB at a time, 769 with
+// 32, 764 with 24 and 16; 32768 tokens 10860, 10570, 10690, 10660 and 10660 us; 16 ragged sequences of up to 6007 1500, 1465,
+// 1477, 1467 and 1497 us (shorter parts have more ends).  Within such a part the pairs with the most keys come first (later
 // ones then fill the gaps that they leave); every other part goes backwards, so that the pairs of one round of CTAs are
-// alike at its borders too, the last one forwards.  (Measured with closed forms of this order, on one GPU without a pause.)
+// alike at its borders too, the last one forwards.
 //
 // Sequence b has T_b pairs of `span` tokens (none for what it does not have); count(L) = sum_b max(0, T_b - L) pairs of a head
 // lie at L or later in their sequences, and the rank-th is at the largest L with count(L) > rank.  By one warp, the T_b of up
@@ -792,9 +793,9 @@ static cudaError_t launch(const PromptArgs& a, cudaStream_t st) {
   p.pairs = (int)pairs;
   p.log_span = 7 - p.log_p + (p.tiles == 2);
   const int tokens = std::max(1, (int)std::min((long long)a.t_new, (long long)a.rows / a.B));   // of a sequence, about
-  const int at_once = std::max(1, (32 << 20) / (4 * D * a.Hkv));                                // whose K and V are 32 MB
+  const int at_once = std::max(1, (24 << 20) / (4 * D * a.Hkv));                                // whose K and V are 24 MB
   p.seqs = std::min({a.B, 256, std::max(1, at_once / tokens)});
-  const int heads = tokens <= at_once ? a.Hkv : std::max(1, (int)((long long)at_once * a.Hkv / tokens));
+  const int heads = a.Hkv / std::min(a.Hkv, (tokens - 1) / at_once + 1);                        // parts alike, but for the last
   p.hu = heads * (p.units / a.Hkv);
   p.parts = (a.Hkv + heads - 1) / heads;
   const unsigned grid = (unsigned)std::min(p.pairs, sms);
