@@ -419,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
                 tc::st16(to + c, o);
               }
+              tc::wait_st();   // the second half may scale O again: a load is behind a store only if that is waited for
             }
           }
           l += sum;

@@ -199,6 +199,26 @@ def test_scores_that_jump_within_a_tile():
             run_and_check([12 * 64, 100], 1, 2, D, dtype=dtype, causal=causal, scale=1.0, change=change, seed=2)
 
 
+@pytest.mark.parametrize("dtype,D,G", [(BF, 128, 1), (HF, 64, 4), (BF, 64, 2), (HF, 128, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_scores_that_jump_in_both_halves_of_a_tile(dtype, D, G, causal):
+    """Behind the first tile, both halves of a tile raise the maximum of rows of one warp: every third token in the first
+    half, every third in the second, every third in both.  O is then scaled twice in a row, by 1 where a row does not jump."""
+    first_half = torch.tensor([0, 0, 40, 40, 90, 90, 90, 90, 130, 130, 0, 0], dtype=torch.float32, device="cuda")
+    second_half = torch.tensor([0, 0, 0, 30, 30, 75, 75, 75, 75, 110, 110, 0], dtype=torch.float32, device="cuda")
+    n = 64 * first_half.numel()
+    def change(q, k, v, first):
+        s = slice(first[0], first[0] + n)
+        q.mul_(0.05)
+        q[..., :2] = 0.0
+        third = torch.arange(n, device="cuda") % 3
+        q[s, :, 0] = (third != 1).to(q.dtype)[:, None]
+        q[s, :, 1] = (third != 0).to(q.dtype)[:, None]
+        for c, steps in enumerate((first_half, second_half)):
+            k[s, :, c] = steps.repeat_interleave(64)[:, None].to(k.dtype)
+    run_and_check([n, 100], 1, G, D, dtype=dtype, causal=causal, scale=1.0, change=change, seed=6)
+
+
 def test_scores_of_minus_infinity():
     """Keys that score -inf have no weight; a token that sees no other gets 0 and lse -inf."""
     n, m, G, D = 700, 333, 2, 128
