@@ -517,6 +517,7 @@ struct SoftmaxRow {
         if (o_ready)
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) scale_columns(to + 16 * k, alpha);
+        tc::wait_st();   // the earlier chunks' P: a load is behind a store only if that is waited for
 #pragma unroll 1
         for (int k = c_lo / 32; k < c / 32; ++k) scale_p(ts + 16 * k, alpha);
         tc::wait_st();

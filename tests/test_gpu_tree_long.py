@@ -16,8 +16,8 @@ FORMATS = dict(int4=kvq.KVQ_FMT_INT4_G32, e2m1=kvq.KVQ_FMT_FP4_E2M1_S16, cb2=kvq
                cb2s=kvq.KVQ_FMT_CB2_STATIC, a3=kvq.KVQ_FMT_ASYM3_OUTLIER, cb2g=kvq.KVQ_FMT_CB2_GROUP4)
 
 
-def filled(fmt, lens, Hkv, D, seed=1):
-    """A cache of random tokens; every seventh page of a tiered one is an FP8 page."""
+def filled(fmt, lens, Hkv, D, seed=1, change=None):
+    """A cache of random tokens; every seventh page of a tiered one is an FP8 page.  change(k, v): edits of them."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     B, L = len(lens), max(lens)
     P = -(-L // 16) + 3
@@ -29,6 +29,8 @@ def filled(fmt, lens, Hkv, D, seed=1):
     cache = kvq.QuantizedKVCache(fmt, B, Hkv, D, P, B * P, int(tiers.sum()), page_table=pt,
                                  static_channels=2 if fmt == kvq.KVQ_FMT_CB2_STATIC else 0)
     k, v = [torch.randn((B, L, Hkv, D), generator=g, device="cuda") for _ in range(2)]
+    if change:
+        change(k, v)
     if fmt == kvq.KVQ_FMT_CB2_STATIC:
         kvq.kvq_select_static_channels(cache, k[0, :64].contiguous(), v[0, :64].contiguous())
     kvq.kvq_quantize_append(cache, k, v, torch.tensor(lens, dtype=torch.int32, device="cuda"))
@@ -67,6 +69,30 @@ def test_many_tiles(name, D):
         e_out, e_lse, weight, reach = exact(cache, lens, q, scale)
         E = scale * (D + 4) * 2.0 ** -23 * reach
         for splits in (1, 2, 0):
+            lse = torch.empty((2, T, Hq), device="cuda")
+            out = kvq.kvq_tree_attention(cache, q, scale, max(lens), num_splits=splits, out_dtype=torch.float32, lse=lse)
+            assert ((out - e_out).abs() <= 2 * (2 * E[..., None] + 2.0 ** -20 + 2.0 ** -10) * weight).all()
+            assert ((lse - e_lse).abs() <= E + 2.0 ** -20 + 2.0 ** -22 * e_lse.abs()).all()
+    assert cache.status_word() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("name", list(FORMATS))
+def test_scores_that_jump_between_the_chunks_of_a_tile(name, D):
+    """Each run of 64 tokens scores far above the one before, for every second node: the maximum rises between the chunks of
+    a tile, whose earlier weights are then scaled where they lie, by 1 for the nodes that do not jump."""
+    lens, Hkv, scale = [7 * 64 + 50, 300], 2, D ** -0.5
+    def change(k, v):
+        run = torch.arange(k.shape[1], device="cuda") // 64
+        k[..., 0] = (12.0 * 2.0 ** run)[None, :, None]
+    cache, g = filled(FORMATS[name], lens, Hkv, D, seed=3, change=change)
+    for T, Hq in ((3, 16), (16, 16), (33, 16)):
+        q = (2 * torch.randn((2, T, Hq, D), generator=g, device="cuda")).to(torch.bfloat16)
+        q[..., 0] = 0
+        q[:, ::2, :, 0] = 1 / scale
+        e_out, e_lse, weight, reach = exact(cache, lens, q, scale)
+        E = scale * (D + 4) * 2.0 ** -23 * reach
+        for splits in (1, 0):
             lse = torch.empty((2, T, Hq), device="cuda")
             out = kvq.kvq_tree_attention(cache, q, scale, max(lens), num_splits=splits, out_dtype=torch.float32, lse=lse)
             assert ((out - e_out).abs() <= 2 * (2 * E[..., None] + 2.0 ** -20 + 2.0 ** -10) * weight).all()
