@@ -137,20 +137,23 @@ struct Pair {
 // alike at its borders too, the last one forwards.
 //
 // Sequence b has T_b pairs of `span` tokens (none for what it does not have); count(L) = sum_b max(0, T_b - L) pairs of a head
-// lie at L or later in their sequences, and the rank-th is at the largest L with count(L) > rank.  By one warp, the T_b of up
-// to 256 sequences in registers: asked for rising indices, it reads each length once (2048 sequences of up to 200 tokens:
-// 1.03 ms; with the lengths behind the 256th read again for each pair 10.5 ms).
+// lie at L or later in their sequences, and the rank-th is at the largest L with count(L) > rank.  By one warp, the T_b of 256
+// sequences in registers, however few are taken at a time: asked for rising indices, it reads each length once (2048
+// sequences of up to 200 tokens: 1.03 ms; with the lengths behind the 256th read again for each pair 10.5 ms; 1024
+// sequences of up to 64 tokens, padded to 4096 and so taken one at a time: 278 us; with a load for each of them 562 us).
 struct Finder {
   static constexpr int R = 8;
   const Launch& p;
   const PromptArgs& a;
   int lane, most, T[R];
   int seq0;                    // the first of the `seqs` sequences
+  int at, W[R];                // its place among those whose T_b are in registers
   unsigned item0 = 0, n = 0;   // their first item (pair x unit), and their pairs of a head
   bool even;                   // every sequence has t_new tokens
   __device__ __forceinline__ Finder(const Launch& launch, int ln) : p(launch), a(launch.a), lane(ln) {
     most = ((a.t_new - 1) >> p.log_span) + 1;
     seq0 = -p.seqs;
+    at = 32 * R;
     even = !a.lens && !a.first && (long long)a.B * a.t_new <= a.rows;
 #pragma unroll
     for (int k = 0; k < R; ++k) T[k] = 0;
@@ -177,12 +180,18 @@ struct Finder {
         if (a.B - seq0 <= p.seqs) return false;
         item0 += n * p.units;
         seq0 += p.seqs;
+        at += p.seqs;
+        if (at + p.seqs > 32 * R) {
+          at = 0;
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-          const int j = lane + 32 * k, s = seq0 + j;
-          int len;
-          T[k] = j < p.seqs && s < a.B && prompt_rows(a, s, first, len, bad) ? ((len - 1) >> p.log_span) + 1 : 0;
+          for (int k = 0; k < R; ++k) {
+            const int s = seq0 + lane + 32 * k;
+            int len;
+            W[k] = s < a.B && prompt_rows(a, s, first, len, bad) ? ((len - 1) >> p.log_span) + 1 : 0;
+          }
         }
+#pragma unroll
+        for (int k = 0; k < R; ++k) T[k] = (unsigned)(lane - at + 32 * k) < (unsigned)p.seqs ? W[k] : 0;
         n = count(0);
       }
     }

@@ -266,6 +266,68 @@ def test_runs_of_sequences_without_tokens():
     run_and_check([0] * 300, 1, 1, 64)
 
 
+def padded_and_packed(B, t_new, lens, Hkv, G, D, seed):
+    """The same sequences as a padded batch, NaN behind each, and packed."""
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    first = (n.cumsum(0) - n).to(torch.int32)
+    packed = inputs(sum(lens), Hkv * G, Hkv, D, BF, seed)
+    at = torch.cat([b * t_new + torch.arange(m) for b, m in enumerate(lens)]).cuda()   # of each packed row
+    padded = []
+    for x in packed:
+        y = torch.full((B * t_new, *x.shape[1:]), NAN, dtype=BF, device="cuda")
+        y[at] = x
+        padded.append(y.unflatten(0, (B, t_new)))
+    return n, first, packed, padded, at
+
+
+@pytest.mark.parametrize("B,t_new", [(300, 2400), (67, 12300), (515, 1000)])
+def test_short_prompts_padded_to_a_long_one(B, t_new):
+    """Few sequences are taken at a time where their padded length is long: the same bits as the same sequences packed."""
+    Hkv, G, D = 4, 2, 128
+    lens = torch.randint(0, 65, (B,), generator=torch.Generator().manual_seed(B)).tolist()
+    for b in (3, B // 2, B - 2):
+        lens[b] = t_new - b % 5
+    n, first, packed, padded, at = padded_and_packed(B, t_new, lens, Hkv, G, D, 17)
+    cache, rows = handle(B, Hkv, D), B * t_new
+    wlse = torch.empty((sum(lens), Hkv * G), device="cuda")
+    want = kvq.kvq_prompt_attention(cache, *packed, 0.09, t_per_seq=n, first_row=first, t_new=max(lens), lse=wlse)
+    out, lse = torch.full((rows, Hkv * G, D), 7.0, dtype=BF, device="cuda"), torch.full((rows, Hkv * G), 7.0, device="cuda")
+    kvq.kvq_prompt_attention(cache, *padded, 0.09, t_per_seq=n, out=out.unflatten(0, (B, t_new)), lse=lse.unflatten(0, (B, t_new)))
+    assert torch.equal(out[at], want) and torch.equal(lse[at], wlse) and cache.status_word() == 0
+    out[at], lse[at] = 7.0, 7.0
+    assert (out == 7).all() and (lse == 7).all()
+    for b in (0, 3, B - 1):
+        s = slice(int(first[b]), int(first[b]) + lens[b])
+        check(want[s], wlse[s], *[x[s] for x in packed], 0.09, True)
+
+
+def test_padding_costs_little():
+    """256 prompts of up to 64 tokens take about as long padded to 6200 as packed (and not a memory latency for each sequence more:
+    four times as long)."""
+    B, t_new, Hkv, G, D = 256, 6200, 4, 1, 128
+    lens = torch.randint(1, 65, (B,), generator=torch.Generator().manual_seed(2)).tolist()
+    n, first, packed, padded, _ = padded_and_packed(B, t_new, lens, Hkv, G, D, 18)
+    cache, out, wide = handle(B, Hkv, D), torch.empty_like(packed[0]), torch.empty_like(padded[0])
+    def us(call):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                call()
+        best = math.inf
+        for _ in range(10):
+            a, b = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b) * 200)
+        return best
+    apart = us(lambda: kvq.kvq_prompt_attention(cache, *packed, 0.09, t_per_seq=n, first_row=first, t_new=64, out=out))
+    filled = us(lambda: kvq.kvq_prompt_attention(cache, *padded, 0.09, t_per_seq=n, out=wide))
+    assert filled < 2 * apart, (filled, apart)
+
+
 def test_a_sequence_that_does_not_fit_among_many():
     n, at = 5, 801
     B, Hkv, G, D = 1000, 1, 1, 64
