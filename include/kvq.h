@@ -443,7 +443,7 @@ kvq_status kvq_evict_pages(const kvq_config* cfg, const kvq_cache* cache, const 
  * for the pairs i < rot_dim / 2 of the first rot_dim channels, (a, b) =
  * (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved = 1, and
  *   phi = positions[pair_axis[i]][r] * inv_freq[i]
- * (the product is not rounded to binary32: within 2^-22 of a turn at any int32
+ * (the product is not rounded to binary32: within 2^-27 of a turn at any int32
  * position for |inv_freq| < 2 pi); the channels from rot_dim on are n.
  *   q, k        device, in_dtype (bf16, f16, f32); either may be NULL (its gains
  *               and output are then not read).  The squares of a row must add up

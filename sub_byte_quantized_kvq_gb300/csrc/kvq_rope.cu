@@ -7,10 +7,11 @@
 //
 // Angles: a product in binary32 would be off by 2^-24 phi radians, 0.008 at 128k
 // tokens.  Only phi modulo a turn counts, so a pair's frequency is turned once
-// into a 64-bit fixed-point fraction of a turn per position (in binary64, off by
-// at most 2^-55), and position x fraction modulo 2^64 is one integer product:
-// the phase is good to 2^-24 of a turn at position 2^31 and 2^-40 at 32k.  Its
-// top bits give the quadrant, the rest an angle within an eighth of a turn.
+// into a 64-bit fixed-point fraction of a turn per position (its 24 bits times 96 of
+// 1 / (2 pi), off by at most 2^-63), and position x fraction modulo 2^64 is one
+// integer product: the phase is off by less than 2^-32 of a turn at position 2^31.
+// It is cut to 32 bits; their top gives the quadrant, the rest an angle within an
+// eighth of a turn, which binary32 holds to 2^-28 of a turn.
 //
 // What bounds it: memory.  Each value is read once and written once, 16 bytes a
 // lane; D / 16 lanes hold a head (chunks of 8 channels l and l + R / 16, so a
@@ -78,10 +79,16 @@ __device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&u)[N]) 
   for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(p + 4 * i) = *reinterpret_cast<const uint4*>(u + i);
 }
 
-// A frequency as a fraction of a turn per position, modulo 2^64.
+// A frequency m 2^-s as a fraction of a turn per position, modulo 2^64: m times the first 96 bits of 1 / (2 pi), in whole
+// numbers (off by less than 2^-63 below a frequency of 64, by 2^-32 at 2^55).  In binary64, 1 / (2 pi) rounded once, the
+// fraction is off by up to 2^-52.9 and the phase at position 2^31 by more than 2^-22 of a turn; as two binary64 numbers it
+// takes a decode step 0.5 us longer.
 __device__ __forceinline__ uint64_t turn_per_position(float inv_freq) {
-  const double t = (double)inv_freq * 0.15915494309189533577;   // 1 / (2 pi)
-  return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+  const uint32_t u = __float_as_uint(inv_freq), e = u >> 23 & 255u, m = (u & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int s = max(150 - (int)max(e, 1u), -31);
+  const uint64_t a1 = (uint64_t)m * 0x9391054Au + ((uint64_t)m * 0x7F09D5F4u >> 32), a2 = (uint64_t)m * 0x28BE60DBu + (a1 >> 32);
+  const uint64_t per = s >= 32 ? a2 >> min(s - 32, 63) : a2 << (32 - s) | (a1 << 32) >> (32 + s);
+  return u >> 31 ? 0ull - per : per;
 }
 // sin and cos of position * frequency.
 __device__ __forceinline__ void turn_sincos(int pos, uint64_t per, float& s, float& c) {

@@ -1,4 +1,6 @@
 """kvq_norm_rope against its 64-bit definition."""
+import math
+
 import pytest
 import torch
 
@@ -86,6 +88,28 @@ def test_positions_of_any_size():
     angle = 6.2832 * (2.0 ** -53 * pos.double().abs().cpu()[0] + 2.0 ** -33) + 2.0 ** -53 * 6.25 * pos.double().abs().cpu()[0]
     err = (qo.double().cpu() - y).abs()
     assert (err <= ref.norm_rope_bound(y, size, F32) + angle[:, None, None] * size).all()
+
+
+def test_phase_of_the_farthest_positions():
+    """The phase itself, against exact fractions, at frequencies whose product with a rounded 1 / (2 pi) would be off by more than
+    2^-22 of a turn there: within 2^-27 of a turn at any int32 position."""
+    inv_tau = 0x28BE60DB9391054A7F09D5F47D4D377036D8A5664F10E410   # 1 / (2 pi) 2^192: 2^64 turns' worth of bits behind any product here
+    f = torch.tensor([6.2800726890563965, 6.279623508453369, 6.2367072105407715, 6.252718925476074, -6.282087802886963, -0.9548900127410889,
+                      0.9847080707550049, 1.0, 2.0 ** -20, 1e-6, -1e-6, 1e-30, 0.0, 3.0, 5.5, -2.0 ** -12])
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 123, 1500000001, -2000000011, 1 << 30, 12345, 131071, 1, 0]
+    D, R = 64, 32
+    q = torch.zeros((len(pos), 1, D))
+    q[..., :R // 2] = 1.0
+    qo, _ = kvq.kvq_norm_rope(handle(1, D), q.cuda(), None, torch.tensor(pos, dtype=torch.int32).cuda(), f.cuda(), eps=None)
+    qo = qo.double().cpu()
+    # 2^-27 of a turn, the sine's or cosine's own error (2 steps of 2^-24) and the rotation's rounding (one)
+    bound = 2 * math.pi * 2.0 ** -27 + 3 * 2.0 ** -24
+    for j, x in enumerate(f.tolist()):
+        num, den = x.as_integer_ratio()
+        for r, p in enumerate(pos):
+            turn = (p * num * inv_tau // den) % (1 << 192) / (1 << 192)
+            assert abs(float(qo[r, 0, j]) - math.cos(2 * math.pi * turn)) <= bound, (x, p)
+            assert abs(float(qo[r, 0, R // 2 + j]) - math.sin(2 * math.pi * turn)) <= bound, (x, p)
 
 
 def test_parts_of_one_projection_and_in_place():
