@@ -491,9 +491,10 @@ kvq_status kvq_norm_rope(const kvq_config* cfg, const void* q, int64_t q_stride,
  * Rows of out and lse that belong to no sequence are not written; rows of q, k and
  * v that a token does not attend to (later tokens, other sequences, rows of none)
  * never reach it, whatever they hold.  Weights are rounded to the inputs' type
- * (off by at most 2^-8 of each for bf16, 2^-11 for f16; twice that for keys whose
- * weights a later one within 128 keys exceeds by far), the sums are fp32.  A token
- * whose scores are all -inf gets 0 and lse -inf.  |v| below 2^90 (the sums before
+ * (off by at most 2^-8 of each for bf16, by 2^-11 of each and 2^-31 of the token's
+ * largest for f16, which loses a key that scores 21.5 below the highest; twice that
+ * for keys whose weights a later one within 128 keys exceeds by far), the sums are
+ * fp32, and lse has every key.  A token whose scores are all -inf gets 0 and lse -inf.  |v| below 2^90 (the sums before
  * the division reach 2^10 n |v|).  A call that sets KVQ_STATUS_TIMEOUT
  * leaves NaN in the rows of every CTA that gave up.  One launch. */
 kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int64_t q_stride, const void* k, int64_t k_stride,

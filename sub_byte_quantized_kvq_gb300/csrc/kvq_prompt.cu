@@ -28,7 +28,9 @@
 // is rounded to the inputs' type, as the MMA takes it: off by at most 2^-8 (bf16) or
 // 2^-11 (fp16) of each weight, as an output of that type is itself, and averaged
 // over the keys; l adds the weights before they are rounded.  fp16 weights are
-// biased by 2^6, so that small ones keep their bits (a half's sum stays below 2^15).
+// biased by 2^6, so that small ones keep their bits (a half's sum stays below 2^15):
+// those below 2^-20 of a row's largest are subnormal halves, off by up to 2^-31 of it,
+// and those below 2^-31 become 0 in O.
 //
 // What bounds it: MMA time and the power limit for long prompts, the ends of pairs
 // for shorter ones.  128 keys of a pair are 2048 cycles of MMAs (D = 128), measured

@@ -219,6 +219,32 @@ def test_scores_that_jump_in_both_halves_of_a_tile(dtype, D, G, causal):
     run_and_check([n, 100], 1, G, D, dtype=dtype, causal=causal, scale=1.0, change=change, seed=6)
 
 
+@pytest.mark.parametrize("below", [8.0, 14.0, 17.0, 20.0, 24.0])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_one_key_far_above_the_rest(dtype, below):
+    """A first key that takes nearly all the weight and whose V is 0: what is left of the output are the small weights, which
+    fp16 holds to 2^-31 of the largest (a relative bound alone does not hold there), bf16 to 2^-8 of each."""
+    n, D = 2500, 64
+    def change(q, k, v, first):
+        q.mul_(0.02)
+        q[..., 0] = 1.0
+        k[..., 0] = 0.0
+        k[first[0], :, 0] = below
+        v[first[0]] = 0.0
+        v.copy_(v.abs())
+    out, lse, q, k, v, first, scale = run([n], 1, 2, D, dtype=dtype, scale=1.0, change=change, out_dtype=F32, seed=12)
+    s = slice(first[0], first[0] + n)
+    check(out[s], lse[s], q[s], k[s], v[s], scale, True)
+    y, _, size, reach = ref.prompt(q[s], k[s], v[s], scale, True)
+    e = 2.0 ** -11 if dtype is HF else 2.0 ** -8
+    loss = (((out[s].double() - y).abs() / size.clamp_min(1e-300))[n // 2:]).max()
+    # 2^-31 of the largest weight, over what the small ones hold: e^-below of it each, the noise of the other channels included
+    few = 2.0 ** -31 / math.exp(-below - 1.5) if dtype is HF else 0.0
+    # scores: 2 (2^-23 (D + 2) sum |q k| + 2^-21), sums 2^-23 n, as in prompt_bounds
+    rest = 2 * (2.0 ** -23 * (D + 2) * float(reach.max()) + 2.0 ** -21) + 2.0 ** -23 * n
+    assert loss <= e + few + rest, float(loss)
+
+
 def test_scores_of_minus_infinity():
     """Keys that score -inf have no weight; a token that sees no other gets 0 and lse -inf."""
     n, m, G, D = 700, 333, 2, 128
