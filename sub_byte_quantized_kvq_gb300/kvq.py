@@ -598,8 +598,10 @@ def kvq_norm_rope(cache: QuantizedKVCache, q: torch.Tensor | None, k: torch.Tens
         assert k_weight.dtype is torch.float32 and k_weight.is_contiguous() and k_weight.shape == (D,)
     if eps is None:
         eps = -1.0
-    elif not eps >= 0:
-        raise ValueError("eps has to be at least 0 (None: no norm)")
+    else:
+        eps = float(eps)
+        if not eps >= 0:
+            raise ValueError("eps has to be at least 0 (None: no norm)")
     _check_on(index, q, k, q_out, k_out, None if rot == 0 else positions, inv_freq, q_weight, k_weight)
     if rows:
         _call("kvq_norm_rope", index, stream, pcfg, qp or None, qs, Hq, kp or None, ks, _DTYPE[dtype], rows, _addr(q_weight),
@@ -649,7 +651,7 @@ def kvq_prompt_attention(cache: QuantizedKVCache, q: torch.Tensor, k: torch.Tens
     _check_on(index, q, k, v, t_per_seq, first_row, out, lse)
     if rows:
         _call("kvq_prompt_attention", index, stream, pcfg, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, code, Hq, rows,
-              _addr(first_row), _addr(t_per_seq), t_new, softmax_scale, 1 if causal else 0, out.data_ptr(), outs, _DTYPE[od],
+              _addr(first_row), _addr(t_per_seq), t_new, float(softmax_scale), 1 if causal else 0, out.data_ptr(), outs, _DTYPE[od],
               _addr(lse), cache.status.data_ptr())
     return out
 
