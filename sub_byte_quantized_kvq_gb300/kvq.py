@@ -543,7 +543,7 @@ def kvq_norm_rope(cache: QuantizedKVCache, q: torch.Tensor | None, k: torch.Tens
                   k_out: torch.Tensor | None = None, out_dtype=None, stream=None):
     """Per-head RMS norm (eps None: none) of q [..., Hq, D] and k [..., Hkv, D] (bf16, f16 or f32; either may be
     None) and their rotary positions in one pass; returns (q_out, k_out).  positions: int32, one a row ([rows] or
-    q's leading shape), or [axes, rows] with pair_axis, the axis of each of the rot_dim / 2 pairs (a list).
+    q's leading shape), or [axes, rows] with pair_axis, the axis of each of the rot_dim / 2 pairs (a sequence).
     inv_freq: fp32 [rot_dim / 2] (None: norms alone).  q_weight, k_weight: fp32 [D] gains (None: ones).  The outputs
     may be the inputs."""
     cfg, (pcfg, _, index) = cache.cfg, _refs(cache)
@@ -591,7 +591,7 @@ def kvq_norm_rope(cache: QuantizedKVCache, q: torch.Tensor | None, k: torch.Tens
     if pair_axis is not None:
         if len(pair_axis) != rot // 2 or (rot and not 0 <= min(pair_axis) <= max(pair_axis) < axes):
             raise ValueError(f"pair_axis: an axis below {axes} for each of the {rot // 2} pairs")
-        pairs = bytes(pair_axis)
+        pairs = bytes(list(pair_axis))   # (not an array's own bytes)
     if q_weight is not None:
         assert q_weight.dtype is torch.float32 and q_weight.is_contiguous() and q_weight.shape == (D,)
     if k_weight is not None:

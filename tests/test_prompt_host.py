@@ -52,3 +52,18 @@ def test_an_eps_that_is_not_one(kvq, calls, bad):
     with pytest.raises(ValueError):
         kvq.kvq_norm_rope(cache, rows(6, 4), rows(6, 2), None, None, eps=bad)
     assert not calls
+
+
+@pytest.mark.parametrize("form", [list, tuple, np.array, lambda x: np.array(x, dtype=np.uint8), torch.tensor,
+                                  lambda x: torch.tensor(x, dtype=torch.int32)],
+                         ids=["list", "tuple", "int64 array", "uint8 array", "tensor", "int32 tensor"])
+def test_axes_of_pairs_in_any_sequence(kvq, calls, form):
+    """pair_axis is a sequence of numbers: an array's own bytes, eight for a number, are not its axes."""
+    cache, axes = kvq.QuantizedKVCache(1, 2, 2, 64, 1, 1, device="cpu"), [(i * 3) // 32 for i in range(32)]
+    kvq.kvq_norm_rope(cache, rows(6, 4), rows(6, 2), torch.zeros((3, 6), dtype=torch.int32), torch.ones(32), pair_axis=form(axes))
+    (_, args), = calls
+    assert [a for a in args if isinstance(a, bytes)] == [bytes(axes)]
+    for bad in (axes[:-1], axes[:-1] + [3], [-1] + axes[1:]):
+        with pytest.raises(ValueError):
+            kvq.kvq_norm_rope(cache, rows(6, 4), rows(6, 2), torch.zeros((3, 6), dtype=torch.int32), torch.ones(32), pair_axis=bad)
+    assert len(calls) == 1
