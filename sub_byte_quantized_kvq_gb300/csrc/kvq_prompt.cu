@@ -35,19 +35,21 @@
 // What bounds it: MMA time and the power limit for long prompts, the ends of pairs
 // for shorter ones.  128 keys of a pair are 2048 cycles of MMAs (D = 128), measured
 // as 2100 to 2300 (S reads both operands from shared memory), and take 2600: the
-// softmax of a tile (16384 exponentials at 16 a cycle and SM are 1024 cycles, with
-// the fused multiply-adds, sums and conversions about 700 a half for all four warps
-// of a scheduler) runs beside the other tile's MMAs, and each hand-over between the
-// roles costs about 200.  A pair costs 5000 to 8000 cycles at its ends (first
-// softmax, output of 64 KB, cleaning of the last V tiles).
-//   32768 tokens, 64 heads of 128, causal: 10.2 to 10.4 ms, 1.69 to 1.73 PFLOP/s (a
+// softmax of a tile runs beside the other tile's MMAs (16384 exponentials at 32 a
+// cycle and SM, measured, are 512 cycles; with the fused multiply-adds, sums and
+// conversions about 700 for half the keys of both tiles, one warp of each on a
+// scheduler), and each hand-over between the roles costs about 200.  A pair costs
+// 5000 to 8000 cycles at its ends (first softmax, output of 64 KB, cleaning of the
+// last V tiles).  With D = 64, 128 keys of a pair are 1024 cycles of MMAs, and the
+// softmax's 1400 are the limit.
+//   32768 tokens, 64 heads of 128, causal: 10.3 to 10.4 ms, 1.69 to 1.71 PFLOP/s (a
 //   library product of 8192^3 holds 1.74 under the same power limit)
-//   8 x 4096, 32 heads: 700 us, 1.57 PFLOP/s (760 without a pause);  17 tokens: 5.7 us
+//   8 x 4096, 32 heads: 705 us, 1.56 PFLOP/s (772 without a pause);  17 tokens: 5.9 us
 // What carried it: the MMAs issued by one elected lane of a converged warp (130 ->
 // 64 cycles an MMA of N = 128; 12.2 -> 11.1 ms), one place for both tiles' S and no
 // maximum in the common path (10.7 ms), S a step ahead of PV (17 tokens: 6.9 -> 5.7
 // us), all weights computed before the wait for the last PV (10.4 ms), pairs in
-// parts that L2 holds (8 x 4096: 740 -> 700 us, without a pause 830 -> 760).  The
+// parts that L2 holds (8 x 4096: 746 -> 704 us, without a pause 854 -> 772).  The
 // compiled softmax changes by up to 8% with code elsewhere in the kernel: time
 // every change.
 #include <algorithm>
@@ -91,7 +93,7 @@ struct Launch {
 
 struct Wait {
   volatile int* stop;
-  // A bounded wait: gives up after 2e8 cycles (100 ms), or when another role has.
+  // A bounded wait: gives up after 2e8 cycles (about 100 ms), or when another role has.
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();

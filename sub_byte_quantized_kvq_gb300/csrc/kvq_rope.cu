@@ -17,9 +17,11 @@
 // lane; D / 16 lanes hold a head (chunks of 8 channels l and l + R / 16, so a
 // pair's two channels are in one lane in either order of pairs), so a warp does
 // 32 / (D / 16) heads a step and shares the sines and cosines of its row, each
-// computed by one lane.  131072 rows of 40 heads of 128, bf16 (2.7 GB): 420 us, 6.4
-// TB/s; 8 x 4096 rows: 112 us, 6.0 TB/s; one row: 4.1 us, a launch and the latency
-// of positions, sines and one load.
+// computed by one lane.  131072 rows of 40 heads of 128, bf16 (2.7 GB): 419 us, 6.4
+// TB/s; 8 x 4096 rows: 112 us, 6.0 TB/s; one row: 3.8 to 4.2 us, a launch and the
+// latency of positions, sines and one load.  Items are groups of one role: heads
+// that do not fill the last group of q or of k leave lanes without work (D = 64, 4
+// query heads and 1 kv head: 5 of 16 places are used).
 #include <algorithm>
 #include <atomic>
 
@@ -104,14 +106,15 @@ __device__ __forceinline__ void turn_sincos(int pos, uint64_t per, float& s, flo
   if ((quad + 1) & 2) c = -c;
 }
 
-// CTAs an SM: by the registers that keep the common types from spilling.
+// CTAs an SM: 80 registers a thread for fp32 rows, 64 for the others, where at most 48 bytes a thread are spilled (none of
+// fp32 rows but for fp32 results, 32).
 template <int IN>
 constexpr int rope_ctas() { return IN == KVQ_F32 ? 3 : 4; }
 
 // Item (row, g) is 32 / (D / 16) heads of one row: q's groups first, then k's.  A warp takes whole rows, as many as every
 // warp can have, then a run of the items of the rows that are left; the next item's loads are in flight while one is
-// computed.  (7777 rows of 10 items, 4864 warps: 33 us, or 38 with whole rows alone; 131072 rows: 410 us, or 429 where a
-// warp's rows lie behind one another.)
+// computed.  (7777 rows of 10 items, 4864 warps: 15% longer with whole rows alone; 131072 rows: 5% longer where a warp's rows
+// lie behind one another.)
 template <int D, int IN, int OUT>
 __global__ void __launch_bounds__(32 * kRopeWarps, rope_ctas<IN>()) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH, PER = 8 / HPW;   // lanes a head, heads a step, pairs whose phase a lane computes

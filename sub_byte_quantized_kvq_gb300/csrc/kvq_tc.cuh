@@ -1,5 +1,5 @@
 // kvq_tc.cuh -- inline-PTX helpers of the 5th-generation tensor cores (tcgen05,
-// tensor memory, tiled TMA) shared by the fused projection and tree attention.
+// tensor memory, tiled TMA) shared by the fused projection, tree and prompt attention.
 #pragma once
 #include <cuda.h>
 
